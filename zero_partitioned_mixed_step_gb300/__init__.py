@@ -12,6 +12,9 @@ Entry points (same names as the C ABI):
   zero_step_fused, zero_reduce_scatter_accumulate,
   zero_step_fused_accumulated, zero_step_fused_buckets,
   zero_step_buckets_pass1, zero_step_buckets_norm, zero_step_buckets_pass2.
+The operators around the step (include/zerostep_ops.h; module ``ops``):
+  zero_tensors_norm, zero_tensors_clip, zero_fp8_quantize, zero_fp8_matmul,
+  zero_rmsnorm_fp8, zero_rmsnorm_backward.
 ``ZeroStep`` owns the buffers of one simulated data-parallel group and runs
 the fused step on them.
 """
@@ -23,6 +26,8 @@ from typing import List, Optional, Sequence, Tuple
 import torch
 
 from ._abi import (BF16, F16, MAX_WORLD, AdamCfg, Layout, StepState, ZeroError, check, lib)
+from . import ops
+from .ops import *  # noqa: F401,F403
 
 HALF_REDUCE = 2  # added to F16 / BF16: reduce in the half type instead of fp32
 
@@ -33,7 +38,7 @@ __all__ = [
     "zero_grad_norm", "zero_grad_norm_noalloc", "zero_adam_step", "zero_step_finalize", "zero_step_fused",
     "zero_reduce_scatter_accumulate", "zero_step_fused_accumulated", "zero_step_fused_buckets",
     "zero_step_buckets_pass1", "zero_step_buckets_norm", "zero_step_buckets_pass2",
-    "host_empty",
+    "host_empty", *ops.__all__,
 ]
 
 _TORCH_DT = {F16: torch.float16, BF16: torch.bfloat16}

@@ -1,4 +1,5 @@
-"""Build libzerostep.so (the C-ABI library) in-tree with nvcc for sm_103a."""
+"""Build libzerostep.so (the step) and libzerostep_ops.so (the operators around
+it) in-tree with nvcc for sm_103a."""
 from __future__ import annotations
 
 import concurrent.futures
@@ -14,6 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libzerostep.so")
+OPS = os.path.join(CSRC, "ops")
+OPS_LIB = os.path.join(BUILD, "libzerostep_ops.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -33,6 +36,8 @@ def nvcc() -> str:
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-Xcompiler", "-ffp-contract=off",
               "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden", "-Xcompiler", "-Wall", "-I", INCLUDE, *ARCH]
+# The operators' arithmetic has no oracle to match bit for bit: contraction is allowed.
+OPS_NVCC_FLAGS = [f for f in NVCC_FLAGS if f != "-fmad=false"]
 
 
 def _sources():
@@ -44,36 +49,61 @@ def _inputs():
         os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "zerostep.h"), __file__]
 
 
-def stale() -> bool:
-    if not os.path.exists(LIB):
+def _ops_sources():
+    return sorted(glob.glob(os.path.join(OPS, "*.cu")))
+
+
+def _ops_inputs():
+    return _ops_sources() + glob.glob(os.path.join(OPS, "*.cuh")) + [
+        os.path.join(INCLUDE, "zerostep.h"), os.path.join(INCLUDE, "zerostep_ops.h"), __file__]
+
+
+def _older(lib: str, inputs) -> bool:
+    if not os.path.exists(lib):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(f) > t for f in _inputs())
+    t = os.path.getmtime(lib)
+    return any(os.path.getmtime(f) > t for f in inputs)
+
+
+def stale() -> bool:
+    return _older(LIB, _inputs()) or _older(OPS_LIB, _ops_inputs())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every translation unit in parallel and link the shared library.
-    Returns the library path."""
-    if not force and not stale():
+    """Compile every translation unit of both libraries in parallel and link
+    them.  Returns the step library's path."""
+    todo = [(lib, sources(), flags)
+            for lib, sources, inputs, flags in ((LIB, _sources, _inputs, NVCC_FLAGS),
+                                                (OPS_LIB, _ops_sources, _ops_inputs, OPS_NVCC_FLAGS))
+            if force or _older(lib, inputs())]
+    if not todo:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    objs = []
 
-    def compile_one(src):
-        obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-        cmd = [nvcc(), *NVCC_FLAGS, "-c", src, "-o", obj]
+    def compile_one(job):
+        lib, src, flags = job
+        obj = os.path.join(BUILD, ("ops_" if lib == OPS_LIB else "") + os.path.basename(src) + ".o")
+        cmd = [nvcc(), *flags, "-c", src, "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
-        return obj, r.stderr
+        return lib, obj, r.stderr
 
+    objs = {}
     with concurrent.futures.ThreadPoolExecutor(max_workers=8) as ex:
-        for obj, log in ex.map(compile_one, _sources()):
-            objs.append(obj)
+        for lib, obj, log in ex.map(compile_one, [(lib, src, flags) for lib, srcs, flags in todo
+                                                  for src in srcs]):
+            objs.setdefault(lib, []).append(obj)
             if verbose and log:
                 print(log)
+    for lib, _, _ in todo:
+        _link(objs[lib], lib)
+    return LIB
+
+
+def _link(objs, lib: str) -> None:
     fd, tmp = tempfile.mkstemp(suffix=".so", dir=BUILD)
     os.close(fd)
     cuda_lib = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "lib64")
@@ -82,8 +112,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    return LIB
+    os.replace(tmp, lib)
 
 
 if __name__ == "__main__":

@@ -1,0 +1,223 @@
+// A matrix in 8-bit floating point with a scale for each 1x128 block or
+// 128x128 tile, and its transpose:
+//
+//   s = max(amax / qmax, 2^-126),  q = round(x * (1 / s))
+//
+// Bound by memory: x is read once and both forms are written from the same
+// registers.  A CTA takes a 128x128 tile; each thread holds an 8x8 patch (8
+// neighbouring rows, 8 neighbouring columns), so that a row's 16 bytes load at
+// once, a row's amax is a reduction over 16 lanes, a column's over 8 registers
+// and the 16 row groups, and 8 rows of a column pack into the 8 bytes that the
+// transposed form has side by side.
+#include "ops.cuh"
+
+namespace zo {
+
+constexpr int kQThreads = 256;  // 16 row groups x 16 column groups of 8x8
+
+struct QuantParams {
+    const void *x;
+    int64_t rows, cols, ldx;
+    uint8_t *q, *qt;
+    int64_t ldq, ldqt;
+    float *s, *st;
+    int64_t lds, ldst;
+    int32_t wide_x, wide_q, wide_qt;
+    int32_t row_tiles;
+};
+
+// TILE: one scale per tile.  TRANS: the transposed form is wanted (q may be
+// too: p.q says so).
+template <class T, int F8, bool TILE, bool TRANS>
+__global__ void __launch_bounds__(kQThreads) quantize_kernel(const QuantParams p)
+{
+    __shared__ uint32_t amax_sh[16][kBlock];  // a row group's amax of each column
+    __shared__ float inv_sh[kBlock];
+    __shared__ uint2 t_sh[TRANS ? kBlock : 1][16];
+    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
+    const int64_t tr = blockIdx.x % p.row_tiles, tc = blockIdx.x / p.row_tiles;
+    const int64_t r0 = tr * kBlock + rg * 8, c0 = tc * kBlock + cg * 8;
+    const int nc = (int)min((int64_t)8, p.cols - c0);   // may be <= 0
+    const int nr = (int)min((int64_t)8, p.rows - r0);
+    const T *x = static_cast<const T *>(p.x) + r0 * p.ldx + c0;
+
+    float v[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        load8(x + i * p.ldx, i < nr ? nc : 0, p.wide_x, v[i]);
+
+    float inv_row[8];
+    if (TILE) {
+        uint32_t a = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                a = max(a, magnitude(v[i][j]));
+        a = max_over<32>(a);
+        if ((threadIdx.x & 31) == 0)
+            amax_sh[0][threadIdx.x >> 5] = a;
+        __syncthreads();
+        a = 0;
+#pragma unroll
+        for (int w = 0; w < kQThreads / 32; ++w)
+            a = max(a, amax_sh[0][w]);
+        const float s = block_scale<F8>(a);
+        const float inv = __fdiv_rn(1.0f, s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            inv_row[i] = inv;
+        if (threadIdx.x == 0) {
+            if (p.q)
+                p.s[tc * p.lds + tr] = s;
+            if (TRANS)
+                p.st[tr * p.ldst + tc] = s;
+        }
+    } else if (p.q) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t a = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                a = max(a, magnitude(v[i][j]));
+            a = max_over<16>(a);
+            const float s = block_scale<F8>(a);
+            inv_row[i] = __fdiv_rn(1.0f, s);
+            if (cg == i && i < nr)  // 8 lanes of the row group write 8 rows
+                p.s[tc * p.lds + r0 + i] = s;
+        }
+    }
+    if (p.q) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint2 o;
+            o.x = pack4<F8>(v[i][0] * inv_row[i], v[i][1] * inv_row[i], v[i][2] * inv_row[i],
+                            v[i][3] * inv_row[i]);
+            o.y = pack4<F8>(v[i][4] * inv_row[i], v[i][5] * inv_row[i], v[i][6] * inv_row[i],
+                            v[i][7] * inv_row[i]);
+            if (i < nr)
+                store8b(p.q + (r0 + i) * p.ldq + c0, nc, p.wide_q, o);
+        }
+    }
+    if (!TRANS)
+        return;
+
+    if (!TILE) {
+        // the columns' amax over the tile's 128 rows
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint32_t a = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                a = max(a, magnitude(v[i][j]));
+            amax_sh[rg][cg * 8 + j] = a;
+        }
+        __syncthreads();
+        if (threadIdx.x < kBlock) {
+            uint32_t a = 0;
+#pragma unroll
+            for (int g = 0; g < 16; ++g)
+                a = max(a, amax_sh[g][threadIdx.x]);
+            const float s = block_scale<F8>(a);
+            inv_sh[threadIdx.x] = __fdiv_rn(1.0f, s);
+            const int64_t c = tc * kBlock + threadIdx.x;
+            if (c < p.cols)
+                p.st[tr * p.ldst + c] = s;
+        }
+        __syncthreads();
+    }
+    // The transposed tile through shared memory: column c's 128 bytes lie as 16
+    // units of 8 rows, unit g at place g ^ (c / 8), so that the 16 column
+    // groups of a half-warp, whose columns are 1024 bytes apart, write to
+    // different banks.
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float inv = TILE ? inv_row[0] : inv_sh[cg * 8 + j];
+        uint2 o;
+        o.x = pack4<F8>(v[0][j] * inv, v[1][j] * inv, v[2][j] * inv, v[3][j] * inv);
+        o.y = pack4<F8>(v[4][j] * inv, v[5][j] * inv, v[6][j] * inv, v[7][j] * inv);
+        t_sh[cg * 8 + j][rg ^ cg] = o;
+    }
+    __syncthreads();
+    // 16 threads write a column's 128 rows
+    const int64_t row = tr * kBlock + cg * 8;
+    const int n = (int)min((int64_t)8, p.rows - row);
+    if (n > 0)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = i * 16 + rg;
+            const int64_t col = tc * kBlock + c;
+            if (col < p.cols)
+                store8b(p.qt + col * p.ldqt + row, n, p.wide_qt, t_sh[c][cg ^ (c >> 3)]);
+        }
+}
+
+template <class T, int F8>
+static int launch_quantize(const QuantParams &p, bool tile, cudaStream_t stream)
+{
+    const int64_t grid = p.row_tiles * ceil_div(p.cols, kBlock);
+    if (grid > kMaxDim)
+        return ZERO_EINVAL;
+    auto go = [&](auto kernel) {
+        kernel<<<(unsigned)grid, kQThreads, 0, stream>>>(p);
+        return launch_status();
+    };
+    if (p.qt)
+        return tile ? go(quantize_kernel<T, F8, true, true>) : go(quantize_kernel<T, F8, false, true>);
+    return tile ? go(quantize_kernel<T, F8, true, false>) : go(quantize_kernel<T, F8, false, false>);
+}
+
+}  // namespace zo
+
+using namespace zo;
+
+extern "C" int zero_fp8_quantize(const void *x, int type, int64_t rows, int64_t cols, int64_t ldx,
+                                 int fp8, int tile, void *q, int64_t ldq, float *s, int64_t lds,
+                                 void *qt, int64_t ldqt, float *st, int64_t ldst,
+                                 zero_stream_t stream)
+{
+    if (!is_float(type) || !is_fp8(fp8) || bad_dim(rows) || bad_dim(cols) || (tile != 0 && tile != 1))
+        return ZERO_EINVAL;
+    if (rows == 0 || cols == 0)
+        return ZERO_OK;
+    if ((!q && !qt) || !q != !s || !qt != !st)
+        return ZERO_EINVAL;
+    int rc = check_matrix(x, rows, cols, ldx, type_bytes(type));
+    if (!rc && q)
+        rc = check_matrix(q, rows, cols, ldq, 1);
+    if (!rc && q)
+        rc = check_matrix(s, ceil_div(cols, kBlock), tile ? ceil_div(rows, kBlock) : rows, lds, 4);
+    if (!rc && qt)
+        rc = check_matrix(qt, cols, rows, ldqt, 1);
+    if (!rc && qt)
+        rc = check_matrix(st, ceil_div(rows, kBlock), tile ? ceil_div(cols, kBlock) : cols, ldst, 4);
+    if (rc)
+        return rc;
+    QuantParams p{};
+    p.x = x;
+    p.rows = rows;
+    p.cols = cols;
+    p.ldx = ldx;
+    p.q = static_cast<uint8_t *>(q);
+    p.ldq = ldq;
+    p.s = s;
+    p.lds = lds;
+    p.qt = static_cast<uint8_t *>(qt);
+    p.ldqt = ldqt;
+    p.st = st;
+    p.ldst = ldst;
+    p.wide_x = rows_aligned(x, ldx, type_bytes(type), 16);
+    p.wide_q = q && rows_aligned(q, ldq, 1, 8);
+    p.wide_qt = qt && rows_aligned(qt, ldqt, 1, 8);
+    p.row_tiles = (int32_t)ceil_div(rows, kBlock);
+    auto by_fp8 = [&](auto x_type) {
+        using T = decltype(x_type);
+        return fp8 == ZERO_T_E4M3 ? launch_quantize<T, ZERO_T_E4M3>(p, tile != 0, stream)
+                                  : launch_quantize<T, ZERO_T_E5M2>(p, tile != 0, stream);
+    };
+    if (type == ZERO_T_F16)
+        return by_fp8(f16{});
+    if (type == ZERO_T_BF16)
+        return by_fp8(bf16{});
+    return by_fp8(0.0f);
+}

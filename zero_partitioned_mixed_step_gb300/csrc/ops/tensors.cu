@@ -1,0 +1,500 @@
+// The global L2 norm over many gradient tensors, and the clipped gradients.
+//
+//   sumsq = sum_t sum_i (x_ti * inv_scale)^2
+//   out   = x * (inv_scale * c),  c = min(1, max_norm / (sqrt(sumsq) + 1e-6))
+//
+// Both are bound by memory: the norm reads every element once, the clip reads
+// and writes it once more (no update can start before the norm is known, and
+// a model's gradients are far more than L2 holds).  The tensors' pointers and
+// sizes travel as kernel arguments (up to kCapacity of them per launch), so a
+// call with new gradients needs no copy to the device and no table there.  A
+// tensor is cut into chunks of a size that follows from the list's total
+// alone, a CTA takes one, and the hardware hands out the chunks: the sum's
+// order depends on the sizes, not on the GPU.
+#include "ops.cuh"
+
+#include <atomic>
+#include <cstring>
+
+namespace zo {
+
+constexpr int kThreads = 256;
+constexpr int kUnit = 8;                  // elements of one wide access
+constexpr int64_t kMinChunk = 4096;       // elements
+constexpr int64_t kTargetChunks = 16384;  // of a whole list
+constexpr int kCapacity = 1024;           // tensors per launch
+constexpr int kHeader = 256;              // bytes of the workspace ahead of the chunk sums
+
+// The workspace's start: zero between calls.
+struct Header {
+    uint32_t done;  // finished CTAs of the running launch
+    uint32_t bad;   // 1: something is not finite
+};
+
+int device_sms()
+{
+    constexpr int kDevices = 64;
+    static std::atomic<int> count[kDevices];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return 1;
+    if (dev >= 0 && dev < kDevices && (sms = count[dev].load(std::memory_order_acquire)) > 0)
+        return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+        return 1;
+    if (dev >= 0 && dev < kDevices)
+        count[dev].store(sms, std::memory_order_release);
+    return sms;
+}
+
+static int64_t chunk_elems(int64_t total)
+{
+    const int64_t c = ceil_div(ceil_div(total, kTargetChunks), kMinChunk) * kMinChunk;
+    return c < kMinChunk ? kMinChunk : c;
+}
+
+// One launch's tensors.  first[t] is tensor t's first chunk, first[n] the
+// number of chunks.  Empty tensors are left out.
+template <int CAP, bool OUT>
+struct List {
+    const void *x[CAP];
+    void *out[OUT ? CAP : 1];
+    int64_t numel[CAP];
+    uint32_t first[CAP + 1];
+    int32_t index[CAP];   // in the caller's list
+    uint8_t type[CAP];
+    uint8_t out_type[OUT ? CAP : 1];
+    int64_t chunk;
+    int32_t n;
+};
+
+template <int CAP, bool OUT>
+__device__ __forceinline__ int find_tensor(const List<CAP, OUT> &l, uint32_t c)
+{
+    int lo = 0, hi = l.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (l.first[mid] <= c)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// ------------------------------------------------------------------ norm
+
+// The sum of two pairs (hi, lo) of fp32 values, hi carrying the rounded sum.
+__device__ __forceinline__ float2 pair_add(float2 a, float2 b)
+{
+    const float s = __fadd_rn(a.x, b.x);
+    const float bb = __fsub_rn(s, a.x);
+    const float err = __fadd_rn(__fsub_rn(a.x, __fsub_rn(s, bb)), __fsub_rn(b.x, bb));
+    return make_float2(s, __fadd_rn(__fadd_rn(a.y, b.y), err));
+}
+
+// The squares of n elements from p: eight running fp32 sums per thread.
+template <class T>
+__device__ __forceinline__ float2 sum_chunk(const T *p, int64_t n, float inv)
+{
+    float acc[kUnit];
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i)
+        acc[i] = 0.0f;
+    const bool wide = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+#pragma unroll 4
+    for (int64_t u = threadIdx.x; u * kUnit < n; u += kThreads) {
+        const int64_t left = n - u * kUnit;
+        float x[kUnit];
+        load8(p + u * kUnit, left < kUnit ? (int)left : kUnit, wide, x);
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) {
+            const float g = __fmul_rn(x[i], inv);
+            acc[i] = fmaf(g, g, acc[i]);
+        }
+    }
+    float2 s = make_float2(acc[0], 0.0f);
+#pragma unroll
+    for (int i = 1; i < kUnit; ++i)
+        s = pair_add(s, make_float2(acc[i], 0.0f));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        s = pair_add(s, make_float2(__shfl_xor_sync(0xFFFFFFFFu, s.x, o),
+                                    __shfl_xor_sync(0xFFFFFFFFu, s.y, o)));
+    return s;
+}
+
+// The same in binary64, for chunks whose fp32 sum is out of range; *bad is set
+// where an element is not finite.  Units of zeros (a chunk of zeros comes here
+// too) cost their load alone.
+template <class T>
+__device__ double sum_chunk_wide(const T *p, int64_t n, float inv, bool *bad)
+{
+    double s = 0.0;
+    const bool wide = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+#pragma unroll 2
+    for (int64_t u = threadIdx.x; u * kUnit < n; u += kThreads) {
+        const int64_t left = n - u * kUnit;
+        float x[kUnit];
+        load8(p + u * kUnit, left < kUnit ? (int)left : kUnit, wide, x);
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i)
+            any |= x[i] != 0.0f;  // NaN too
+        if (any)
+            for (int i = 0; i < kUnit; ++i) {
+                const float g = __fmul_rn(x[i], inv);
+                *bad |= !isfinite(g);
+                s += (double)g * g;
+            }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    return s;
+}
+
+template <class F>
+__device__ __forceinline__ auto by_type(int type, const void *p, int64_t at, F &&f)
+{
+    if (type == ZERO_T_F16)
+        return f(static_cast<const f16 *>(p) + at);
+    if (type == ZERO_T_BF16)
+        return f(static_cast<const bf16 *>(p) + at);
+    return f(static_cast<const float *>(p) + at);
+}
+
+// Doubles p[0 .. n) summed by one CTA in a fixed order; valid in thread 0.
+__device__ double cta_sum(const double *p, int64_t n, double *shared)
+{
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += kThreads)
+        s += __ldcg(p + i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        shared[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = 0.0;
+    if (threadIdx.x == 0)
+        for (int w = 0; w < kThreads / 32; ++w)
+            s += shared[w];
+    return s;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads)
+    norm_kernel(const __grid_constant__ List<CAP, false> l, float inv, double *tensor_sumsq,
+                zero_tensors_stat *stat, Header *head, double *sums, int first_launch,
+                int last_launch)
+{
+    __shared__ float2 warp_pair[kThreads / 32];
+    __shared__ double warp_sum[kThreads / 32];
+    __shared__ double redo;
+    __shared__ int last;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t c = blockIdx.x;
+    if (l.n > 0) {
+        const int t = find_tensor(l, c);
+        const int64_t at = (int64_t)(c - l.first[t]) * l.chunk;
+        const int64_t left = l.numel[t] - at;
+        const int64_t n = left < l.chunk ? left : l.chunk;
+        const float2 s = by_type(l.type[t], l.x[t], at,
+                                 [&](auto *p) { return sum_chunk(p, n, inv); });
+        if (lane == 0)
+            warp_pair[warp] = s;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            float2 a = warp_pair[0];
+            for (int w = 1; w < kThreads / 32; ++w)
+                a = pair_add(a, warp_pair[w]);
+            redo = (double)a.x + (double)a.y;
+        }
+        __syncthreads();
+        double sum = redo;
+        // below 2^-90 some squares of the chunk may have lost bits under
+        // fp32's smallest normal number
+        if (!(sum >= 0x1p-90 && sum <= 0x1p126)) {
+            bool bad = false;
+            const double d = by_type(l.type[t], l.x[t], at,
+                                     [&](auto *p) { return sum_chunk_wide(p, n, inv, &bad); });
+            if (lane == 0)
+                warp_sum[warp] = d;
+            if (__syncthreads_or(bad) && threadIdx.x == 0)
+                atomicOr(&head->bad, 1u);
+            if (threadIdx.x == 0) {
+                sum = warp_sum[0];
+                for (int w = 1; w < kThreads / 32; ++w)
+                    sum += warp_sum[w];
+            }
+        }
+        if (threadIdx.x == 0)
+            sums[c] = sum;
+    }
+    if (threadIdx.x == 0) {
+        __threadfence();
+        last = atomicAdd(&head->done, 1u) == gridDim.x - 1;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!last)
+        return;
+    // every chunk of this launch is summed: the tensors' sums, and the total
+    if (tensor_sumsq)
+        for (int t = warp; t < l.n; t += kThreads / 32) {
+            double s = 0.0;
+            for (uint32_t i = l.first[t] + lane; i < l.first[t + 1]; i += 32)
+                s += __ldcg(sums + i);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+            if (lane == 0)
+                tensor_sumsq[l.index[t]] = s;
+        }
+    const double total = cta_sum(sums, l.n > 0 ? l.first[l.n] : 0, warp_sum);
+    if (threadIdx.x == 0) {
+        const double all = first_launch ? total : stat->sumsq + total;
+        stat->sumsq = all;
+        stat->norm = (float)sqrt(all);
+        head->done = 0;
+        if (last_launch) {
+            stat->found_inf = (int32_t)head->bad;
+            head->bad = 0;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ clip
+
+template <class T, class U>
+__device__ __forceinline__ void scale_chunk(const T *p, U *o, int64_t n, float f)
+{
+    const bool wide = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+    const bool wide_out = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
+#pragma unroll 4
+    for (int64_t u = threadIdx.x; u * kUnit < n; u += kThreads) {
+        const int64_t left = n - u * kUnit;
+        const int m = left < kUnit ? (int)left : kUnit;
+        float x[kUnit];
+        load8(p + u * kUnit, m, wide, x);
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i)
+            x[i] = __fmul_rn(x[i], f);
+        store8(o + u * kUnit, m, wide_out, x);
+    }
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads)
+    clip_kernel(const __grid_constant__ List<CAP, true> l, float inv, float max_norm,
+                const zero_tensors_stat *stat)
+{
+    float c = 1.0f;
+    if (max_norm > 0.0f && stat->found_inf == 0) {
+        // the norm from sumsq (which the caller may have added over ranks),
+        // in fp32 where it is in range: GB300's binary64 is slow
+        const double s = stat->sumsq;
+        const float norm = s >= 0x1p-120 && s <= 0x1p120 ? __fsqrt_rn((float)s) : (float)sqrt(s);
+        c = fminf(1.0f, __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f)));
+    }
+    const float f = __fmul_rn(inv, c);
+    const int t = find_tensor(l, blockIdx.x);
+    if (f == 1.0f && l.out[t] == l.x[t])
+        return;  // in place and unchanged
+    const int64_t at = (int64_t)(blockIdx.x - l.first[t]) * l.chunk;
+    const int64_t left = l.numel[t] - at;
+    const int64_t n = left < l.chunk ? left : l.chunk;
+    by_type(l.type[t], l.x[t], at, [&](auto *p) {
+        if (l.out_type[t] == ZERO_T_F16)
+            scale_chunk(p, static_cast<f16 *>(l.out[t]) + at, n, f);
+        else if (l.out_type[t] == ZERO_T_BF16)
+            scale_chunk(p, static_cast<bf16 *>(l.out[t]) + at, n, f);
+        else
+            scale_chunk(p, static_cast<float *>(l.out[t]) + at, n, f);
+    });
+}
+
+// ------------------------------------------------------------------ host
+
+// Checks a list's sizes; its total.
+static int list_total(int n, const int64_t *numel, int64_t *total)
+{
+    if (n < 0 || (n > 0 && !numel))
+        return ZERO_EINVAL;
+    int64_t sum = 0;
+    for (int t = 0; t < n; ++t) {
+        if (numel[t] < 0 || numel[t] > (INT64_C(1) << 45) || sum > (INT64_C(1) << 45))
+            return ZERO_EINVAL;
+        sum += numel[t];
+    }
+    *total = sum;
+    return ZERO_OK;
+}
+
+// Fills a launch's list from the caller's tensor t on; returns the next one.
+template <int CAP, bool OUT>
+static int fill(List<CAP, OUT> &l, int t, int n, const void *const *x, const int64_t *numel,
+                const int32_t *type, void *const *out, const int32_t *out_type, int64_t chunk)
+{
+    l.chunk = chunk;
+    l.n = 0;
+    uint32_t c = 0;
+    for (; t < n && l.n < CAP; ++t) {
+        if (numel[t] == 0)
+            continue;
+        const int64_t more = ceil_div(numel[t], chunk);
+        l.x[l.n] = x[t];
+        l.numel[l.n] = numel[t];
+        l.first[l.n] = c;
+        l.index[l.n] = t;
+        l.type[l.n] = (uint8_t)type[t];
+        if (OUT) {
+            l.out[l.n] = out ? out[t] : const_cast<void *>(x[t]);
+            l.out_type[l.n] = (uint8_t)(out ? out_type[t] : type[t]);
+        }
+        c += (uint32_t)more;
+        ++l.n;
+    }
+    while (t < n && numel[t] == 0)
+        ++t;
+    l.first[l.n] = c;
+    return t;
+}
+
+// Runs `launch` on lists of the smallest capacity that holds the tensors.
+template <bool OUT, class F>
+static int for_each_list(int n, const void *const *x, const int64_t *numel, const int32_t *type,
+                         void *const *out, const int32_t *out_type, int64_t total, F &&launch)
+{
+    const int64_t chunk = chunk_elems(total);
+    int full = 0;
+    for (int t = 0; t < n; ++t)
+        full += numel[t] > 0;
+    auto go = [&](auto &l) {
+        int t = 0;
+        bool first = true;
+        do {
+            t = fill(l, t, n, x, numel, type, out, out_type, chunk);
+            const int rc = launch(l, first, t >= n);
+            if (rc)
+                return rc;
+            first = false;
+        } while (t < n);
+        return (int)ZERO_OK;
+    };
+    // the arguments are copied at every launch, so a short list takes a short one
+    if (full <= 64) {
+        List<64, OUT> l;
+        return go(l);
+    }
+    if (full <= 320) {
+        List<320, OUT> l;
+        return go(l);
+    }
+    List<kCapacity - (OUT ? 200 : 0), OUT> l;
+    return go(l);
+}
+
+static int check_list(int n, const void *const *x, const int64_t *numel, const int32_t *type,
+                      int64_t *total)
+{
+    const int rc = list_total(n, numel, total);
+    if (rc)
+        return rc;
+    if (n > 0 && (!x || !type))
+        return ZERO_EINVAL;
+    for (int t = 0; t < n; ++t) {
+        if (!is_float(type[t]) || (numel[t] > 0 && !x[t]))
+            return ZERO_EINVAL;
+        if (!aligned(x[t], (uintptr_t)type_bytes(type[t])))
+            return ZERO_EALIGN;
+    }
+    return ZERO_OK;
+}
+
+}  // namespace zo
+
+using namespace zo;
+
+extern "C" {
+
+size_t zero_tensors_workspace_bytes(int n, const int64_t *numel)
+{
+    int64_t total = 0;
+    if (list_total(n, numel, &total))
+        return 0;
+    const int64_t chunk = chunk_elems(total);
+    int64_t chunks = 0;
+    for (int t = 0; t < n; ++t)
+        chunks += ceil_div(numel[t], chunk);
+    return (size_t)(kHeader + chunks * (int64_t)sizeof(double));
+}
+
+int zero_tensors_norm(int n, const void *const *x, const int64_t *numel, const int32_t *type,
+                      float inv_scale, double *tensor_sumsq, zero_tensors_stat *stat, void *ws,
+                      size_t ws_bytes, zero_stream_t stream)
+{
+    int64_t total = 0;
+    const int rc = check_list(n, x, numel, type, &total);
+    if (rc)
+        return rc;
+    if (!stat || !ws || !(inv_scale > 0.0f) || !std::isfinite(inv_scale))
+        return ZERO_EINVAL;
+    if (!aligned(stat, 8) || !aligned(ws, 16) || !aligned(tensor_sumsq, 8))
+        return ZERO_EALIGN;
+    if (ws_bytes < zero_tensors_workspace_bytes(n, numel))
+        return ZERO_ESPACE;
+    if (tensor_sumsq)
+        for (int t = 0; t < n; ++t)
+            if (numel[t] == 0) {  // the kernels see no empty tensor
+                const cudaError_t e = cudaMemsetAsync(tensor_sumsq, 0, sizeof(double) * (size_t)n,
+                                                      stream);
+                if (e != cudaSuccess)
+                    return cuda_error(e);
+                break;
+            }
+    Header *head = static_cast<Header *>(ws);
+    double *sums = reinterpret_cast<double *>(static_cast<char *>(ws) + kHeader);
+    return for_each_list<false>(
+        n, x, numel, type, nullptr, nullptr, total, [&](auto &l, bool first, bool last) {
+            const uint32_t chunks = l.n ? l.first[l.n] : 1;  // an empty list still ends the norm
+            norm_kernel<<<chunks, kThreads, 0, stream>>>(l, inv_scale, tensor_sumsq, stat, head,
+                                                         sums, first ? 1 : 0, last ? 1 : 0);
+            return launch_status();
+        });
+}
+
+int zero_tensors_clip(int n, const void *const *x, const int64_t *numel, const int32_t *type,
+                      void *const *out, const int32_t *out_type, float inv_scale, double max_norm,
+                      const zero_tensors_stat *stat, zero_stream_t stream)
+{
+    int64_t total = 0;
+    int rc = check_list(n, x, numel, type, &total);
+    if (rc)
+        return rc;
+    if (!stat || !(inv_scale > 0.0f) || !std::isfinite(inv_scale) || !(max_norm >= 0.0) ||
+        (out && n > 0 && !out_type))
+        return ZERO_EINVAL;
+    if (!aligned(stat, 8))
+        return ZERO_EALIGN;
+    if (out)
+        for (int t = 0; t < n; ++t) {
+            if (!is_float(out_type[t]) || (numel[t] > 0 && !out[t]) ||
+                (numel[t] > 0 && out[t] == x[t] && out_type[t] != type[t]))
+                return ZERO_EINVAL;
+            if (!aligned(out[t], (uintptr_t)type_bytes(out_type[t])))
+                return ZERO_EALIGN;
+        }
+    if (total == 0)
+        return ZERO_OK;
+    return for_each_list<true>(n, x, numel, type, out, out_type, total,
+                               [&](auto &l, bool, bool) {
+                                   clip_kernel<<<l.first[l.n], kThreads, 0, stream>>>(
+                                       l, inv_scale, (float)max_norm, stat);
+                                   return launch_status();
+                               });
+}
+
+}  // extern "C"

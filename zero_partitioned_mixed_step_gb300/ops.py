@@ -1,0 +1,286 @@
+"""Binding of the operators around the step (include/zerostep_ops.h): the
+functions marshal arguments, libzerostep_ops.so's sm_103a kernels compute.
+
+Matrices are 2-D CUDA tensors whose rows are contiguous (any row stride); the
+caller makes the outputs.  8-bit matrices are torch.float8_e4m3fn or
+torch.float8_e5m2 tensors with fp32 scales of shape [ceil(cols / 128), rows]
+(1x128 blocks) or [ceil(cols / 128), ceil(rows / 128)] (128x128 tiles);
+``fp8_empty`` makes a pair whose rows start on 16-byte boundaries, as
+``zero_fp8_matmul`` wants them.  Work is enqueued on torch's current stream
+unless one is given; a tensor used on another stream than the one it was
+allocated on is the caller's to keep alive, as with any torch operator.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Sequence, Tuple, Union
+
+import torch
+
+from ._abi import ZeroError
+from ._ops_abi import (BLOCK, T_BF16, T_E4M3, T_E5M2, T_F16, T_F32, TensorsStat, check, lib)
+
+__all__ = [
+    "BLOCK", "TensorList", "TensorsStat", "tensor_list", "new_tensors_stat", "read_tensors_stat",
+    "zero_tensors_workspace_bytes", "zero_tensors_norm", "zero_tensors_clip", "fp8_empty",
+    "zero_fp8_quantize", "zero_fp8_matmul_workspace_bytes", "zero_fp8_matmul",
+    "zero_rmsnorm_fp8", "zero_rmsnorm_workspace_bytes", "zero_rmsnorm_backward",
+]
+
+_TYPE = {torch.float16: T_F16, torch.bfloat16: T_BF16, torch.float32: T_F32,
+         torch.float8_e4m3fn: T_E4M3, torch.float8_e5m2: T_E5M2}
+
+
+def _stream(stream, device: torch.device) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _type(t: torch.Tensor) -> int:
+    code = _TYPE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"no operator takes {t.dtype}")
+    return code
+
+
+def _on_device(t: torch.Tensor) -> int:
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError("CUDA tensor of the current device expected")
+    return t.data_ptr()
+
+
+def _flat(t: Optional[torch.Tensor]) -> Optional[int]:
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("contiguous tensor expected")
+    return _on_device(t)
+
+
+def _matrix(t: Optional[torch.Tensor], rows: int, cols: int, name: str,
+            dtypes=None) -> Tuple[Optional[int], int]:
+    """(pointer, row stride) of a [rows, cols] matrix with contiguous rows."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
+    if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name}: contiguous rows expected, strides {t.stride()}")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise TypeError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    # torch gives a single row any stride
+    return _on_device(t), max(t.stride(0), cols) if rows > 1 else _row_stride(t, cols)
+
+
+def _row_stride(t: torch.Tensor, cols: int) -> int:
+    """A stride for a matrix of one row: no second row is ever reached, so the
+    next multiple of 16 elements serves every alignment rule."""
+    return (cols + 15) // 16 * 16
+
+
+def _blocks(n: int) -> int:
+    return (n + BLOCK - 1) // BLOCK
+
+
+_F8 = (torch.float8_e4m3fn, torch.float8_e5m2)
+_HALF = (torch.float16, torch.bfloat16)
+_FLOAT = (torch.float16, torch.bfloat16, torch.float32)
+_F32 = (torch.float32,)
+
+
+# ----------------------------------------------------------------- many tensors
+
+class TensorList:
+    """The pointers, sizes and types of a list of contiguous CUDA tensors, in
+    the form the library reads; keeps the tensors alive.  A program whose
+    gradients stay where they are makes it once."""
+
+    def __init__(self, tensors: Sequence[torch.Tensor]):
+        self.tensors = list(tensors)
+        n = self.n = len(self.tensors)
+        self.ptr = (ctypes.c_void_p * max(n, 1))(*[_flat(t) for t in self.tensors])
+        self.numel = (ctypes.c_int64 * max(n, 1))(*[t.numel() for t in self.tensors])
+        self.type = (ctypes.c_int32 * max(n, 1))(*[_type(t) for t in self.tensors])
+
+
+Tensors = Union[TensorList, Sequence[torch.Tensor]]
+
+
+def tensor_list(tensors: Tensors) -> TensorList:
+    return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+
+
+def new_tensors_stat(device="cuda") -> torch.Tensor:
+    """A device-resident zero_tensors_stat (16 bytes: sumsq, norm, found_inf)."""
+    return torch.zeros(ctypes.sizeof(TensorsStat), dtype=torch.uint8, device=device)
+
+
+def read_tensors_stat(stat: torch.Tensor) -> TensorsStat:
+    """Copy a device stat to the host (synchronises with its stream)."""
+    return TensorsStat.from_buffer_copy(bytes(stat.cpu().numpy().tobytes()))
+
+
+def zero_tensors_workspace_bytes(tensors: Tensors) -> int:
+    """Workspace bytes of zero_tensors_norm (zero-fill it before first use)."""
+    l = tensor_list(tensors)
+    n = lib().zero_tensors_workspace_bytes(l.n, l.numel)
+    if n == 0:
+        raise ZeroError("zero_tensors_workspace_bytes", -1)
+    return n
+
+
+def zero_tensors_norm(tensors: Tensors, inv_scale: float, stat: torch.Tensor, ws: torch.Tensor,
+                      tensor_sumsq: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The global norm of the tensors times inv_scale into ``stat``;
+    ``tensor_sumsq``: one float64 per tensor, each tensor's sum of squares."""
+    l = tensor_list(tensors)
+    if stat.numel() * stat.element_size() < ctypes.sizeof(TensorsStat):
+        raise ValueError("stat: 16 bytes expected (new_tensors_stat)")
+    if tensor_sumsq is not None and (tensor_sumsq.dtype != torch.float64
+                                     or tensor_sumsq.numel() != l.n):
+        raise ValueError("tensor_sumsq: one float64 for each tensor expected")
+    check("zero_tensors_norm",
+          lib().zero_tensors_norm(l.n, l.ptr, l.numel, l.type, inv_scale, _flat(tensor_sumsq),
+                                  _flat(stat), _flat(ws), ws.numel() * ws.element_size(),
+                                  _stream(stream, stat.device)))
+
+
+def zero_tensors_clip(tensors: Tensors, out: Optional[Tensors], inv_scale: float, max_norm: float,
+                      stat: torch.Tensor, stream=None) -> None:
+    """out = tensors * inv_scale * min(1, max_norm / (norm + 1e-6)), in place
+    with ``out`` None; max_norm 0 does not clip."""
+    l = tensor_list(tensors)
+    o = tensor_list(out) if out is not None else None
+    if o is not None and (o.n != l.n or any(a != b for a, b in zip(o.numel, l.numel))):
+        raise ValueError("out: as many tensors of the same sizes expected")
+    if stat.numel() * stat.element_size() < ctypes.sizeof(TensorsStat):
+        raise ValueError("stat: 16 bytes expected (new_tensors_stat)")
+    check("zero_tensors_clip",
+          lib().zero_tensors_clip(l.n, l.ptr, l.numel, l.type, o.ptr if o is not None else None,
+                                  o.type if o is not None else None, inv_scale, max_norm,
+                                  _flat(stat), _stream(stream, stat.device)))
+
+
+# ----------------------------------------------------------------- 8-bit matrices
+
+def fp8_empty(rows: int, cols: int, dtype: torch.dtype = torch.float8_e4m3fn, tile: bool = False,
+              device="cuda") -> Tuple[torch.Tensor, torch.Tensor]:
+    """(values, scales) of an 8-bit matrix, uninitialised, rows on 16-byte boundaries."""
+    pitch = (cols + 15) // 16 * 16
+    q = torch.empty(rows, pitch, dtype=dtype, device=device)[:, :cols]
+    s = torch.empty(_blocks(cols), _blocks(rows) if tile else rows, dtype=torch.float32,
+                    device=device)
+    return q, s
+
+
+def zero_fp8_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None,
+                      s: Optional[torch.Tensor] = None, qt: Optional[torch.Tensor] = None,
+                      st: Optional[torch.Tensor] = None, tile: bool = False, stream=None) -> None:
+    """x in 8 bits with a scale for each 1x128 block (or 128x128 tile) into
+    (q, s), and its transpose, blocks along x's rows, into (qt, st)."""
+    if x.dim() != 2:
+        raise ValueError("x: matrix expected")
+    rows, cols = x.shape
+    px, ldx = _matrix(x, rows, cols, "x", _FLOAT)
+    if (q is None) != (s is None) or (qt is None) != (st is None) or (q is None and qt is None):
+        raise ValueError("(q, s), (qt, st) or both expected")
+    if q is not None and qt is not None and q.dtype != qt.dtype:
+        raise TypeError("q and qt: one 8-bit type expected")
+    pq, ldq = _matrix(q, rows, cols, "q", _F8)
+    ps, lds = _matrix(s, _blocks(cols), _blocks(rows) if tile else rows, "s", _F32)
+    pqt, ldqt = _matrix(qt, cols, rows, "qt", _F8)
+    pst, ldst = _matrix(st, _blocks(rows), _blocks(cols) if tile else cols, "st", _F32)
+    check("zero_fp8_quantize",
+          lib().zero_fp8_quantize(px, _type(x), rows, cols, ldx, _type(q if q is not None else qt),
+                                  int(tile), pq, ldq, ps, lds, pqt, ldqt, pst, ldst,
+                                  _stream(stream, x.device)))
+
+
+def zero_fp8_matmul_workspace_bytes(m: int, n: int, k: int) -> int:
+    """Workspace bytes of zero_fp8_matmul (zero-fill it before first use)."""
+    b = lib().zero_fp8_matmul_workspace_bytes(m, n, k)
+    if b == 0:
+        raise ZeroError("zero_fp8_matmul_workspace_bytes", -1)
+    return b
+
+
+def zero_fp8_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor,
+                    out: torch.Tensor, ws: torch.Tensor, add: bool = False, stream=None) -> None:
+    """out[m, n] (+)= a[m, k] b[n, k]^T with a's scales for 1x128 blocks and
+    b's, by their shape, for 128x128 tiles or 1x128 blocks."""
+    if a.dim() != 2 or b.dim() != 2:
+        raise ValueError("a, b: matrices expected")
+    (m, k), n = a.shape, b.shape[0]
+    pa, lda = _matrix(a, m, k, "a", _F8)
+    pb, ldb = _matrix(b, n, k, "b", _F8)
+    psa, ldsa = _matrix(sa, _blocks(k), m, "sa", _F32)
+    tile = sb.dim() == 2 and sb.shape[1] != n
+    psb, ldsb = _matrix(sb, _blocks(k), _blocks(n) if tile else n, "sb", _F32)
+    po, ldo = _matrix(out, m, n, "out", _FLOAT)
+    check("zero_fp8_matmul",
+          lib().zero_fp8_matmul(pa, _type(a), lda, psa, ldsa, pb, _type(b), ldb, psb, ldsb,
+                                int(tile), po, _type(out), ldo, m, n, k, int(add), _flat(ws),
+                                ws.numel() * ws.element_size(), _stream(stream, out.device)))
+
+
+# ----------------------------------------------------------------- root-mean-square norm
+
+def zero_rmsnorm_fp8(x: torch.Tensor, w: torch.Tensor, eps: float,
+                     rstd: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                     h: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                     q: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+    """h = x + residual, rstd = 1 / sqrt(mean(h^2) + eps), y = h * rstd * w in
+    x's type and, in 8 bits with a scale for each 1x128 block, into (q, s)."""
+    if x.dim() != 2:
+        raise ValueError("x: matrix expected")
+    rows, cols = x.shape
+    if w.numel() != cols or rstd is not None and (rstd.numel() != rows
+                                                  or rstd.dtype != torch.float32):
+        raise ValueError("w: one element for each column, rstd: one fp32 for each row expected")
+    px, ldx = _matrix(x, rows, cols, "x", _HALF)
+    pr, ldr = _matrix(residual, rows, cols, "residual", (x.dtype,))
+    ph, ldh = _matrix(h, rows, cols, "h", (x.dtype,))
+    py, ldy = _matrix(y, rows, cols, "y", (x.dtype,))
+    pq, ldq = _matrix(q, rows, cols, "q", _F8)
+    ps, lds = _matrix(s, _blocks(cols), rows, "s", _F32)
+    check("zero_rmsnorm_fp8",
+          lib().zero_rmsnorm_fp8(px, ldx, pr, ldr, _flat(w), _type(w), _type(x), rows, cols, eps,
+                                 ph, ldh, py, ldy, _type(q) if q is not None else T_E4M3, pq, ldq,
+                                 ps, lds, _flat(rstd), _stream(stream, x.device)))
+
+
+def zero_rmsnorm_workspace_bytes(rows: int, cols: int) -> int:
+    """Workspace bytes of zero_rmsnorm_backward."""
+    b = lib().zero_rmsnorm_workspace_bytes(rows, cols)
+    if b == 0:
+        raise ZeroError("zero_rmsnorm_workspace_bytes", -1)
+    return b
+
+
+def zero_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rstd: torch.Tensor,
+                          dx: torch.Tensor, dw: Optional[torch.Tensor], ws: Optional[torch.Tensor],
+                          dres: Optional[torch.Tensor] = None, add_dw: bool = False,
+                          stream=None) -> None:
+    """dx (the gradient of x and of the residual) and dw of zero_rmsnorm_fp8,
+    with the gradient ``dres`` that reaches h by the residual path added."""
+    if dy.dim() != 2:
+        raise ValueError("dy: matrix expected")
+    rows, cols = dy.shape
+    if w.numel() != cols or dw is not None and dw.numel() != cols:
+        raise ValueError("w, dw: one element for each column expected")
+    if rstd.numel() != rows or rstd.dtype != torch.float32:
+        raise ValueError("rstd: one fp32 for each row expected")
+    if dw is not None and ws is None:
+        raise ValueError("ws: a workspace expected (zero_rmsnorm_workspace_bytes)")
+    pdy, lddy = _matrix(dy, rows, cols, "dy", _HALF)
+    ph, ldh = _matrix(h, rows, cols, "h", (dy.dtype,))
+    pdr, lddr = _matrix(dres, rows, cols, "dres", (dy.dtype,))
+    pdx, lddx = _matrix(dx, rows, cols, "dx", (dy.dtype,))
+    check("zero_rmsnorm_backward",
+          lib().zero_rmsnorm_backward(pdy, lddy, ph, ldh, _flat(w), _type(w), _flat(rstd), pdr,
+                                      lddr, _type(dy), rows, cols, pdx, lddx, _flat(dw),
+                                      _type(dw) if dw is not None else T_F32, int(add_dw),
+                                      _flat(ws), ws.numel() * ws.element_size() if ws is not None
+                                      else 0, _stream(stream, dy.device)))
