@@ -1,62 +1,517 @@
 // The product of two 8-bit matrices with a scale for each block of 128.
 //
 //   out[i, j] (+)= sum_b sa[b, i] sb[b, j] (sum over k in block b of a[i, k] b[j, k])
+//
+// The scales change every 128 of k, so the tensor cores cannot keep one sum
+// over k: each block's products go to tensor memory on their own (four
+// tcgen05 products of 32 bytes of k), from where the epilogue warps take them
+// into registers, acc = fma(part, sa * sb, acc).  Tensor memory holds two
+// blocks' sums, so the products of one block run while the last one's are
+// being scaled.
+//
+// A CTA (or a pair of them on neighbouring SMs, which share B) has
+//   NH groups of four epilogue warps, each for 128 rows x 128 columns,
+//   a warp whose first thread issues the TMA copies into a ring of stages
+//   (128 rows of A and NH * 128 of B, 128 bytes of k each), and
+//   a warp whose first thread issues the products.
+// The CTAs are persistent and walk the tiles.  All waits are bounded: the
+// role that gives up marks the workspace's error word, the others follow, the
+// copies and products in flight are waited for (again bounded) and tensor
+// memory is freed.
+#include <cuda.h>
+
+#include <atomic>
+
 #include "ops.cuh"
+#include "tcgen05.cuh"
 
 namespace zo {
 
+constexpr int kHead = 4096;        // bytes of the workspace ahead of the partial sums
+constexpr int kCounters = 256;     // offset of the tiles' counters (zero between calls)
+constexpr int kPlanSms = 152;      // the rule for splitting k counts on a GB300's SMs
+constexpr int kStage = 16 * 1024;  // bytes of one staging buffer of the output
+
 struct MatmulParams {
-    const uint8_t *a, *b;
     const float *sa, *sb;
     void *out;
-    int64_t lda, ldb, ldsa, ldsb, ldo;
-    int64_t m, n, k;
-    int32_t a_type, b_type, b_tile, out_type, add;
+    int32_t *error;
+    uint32_t *counters;
+    float *parts;
+    int64_t ldsa, ldsb, ldo;
+    int32_t m, n, kb;           // rows, columns, blocks of k
+    int32_t tiles_m, tiles_n, splits;
+    int32_t out_type, add, tma_out;
+    uint32_t instr;
 };
 
-__device__ __forceinline__ float fp8_value(uint8_t x, int type)
+template <int CG, int NH>
+struct Shape {
+    static constexpr int kThreads = 128 * NH + 64;
+    static constexpr int kTileM = 128 * CG, kTileN = 128 * NH;
+    static constexpr int kRowsB = 128 / CG;  // of each 128 columns, in one CTA
+    static constexpr int kBytesA = 128 * 128, kBytesB = NH * kRowsB * 128;
+    static constexpr int kStageBytes = kBytesA + kBytesB;
+    static constexpr int kStages = (224 * 1024 - NH * 2 * kStage - 4096) / kStageBytes;
+    static constexpr int kColumns = 256 * NH;  // of tensor memory
+    static constexpr int kSmem = 1024 + kStages * kStageBytes + NH * 2 * kStage;
+};
+
+// Tile (and part of k) number u: groups of 8 row tiles, so that the tiles that
+// run together share what they read in L2.
+struct Unit {
+    int m, n, kb0, kb1, tile, split;
+};
+__device__ __forceinline__ Unit unit_of(const MatmulParams &p, int64_t u)
 {
-    const __half_raw r = __nv_cvt_fp8_to_halfraw(x, type == ZERO_T_E4M3 ? __NV_E4M3 : __NV_E5M2);
-    return __half2float(__half(r));
+    Unit r;
+    r.split = (int)(u % p.splits);
+    r.tile = (int)(u / p.splits);
+    constexpr int kGroup = 8;
+    const int per = kGroup * p.tiles_n, g = r.tile / per, in = r.tile % per;
+    const int rows = min(kGroup, p.tiles_m - g * kGroup);
+    r.m = g * kGroup + in % rows;
+    r.n = in / rows;
+    r.kb0 = (int)((int64_t)p.kb * r.split / p.splits);
+    r.kb1 = (int)((int64_t)p.kb * (r.split + 1) / p.splits);
+    return r;
 }
 
-__global__ void __launch_bounds__(256) matmul_kernel(const MatmulParams p)
+// Writes 16 bytes of a row of a staging buffer (128 rows of 128 bytes, swizzled as the TMA reads them).
+__device__ __forceinline__ void stage16(uint8_t *buf, int row, int piece, uint4 v)
 {
-    __shared__ float as[16][17], bs[16][17];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int64_t i0 = (int64_t)blockIdx.y * 16, j0 = (int64_t)blockIdx.x * 16;
-    const int64_t i = i0 + ty, j = j0 + tx;
-    float acc = 0.0f;
-    for (int64_t k0 = 0; k0 < p.k; k0 += kBlock) {
-        float part = 0.0f;
-        for (int64_t kk = k0; kk < k0 + kBlock && kk < p.k; kk += 16) {
-            const int64_t c = kk + tx;
-            __syncthreads();
-            as[ty][tx] = i0 + ty < p.m && c < p.k ? fp8_value(p.a[(i0 + ty) * p.lda + c], p.a_type) : 0.0f;
-            bs[ty][tx] = j0 + ty < p.n && c < p.k ? fp8_value(p.b[(j0 + ty) * p.ldb + c], p.b_type) : 0.0f;
-            __syncthreads();
+    *reinterpret_cast<uint4 *>(buf + row * 128 + ((piece ^ (row & 7)) << 4)) = v;
+}
+
+template <class T>
+__device__ __forceinline__ uint4 pack16(const uint64_t *acc);  // 16 bytes of T from pairs of sums
+template <>
+__device__ __forceinline__ uint4 pack16<float>(const uint64_t *acc)
+{
+    const float2 a = unpack2(acc[0]), b = unpack2(acc[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+}
+template <>
+__device__ __forceinline__ uint4 pack16<bf16>(const uint64_t *acc)
+{
+    uint32_t r[4];
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                part = fmaf(as[ty][e], bs[tx][e], part);
-        }
-        if (i < p.m && j < p.n) {
-            const int64_t kb = k0 / kBlock;
-            acc = fmaf(part, p.sa[kb * p.ldsa + i] * p.sb[kb * p.ldsb + (p.b_tile ? j / kBlock : j)], acc);
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = unpack2(acc[i]);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a.x, a.y);
+        r[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+template <>
+__device__ __forceinline__ uint4 pack16<f16>(const uint64_t *acc)
+{
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = unpack2(acc[i]);
+        const __half2 h = __floats2half2_rn(a.x, a.y);
+        r[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// 128 rows x 128 columns of sums (a thread one row) to the output by TMA
+// stores (or reductions), through two staging buffers of 128 bytes a row.
+// `id`: the group's barrier.
+template <class T>
+__device__ __forceinline__ void write_tma(const MatmulParams &p, const void *map, const uint64_t acc[64],
+                                          uint8_t *stage, int id, int t, int m0, int n0)
+{
+    constexpr int kCols = 128 / (int)sizeof(T);  // columns of one staging buffer
+    constexpr int kPairs = 8 / (int)sizeof(T);   // pairs of sums in 16 bytes
+#pragma unroll
+    for (int c = 0; c < 128 / kCols; ++c) {
+        uint8_t *buf = stage + (c & 1) * kStage;
+        const int x = n0 + c * kCols;
+        if (t == 0)
+            bulk_wait_read<1>();  // this buffer's last store has read it
+        barrier_of(id, 128);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            stage16(buf, t, i, pack16<T>(acc + (c * 8 + i) * kPairs));
+        fence_async_shared();
+        barrier_of(id, 128);
+        if (t == 0) {
+            if (x < p.n && m0 < p.m) {
+                if (p.add)
+                    tma_add(map, x, m0, smem_u32(buf));
+                else
+                    tma_store(map, x, m0, smem_u32(buf));
+            }
+            bulk_commit();
         }
     }
-    if (i >= p.m || j >= p.n)
-        return;
-    const int64_t at = i * p.ldo + j;
-    if (p.out_type == ZERO_T_F16) {
-        f16 *o = static_cast<f16 *>(p.out) + at;
-        *o = from_f32<f16>(p.add ? to_f32(*o) + acc : acc);
-    } else if (p.out_type == ZERO_T_BF16) {
-        bf16 *o = static_cast<bf16 *>(p.out) + at;
-        *o = from_f32<bf16>(p.add ? to_f32(*o) + acc : acc);
+}
+
+// The same element by element, neighbouring threads side by side, for rows
+// that no TMA store can write and for sums added in a half type; staged in
+// fp32, so that the sum with the old value is rounded once.
+template <class T>
+__device__ __forceinline__ void write_direct(const MatmulParams &p, const uint64_t acc[64], uint8_t *stage,
+                                             int id, int t, int m0, int n0)
+{
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint8_t *buf = stage + (c & 1) * kStage;
+        barrier_of(id, 128);  // its last readers are done
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            stage16(buf, t, i, pack16<float>(acc + (c * 8 + i) * 2));
+        barrier_of(id, 128);
+        const int col = n0 + c * 32 + (t & 31);
+        if (col < p.n)
+            for (int row = t >> 5; row < 128 && m0 + row < p.m; row += 4) {
+                T *o = static_cast<T *>(p.out) + (int64_t)(m0 + row) * p.ldo + col;
+                const float v = *reinterpret_cast<const float *>(
+                    buf + row * 128 + ((((t & 31) >> 2) ^ (row & 7)) << 4) + (t & 3) * 4);
+                *o = from_f32<T>(p.add ? to_f32(*o) + v : v);
+            }
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void write_tile(const MatmulParams &p, const void *map, const uint64_t acc[64],
+                                           uint8_t *stage, int id, int t, int m0, int n0)
+{
+    if (p.tma_out)
+        write_tma<T>(p, map, acc, stage, id, t, m0, n0);
+    else
+        write_direct<T>(p, acc, stage, id, t, m0, n0);
+}
+
+template <int CG, int NH, bool TILE_B>
+__global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
+    matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                  const __grid_constant__ CUtensorMap map_out, const __grid_constant__ MatmulParams p)
+{
+    using S = Shape<CG, NH>;
+    constexpr int kStages = S::kStages;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
+    __shared__ __align__(8) uint64_t sum_full[NH][2], sum_empty[NH][2], drain_bar;
+    __shared__ __align__(16) float col_scale[NH][2][128];
+    __shared__ uint32_t tmem_sh;
+    __shared__ int gave_up_sh, last_sh;
+    volatile int *gave_up = &gave_up_sh;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *staging = smem + kStages * S::kStageBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 1 ? 0 : cluster_rank();
+
+    if (threadIdx.x == 0) {
+        gave_up_sh = 0;
+        for (int i = 0; i < kStages; ++i) {
+            bar_init(smem_u32(&full_bar[i]), 1);
+            bar_init(smem_u32(&empty_bar[i]), 1);
+        }
+        for (int h = 0; h < NH; ++h)
+            for (int i = 0; i < 2; ++i) {
+                bar_init(smem_u32(&sum_full[h][i]), 1);
+                bar_init(smem_u32(&sum_empty[h][i]), 4 * CG);
+            }
+        bar_init(smem_u32(&drain_bar), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 4 * NH + 1)
+        tmem_alloc<CG>(smem_u32(&tmem_sh), S::kColumns);
+    fence_before();
+    __syncthreads();
+    if (CG == 2)
+        cluster_sync();
+    fence_after();
+    const uint32_t tmem = tmem_sh;
+    const int64_t units = (int64_t)p.tiles_m * p.tiles_n * p.splits;
+    const int64_t first = blockIdx.x / CG, step = gridDim.x / CG;
+
+    if (warp == 4 * NH) {
+        // ---------------------------------------------------------- copies
+        if (lane == 0) {
+            int64_t it = 0;
+            bool ok = true;
+            for (int64_t u = first; ok && u < units; u += step) {
+                const Unit w = unit_of(p, u);
+                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                    const int st = (int)(it % kStages);
+                    const uint32_t round = (uint32_t)(it / kStages);
+                    if (!(ok = bar_wait<CG>(smem_u32(&empty_bar[st]), (round & 1) ^ 1, gave_up)))
+                        break;
+                    const uint32_t a = smem_u32(smem + st * S::kStageBytes), b = a + S::kBytesA;
+                    uint32_t full = smem_u32(&full_bar[st]);
+                    if (rank == 0)
+                        bar_expect(full, CG * S::kStageBytes);
+                    if (CG == 2)
+                        full = map_to(full, 0);
+                    tma_load<CG>(a, &map_a, kb * 128, w.m * S::kTileM + (int)rank * 128, full);
+#pragma unroll
+                    for (int h = 0; h < NH; ++h)
+                        tma_load<CG>(b + h * S::kRowsB * 128, &map_b, kb * 128,
+                                     w.n * S::kTileN + h * 128 + (int)rank * S::kRowsB, full);
+                }
+            }
+            if (!ok && rank == 0)  // copies in flight land before the CTA ends
+                for (int64_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+                    for (int k = 0; k < kWaitLimit; ++k)
+                        if (bar_try<CG>(smem_u32(&full_bar[i % kStages]), (uint32_t)(i / kStages) & 1))
+                            break;
+        }
+    } else if (warp == 4 * NH + 1) {
+        // ---------------------------------------------------------- products
+        if (lane == 0 && rank == 0) {
+            int64_t it = 0;
+            bool ok = true;
+            for (int64_t u = first; ok && u < units; u += step) {
+                const Unit w = unit_of(p, u);
+                for (int kb = w.kb0; ok && kb < w.kb1; ++kb, ++it) {
+                    const int st = (int)(it % kStages), buf = (int)(it & 1);
+                    if (!(ok = bar_wait<CG>(smem_u32(&full_bar[st]), (uint32_t)(it / kStages) & 1, gave_up)))
+                        break;
+                    const uint32_t a = smem_u32(smem + st * S::kStageBytes), b = a + S::kBytesA;
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) {
+                        if (!(ok = bar_wait<CG>(smem_u32(&sum_empty[h][buf]), ((uint32_t)(it / 2) & 1) ^ 1,
+                                                gave_up)))
+                            break;
+                        fence_after();
+                        const uint64_t da = smem_desc(a), db = smem_desc(b + h * S::kRowsB * 128);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_f8<CG>(tmem + (buf * NH + h) * 128, da + k * 2, db + k * 2, p.instr, k > 0);
+                        mma_commit<CG>(smem_u32(&sum_full[h][buf]));
+                    }
+                    if (ok)
+                        mma_commit<CG>(smem_u32(&empty_bar[st]));
+                }
+            }
+            if (!ok) {  // products in flight end before tensor memory is freed
+                mma_commit<CG>(smem_u32(&drain_bar));
+                for (int k = 0; k < kWaitLimit; ++k)
+                    if (bar_try<CG>(smem_u32(&drain_bar), 0))
+                        break;
+            }
+        }
     } else {
-        float *o = static_cast<float *>(p.out) + at;
-        *o = p.add ? *o + acc : acc;
+        // ---------------------------------------------------------- scales and output
+        const int h = warp >> 2, quad = warp & 3, t = threadIdx.x & 127, id = 1 + h;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+        uint8_t *stage = staging + h * 2 * kStage;
+        int64_t it = 0;
+        bool ok = true;
+        for (int64_t u = first; u < units; u += step) {
+            const Unit w = unit_of(p, u);
+            const int m0 = w.m * S::kTileM + (int)rank * 128, n0 = w.n * S::kTileN + h * 128;
+            // this thread's row scale, and its column's (or the tile's), two blocks ahead
+            const bool has_row = m0 + t < p.m;
+            const int col = TILE_B ? n0 / 128 : n0 + t;
+            const bool has_col = TILE_B ? n0 < p.n : n0 + t < p.n;
+            const float *psa = p.sa + m0 + t, *psb = p.sb + col;
+            auto row_scale = [&](int kb) { return has_row && kb < w.kb1 ? __ldg(psa + kb * p.ldsa) : 0.0f; };
+            auto col_scale_of = [&](int kb) { return has_col && kb < w.kb1 ? __ldg(psb + kb * p.ldsb) : 0.0f; };
+            float a0 = row_scale(w.kb0), a1 = row_scale(w.kb0 + 1);
+            float b0 = col_scale_of(w.kb0), b1 = col_scale_of(w.kb0 + 1);
+            uint64_t acc[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+                acc[i] = 0;
+            for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                const int buf = (int)(it & 1);
+                const float a = a0, b = b0;
+                a0 = a1;
+                b0 = b1;
+                a1 = row_scale(kb + 2);
+                b1 = col_scale_of(kb + 2);
+                ok = ok && bar_wait_warp<1>(smem_u32(&sum_full[h][buf]), (uint32_t)(it / 2) & 1, gave_up);
+                if (!TILE_B) {
+                    col_scale[h][buf][t] = b;
+                    ok = !barrier_or(id, 128, !ok);
+                }
+                if (!ok)
+                    break;
+                fence_after();
+                const uint64_t s2 = TILE_B ? pack2(a * b, a * b) : pack2(a, a);
+                const uint32_t from = lanes + (uint32_t)((buf * NH + h) * 128);
+                uint32_t r[2][16];
+                tmem_ld16(from, r[0]);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    tmem_wait(r[c & 1]);
+                    if (c < 7) {
+                        tmem_ld16(from + (c + 1) * 16, r[(c + 1) & 1]);
+                    } else {
+                        fence_before();
+                        if (lane == 0) {
+                            uint32_t bar = smem_u32(&sum_empty[h][buf]);
+                            if (CG == 2)
+                                bar = map_to(bar, 0);
+                            bar_arrive<CG>(bar);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint64_t part = pack2(r[c & 1][2 * i], r[c & 1][2 * i + 1]);
+                        uint64_t s = s2;
+                        if (!TILE_B)
+                            s = mul2(s2, *reinterpret_cast<const uint64_t *>(&col_scale[h][buf][c * 16 + 2 * i]));
+                        acc[c * 8 + i] = fma2(part, s, acc[c * 8 + i]);
+                    }
+                }
+            }
+            if (barrier_or(id, 128, !ok)) {
+                ok = false;
+                break;
+            }
+            if (p.splits > 1) {
+                // this part's sums to the workspace; the tile's last part adds
+                // all of them in ascending order
+                float *mine = p.parts + ((int64_t)w.tile * p.splits + w.split) * (128 * 128) + t;
+                if (has_row)
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) {
+                        const float2 v = unpack2(acc[i]);
+                        __stcg(mine + (2 * i) * 128, v.x);
+                        __stcg(mine + (2 * i + 1) * 128, v.y);
+                    }
+                __threadfence();
+                barrier_of(id, 128);
+                if (t == 0) {
+                    last_sh = atomicAdd(p.counters + w.tile, 1u) == (uint32_t)p.splits - 1;
+                    __threadfence();
+                }
+                barrier_of(id, 128);
+                if (!last_sh)
+                    continue;
+                const float *all = p.parts + (int64_t)w.tile * p.splits * (128 * 128) + t;
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                    acc[i] = 0;
+                if (has_row)
+                    for (int s = 0; s < p.splits; ++s, all += 128 * 128)
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) {
+                            const float2 v = unpack2(acc[i]);
+                            acc[i] = pack2(v.x + __ldcg(all + (2 * i) * 128), v.y + __ldcg(all + (2 * i + 1) * 128));
+                        }
+                if (t == 0)
+                    p.counters[w.tile] = 0;
+            }
+            if (p.out_type == ZERO_T_BF16)
+                write_tile<bf16>(p, &map_out, acc, stage, id, t, m0, n0);
+            else if (p.out_type == ZERO_T_F16)
+                write_tile<f16>(p, &map_out, acc, stage, id, t, m0, n0);
+            else
+                write_tile<float>(p, &map_out, acc, stage, id, t, m0, n0);
+        }
+        if (t == 0)
+            bulk_wait_all();
     }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    if (CG == 2)
+        cluster_sync();
+    fence_after();
+    if (warp == 4 * NH + 1)
+        tmem_free<CG>(tmem, S::kColumns);
+    if (threadIdx.x == 0 && gave_up_sh)
+        atomicExch(p.error, 1);
+}
+
+// ------------------------------------------------------------------ host
+
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+// The driver's encoder of tensor maps (looked up once per process).
+static EncodeTiled encoder()
+{
+    static std::atomic<void *> found{nullptr};
+    void *f = found.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult how;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &how) !=
+                cudaSuccess || how != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            return nullptr;
+        }
+        found.store(f, std::memory_order_release);
+    }
+    return reinterpret_cast<EncodeTiled>(f);
+}
+
+// A map of a row-major matrix for boxes of box_rows rows of 128 bytes.
+static int encode(CUtensorMap *map, CUtensorMapDataType type, int bytes, const void *base, int64_t rows,
+                  int64_t cols, int64_t ld, int box_rows)
+{
+    const EncodeTiled f = encoder();
+    if (!f)
+        return cuda_error(cudaErrorSymbolNotFound);
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * (cuuint64_t)bytes};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / bytes), (cuuint32_t)box_rows};
+    const cuuint32_t one[2] = {1, 1};
+    const CUresult r = f(map, type, 2, const_cast<void *>(base), dims, strides, box, one,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? ZERO_OK : ZERO_EINVAL;
+}
+
+// How a product is cut: pairs of CTAs on 256x256 tiles where there are enough
+// of them for the SMs, else single CTAs on 128x128 tiles with k split so that
+// the parts fill the SMs.
+struct Plan {
+    bool pair;
+    int64_t tiles_m, tiles_n;
+    int splits;
+};
+static Plan plan_of(int64_t m, int64_t n, int64_t k)
+{
+    Plan r{};
+    const int64_t kb = ceil_div(k, kBlock);
+    if (ceil_div(m, 256) * ceil_div(n, 256) >= kPlanSms / 2) {
+        r.pair = true;
+        r.tiles_m = ceil_div(m, 256);
+        r.tiles_n = ceil_div(n, 256);
+        r.splits = 1;
+        return r;
+    }
+    r.tiles_m = ceil_div(m, 128);
+    r.tiles_n = ceil_div(n, 128);
+    const int64_t tiles = r.tiles_m * r.tiles_n;
+    int64_t s = kPlanSms / tiles;
+    if (s > kb / 4)  // a part is worth its sums' way through memory from four blocks on
+        s = kb / 4;
+    r.splits = (int)(s < 1 ? 1 : s);
+    return r;
+}
+
+template <int CG, int NH>
+static int launch_matmul(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o, const MatmulParams &p,
+                         bool tile_b, cudaStream_t stream)
+{
+    using S = Shape<CG, NH>;
+    auto kernel = tile_b ? matmul_kernel<CG, NH, true> : matmul_kernel<CG, NH, false>;
+    static_assert(S::kSmem <= 227 * 1024 - 4096, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess)
+        return cuda_error(e);
+    const int64_t units = (int64_t)p.tiles_m * p.tiles_n * p.splits;
+    const int64_t most = device_sms() / CG;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((units < most ? units : most) * CG));
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {CG, 1, 1};
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, a, b, o, p);
+    return e == cudaSuccess ? launch_status() : cuda_error(e);
 }
 
 }  // namespace zo
@@ -69,7 +524,9 @@ size_t zero_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k)
 {
     if (bad_dim(m) || bad_dim(n) || bad_dim(k))
         return 0;
-    return 256;
+    const Plan plan = plan_of(m, n, k);
+    return (size_t)kHead + (plan.splits > 1 ? (size_t)(plan.tiles_m * plan.tiles_n * plan.splits) * 128 * 128 * 4
+                                            : 0);
 }
 
 int zero_fp8_matmul(const void *a, int a_type, int64_t lda, const float *sa, int64_t ldsa,
@@ -82,7 +539,8 @@ int zero_fp8_matmul(const void *a, int a_type, int64_t lda, const float *sa, int
         return ZERO_EINVAL;
     if (m == 0 || n == 0)
         return ZERO_OK;
-    int rc = check_matrix(out, m, n, ldo, type_bytes(out_type));
+    const int ob = type_bytes(out_type);
+    int rc = check_matrix(out, m, n, ldo, ob);
     if (!rc)
         rc = check_matrix(a, m, k, lda, 1);
     if (!rc)
@@ -97,28 +555,47 @@ int zero_fp8_matmul(const void *a, int a_type, int64_t lda, const float *sa, int
         rc = ZERO_ESPACE;
     if (rc)
         return rc;
+    if (k == 0) {
+        if (add)
+            return ZERO_OK;
+        const cudaError_t e = cudaMemset2DAsync(out, (size_t)(ldo * ob), 0, (size_t)(n * ob), (size_t)m, stream);
+        return e == cudaSuccess ? ZERO_OK : cuda_error(e);
+    }
+    const Plan plan = plan_of(m, n, k);
     MatmulParams p{};
-    p.a = static_cast<const uint8_t *>(a);
-    p.b = static_cast<const uint8_t *>(b);
     p.sa = sa;
     p.sb = sb;
     p.out = out;
-    p.lda = lda;
-    p.ldb = ldb;
+    p.error = static_cast<int32_t *>(ws);
+    p.counters = reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + kCounters);
+    p.parts = reinterpret_cast<float *>(static_cast<char *>(ws) + kHead);
     p.ldsa = ldsa;
     p.ldsb = ldsb;
     p.ldo = ldo;
-    p.m = m;
-    p.n = n;
-    p.k = k;
-    p.a_type = a_type;
-    p.b_type = b_type;
-    p.b_tile = b_tile;
+    p.m = (int32_t)m;
+    p.n = (int32_t)n;
+    p.kb = (int32_t)ceil_div(k, kBlock);
+    p.tiles_m = (int32_t)plan.tiles_m;
+    p.tiles_n = (int32_t)plan.tiles_n;
+    p.splits = plan.splits;
     p.out_type = out_type;
     p.add = add ? 1 : 0;
-    const dim3 grid((unsigned)ceil_div(n, 16), (unsigned)ceil_div(m, 16));
-    matmul_kernel<<<grid, 256, 0, stream>>>(p);
-    return launch_status();
+    p.instr = f8_instr(a_type == ZERO_T_E5M2, b_type == ZERO_T_E5M2, plan.pair ? 256 : 128, 128);
+    // a TMA store (or reduction) of whole boxes; half types are added in fp32 and rounded once
+    p.tma_out = rows_aligned(out, ldo, ob, 16) && (!add || out_type == ZERO_T_F32);
+    CUtensorMap ma, mb, mo{};
+    rc = encode(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a, m, k, lda, 128);
+    if (!rc)
+        rc = encode(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, b, n, k, ldb, plan.pair ? 64 : 128);
+    if (!rc && p.tma_out)
+        rc = encode(&mo, out_type == ZERO_T_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                         : out_type == ZERO_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                    ob, out, m, n, ldo, 128);
+    if (rc)
+        return rc;
+    return plan.pair ? launch_matmul<2, 2>(ma, mb, mo, p, b_tile != 0, stream)
+                     : launch_matmul<1, 1>(ma, mb, mo, p, b_tile != 0, stream);
 }
 
 }  // extern "C"
