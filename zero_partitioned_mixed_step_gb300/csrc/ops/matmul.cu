@@ -47,7 +47,9 @@ struct MatmulParams {
 
 template <int CG, int NH>
 struct Shape {
-    static constexpr int kThreads = 128 * NH + 64;
+    // two groups leave no registers to spare: whole warpgroups, so that the
+    // copying one can give some of its own (168 x 384 = 208 x 256 + 88 x 128)
+    static constexpr int kThreads = NH == 1 ? 192 : 384;
     static constexpr int kTileM = 128 * CG, kTileN = 128 * NH;
     static constexpr int kRowsB = 128 / CG;  // of each 128 columns, in one CTA
     static constexpr int kBytesA = 128 * 128, kBytesB = NH * kRowsB * 128;
@@ -229,7 +231,10 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
     const int64_t units = (int64_t)p.tiles_m * p.tiles_n * p.splits;
     const int64_t first = blockIdx.x / CG, step = gridDim.x / CG;
 
-    if (warp == 4 * NH) {
+    if (warp >= 4 * NH) {
+        if (NH == 2)
+            registers_down<88>();
+        if (warp == 4 * NH) {
         // ---------------------------------------------------------- copies
         if (lane == 0) {
             int64_t it = 0;
@@ -239,7 +244,7 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
                 for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                     const int st = (int)(it % kStages);
                     const uint32_t round = (uint32_t)(it / kStages);
-                    if (!(ok = bar_wait<CG>(smem_u32(&empty_bar[st]), (round & 1) ^ 1, gave_up)))
+                    if (!(ok = bar_wait(smem_u32(&empty_bar[st]), (round & 1) ^ 1, gave_up)))
                         break;
                     const uint32_t a = smem_u32(smem + st * S::kStageBytes), b = a + S::kBytesA;
                     uint32_t full = smem_u32(&full_bar[st]);
@@ -257,10 +262,10 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
             if (!ok && rank == 0)  // copies in flight land before the CTA ends
                 for (int64_t i = it > kStages ? it - kStages : 0; i < it; ++i)
                     for (int k = 0; k < kWaitLimit; ++k)
-                        if (bar_try<CG>(smem_u32(&full_bar[i % kStages]), (uint32_t)(i / kStages) & 1))
+                        if (bar_try(smem_u32(&full_bar[i % kStages]), (uint32_t)(i / kStages) & 1))
                             break;
         }
-    } else if (warp == 4 * NH + 1) {
+        } else if (warp == 4 * NH + 1) {
         // ---------------------------------------------------------- products
         if (lane == 0 && rank == 0) {
             int64_t it = 0;
@@ -269,12 +274,12 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
                 const Unit w = unit_of(p, u);
                 for (int kb = w.kb0; ok && kb < w.kb1; ++kb, ++it) {
                     const int st = (int)(it % kStages), buf = (int)(it & 1);
-                    if (!(ok = bar_wait<CG>(smem_u32(&full_bar[st]), (uint32_t)(it / kStages) & 1, gave_up)))
+                    if (!(ok = bar_wait(smem_u32(&full_bar[st]), (uint32_t)(it / kStages) & 1, gave_up)))
                         break;
                     const uint32_t a = smem_u32(smem + st * S::kStageBytes), b = a + S::kBytesA;
 #pragma unroll
                     for (int h = 0; h < NH; ++h) {
-                        if (!(ok = bar_wait<CG>(smem_u32(&sum_empty[h][buf]), ((uint32_t)(it / 2) & 1) ^ 1,
+                        if (!(ok = bar_wait(smem_u32(&sum_empty[h][buf]), ((uint32_t)(it / 2) & 1) ^ 1,
                                                 gave_up)))
                             break;
                         fence_after();
@@ -291,11 +296,14 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
             if (!ok) {  // products in flight end before tensor memory is freed
                 mma_commit<CG>(smem_u32(&drain_bar));
                 for (int k = 0; k < kWaitLimit; ++k)
-                    if (bar_try<CG>(smem_u32(&drain_bar), 0))
+                    if (bar_try(smem_u32(&drain_bar), 0))
                         break;
             }
         }
+        }
     } else {
+        if (NH == 2)
+            registers_up<208>();
         // ---------------------------------------------------------- scales and output
         const int h = warp >> 2, quad = warp & 3, t = threadIdx.x & 127, id = 1 + h;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
@@ -325,7 +333,7 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
                 b0 = b1;
                 a1 = row_scale(kb + 2);
                 b1 = col_scale_of(kb + 2);
-                ok = ok && bar_wait_warp<1>(smem_u32(&sum_full[h][buf]), (uint32_t)(it / 2) & 1, gave_up);
+                ok = ok && bar_wait_warp(smem_u32(&sum_full[h][buf]), (uint32_t)(it / 2) & 1, gave_up);
                 if (!TILE_B) {
                     col_scale[h][buf][t] = b;
                     ok = !barrier_or(id, 128, !ok);

@@ -45,43 +45,50 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
                  : "memory");
 }
 
-// An arrival at a barrier of this CTA or, with CG = 2, of the pair's first one.
+// An arrival at a barrier of this CTA or, with CG = 2, of the pair's first
+// one.  What it orders is tensor memory (by the tcgen05 fences), so CTA scope
+// is enough: a release at cluster scope waits for the thread's other stores,
+// which measured three times the whole product's time.
 template <int CG>
 __device__ __forceinline__ void bar_arrive(uint32_t bar)
 {
     if (CG == 1)
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
     else
-        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-                     : "memory");
+        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-template <int CG>
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
-    if (CG == 1)
-        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;"
-                     " selp.u32 %0, 1, 0, p; }"
-                     : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    else
-        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;"
-                     " selp.u32 %0, 1, 0, p; }"
-                     : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;"
+                 " selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
+}
+
+// The registers of a warpgroup's threads, given to or taken from the block's others.
+template <int N>
+__device__ __forceinline__ void registers_up()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 constexpr int kWaitLimit = 1 << 23;  // polls, each of which may sleep: a second or more
 
 // Waits for a barrier's phase; false when the polls run out or another role of
 // the CTA has given up (*gave_up, in shared memory).
-template <int CG>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up)
 {
-    if (bar_try<CG>(bar, parity))
+    if (bar_try(bar, parity))
         return true;
     for (int i = 0; i < kWaitLimit; ++i) {
-        if (bar_try<CG>(bar, parity))
+        if (bar_try(bar, parity))
             return true;
         if ((i & 63) == 63 && *gave_up)
             return false;
@@ -91,10 +98,9 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
 }
 
 // The same for a whole warp, with one answer.
-template <int CG>
 __device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, volatile int *gave_up)
 {
-    return __all_sync(0xFFFFFFFFu, bar_wait<CG>(bar, parity, gave_up));
+    return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, gave_up));
 }
 
 // ------------------------------------------------------------------ TMA
