@@ -31,6 +31,14 @@ constexpr int kHead = 4096;        // bytes of the workspace ahead of the partia
 constexpr int kCounters = 256;     // offset of the tiles' counters (zero between calls)
 constexpr int kPlanSms = 152;      // the rule for splitting k counts on a GB300's SMs
 constexpr int kStage = 16 * 1024;  // bytes of one staging buffer of the output
+// The scales come through a ring in shared memory, kAhead blocks of k ahead
+// of their use, by a warp of their own.  (Loads into the epilogue threads'
+// registers two blocks ahead were waited for at every block: 1350 cycles a
+// block where the products take 512.)  A slot is written again when the sums
+// of the block three later (kRing - kAhead - 2) are complete: the products of
+// that block waited for every epilogue warp to have taken the sums of the block
+// after the slot's, so all are done with the slot's scales.
+constexpr int kRing = 8, kAhead = 3;
 
 struct MatmulParams {
     const float *sa, *sb;
@@ -40,7 +48,7 @@ struct MatmulParams {
     float *parts;
     int64_t ldsa, ldsb, ldo;
     int32_t m, n, kb;           // rows, columns, blocks of k
-    int32_t tiles_m, tiles_n, splits;
+    int32_t tiles_m, tiles_n, splits, units;
     int32_t out_type, add, tma_out;
     uint32_t instr;
 };
@@ -48,8 +56,8 @@ struct MatmulParams {
 template <int CG, int NH>
 struct Shape {
     // two groups leave no registers to spare: whole warpgroups, so that the
-    // copying one can give some of its own (168 x 384 = 208 x 256 + 88 x 128)
-    static constexpr int kThreads = NH == 1 ? 192 : 384;
+    // copying one can give some of its own (168 x 384 = 216 x 256 + 72 x 128)
+    static constexpr int kThreads = NH == 1 ? 224 : 384;
     static constexpr int kTileM = 128 * CG, kTileN = 128 * NH;
     static constexpr int kRowsB = 128 / CG;  // of each 128 columns, in one CTA
     static constexpr int kBytesA = 128 * 128, kBytesB = NH * kRowsB * 128;
@@ -64,11 +72,11 @@ struct Shape {
 struct Unit {
     int m, n, kb0, kb1, tile, split;
 };
-__device__ __forceinline__ Unit unit_of(const MatmulParams &p, int64_t u)
+__device__ __forceinline__ Unit unit_of(const MatmulParams &p, int u)
 {
     Unit r;
-    r.split = (int)(u % p.splits);
-    r.tile = (int)(u / p.splits);
+    r.split = u % p.splits;
+    r.tile = u / p.splits;
     constexpr int kGroup = 8;
     const int per = kGroup * p.tiles_n, g = r.tile / per, in = r.tile % per;
     const int rows = min(kGroup, p.tiles_m - g * kGroup);
@@ -79,6 +87,30 @@ __device__ __forceinline__ Unit unit_of(const MatmulParams &p, int64_t u)
     return r;
 }
 
+// Walks the blocks of k of a CTA's units, one after the other.
+struct Walk {
+    Unit w;
+    int u, kb;
+    bool more;
+    __device__ __forceinline__ Walk(const MatmulParams &p, int first) : u(first), kb(0), more(first < p.units)
+    {
+        if (more) {
+            w = unit_of(p, u);
+            kb = w.kb0;
+        }
+    }
+    __device__ __forceinline__ void next(const MatmulParams &p, int step)
+    {
+        if (++kb < w.kb1)
+            return;
+        u += step;
+        if ((more = u < p.units)) {
+            w = unit_of(p, u);
+            kb = w.kb0;
+        }
+    }
+};
+
 // Writes 16 bytes of a row of a staging buffer (128 rows of 128 bytes, swizzled as the TMA reads them).
 __device__ __forceinline__ void stage16(uint8_t *buf, int row, int piece, uint4 v)
 {
@@ -86,33 +118,31 @@ __device__ __forceinline__ void stage16(uint8_t *buf, int row, int piece, uint4 
 }
 
 template <class T>
-__device__ __forceinline__ uint4 pack16(const uint64_t *acc);  // 16 bytes of T from pairs of sums
+__device__ __forceinline__ uint4 pack16(const float *acc);  // 16 bytes of T
 template <>
-__device__ __forceinline__ uint4 pack16<float>(const uint64_t *acc)
+__device__ __forceinline__ uint4 pack16<float>(const float *acc)
 {
-    const float2 a = unpack2(acc[0]), b = unpack2(acc[1]);
-    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+    return make_uint4(__float_as_uint(acc[0]), __float_as_uint(acc[1]), __float_as_uint(acc[2]),
+                      __float_as_uint(acc[3]));
 }
 template <>
-__device__ __forceinline__ uint4 pack16<bf16>(const uint64_t *acc)
+__device__ __forceinline__ uint4 pack16<bf16>(const float *acc)
 {
     uint32_t r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 a = unpack2(acc[i]);
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a.x, a.y);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
         r[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 template <>
-__device__ __forceinline__ uint4 pack16<f16>(const uint64_t *acc)
+__device__ __forceinline__ uint4 pack16<f16>(const float *acc)
 {
     uint32_t r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 a = unpack2(acc[i]);
-        const __half2 h = __floats2half2_rn(a.x, a.y);
+        const __half2 h = __floats2half2_rn(acc[2 * i], acc[2 * i + 1]);
         r[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
@@ -122,11 +152,11 @@ __device__ __forceinline__ uint4 pack16<f16>(const uint64_t *acc)
 // stores (or reductions), through two staging buffers of 128 bytes a row.
 // `id`: the group's barrier.
 template <class T>
-__device__ __forceinline__ void write_tma(const MatmulParams &p, const void *map, const uint64_t acc[64],
+__device__ __forceinline__ void write_tma(const MatmulParams &p, const void *map, const float acc[128],
                                           uint8_t *stage, int id, int t, int m0, int n0)
 {
     constexpr int kCols = 128 / (int)sizeof(T);  // columns of one staging buffer
-    constexpr int kPairs = 8 / (int)sizeof(T);   // pairs of sums in 16 bytes
+    constexpr int kPiece = 16 / (int)sizeof(T);  // sums in 16 bytes
 #pragma unroll
     for (int c = 0; c < 128 / kCols; ++c) {
         uint8_t *buf = stage + (c & 1) * kStage;
@@ -136,7 +166,7 @@ __device__ __forceinline__ void write_tma(const MatmulParams &p, const void *map
         barrier_of(id, 128);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            stage16(buf, t, i, pack16<T>(acc + (c * 8 + i) * kPairs));
+            stage16(buf, t, i, pack16<T>(acc + (c * 8 + i) * kPiece));
         fence_async_shared();
         barrier_of(id, 128);
         if (t == 0) {
@@ -155,7 +185,7 @@ __device__ __forceinline__ void write_tma(const MatmulParams &p, const void *map
 // that no TMA store can write and for sums added in a half type; staged in
 // fp32, so that the sum with the old value is rounded once.
 template <class T>
-__device__ __forceinline__ void write_direct(const MatmulParams &p, const uint64_t acc[64], uint8_t *stage,
+__device__ __forceinline__ void write_direct(const MatmulParams &p, const float acc[128], uint8_t *stage,
                                              int id, int t, int m0, int n0)
 {
 #pragma unroll
@@ -164,7 +194,7 @@ __device__ __forceinline__ void write_direct(const MatmulParams &p, const uint64
         barrier_of(id, 128);  // its last readers are done
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            stage16(buf, t, i, pack16<float>(acc + (c * 8 + i) * 2));
+            stage16(buf, t, i, pack16<float>(acc + (c * 8 + i) * 4));
         barrier_of(id, 128);
         const int col = n0 + c * 32 + (t & 31);
         if (col < p.n)
@@ -178,7 +208,7 @@ __device__ __forceinline__ void write_direct(const MatmulParams &p, const uint64
 }
 
 template <class T>
-__device__ __forceinline__ void write_tile(const MatmulParams &p, const void *map, const uint64_t acc[64],
+__device__ __forceinline__ void write_tile(const MatmulParams &p, const void *map, const float acc[128],
                                            uint8_t *stage, int id, int t, int m0, int n0)
 {
     if (p.tma_out)
@@ -197,13 +227,13 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
     __shared__ __align__(8) uint64_t sum_full[NH][2], sum_empty[NH][2], drain_bar;
-    __shared__ __align__(16) float col_scale[NH][2][128];
+    __shared__ __align__(16) float scale_a[kRing][128], scale_b[kRing][TILE_B ? NH : NH * 128];
     __shared__ uint32_t tmem_sh;
     __shared__ int gave_up_sh, last_sh;
     volatile int *gave_up = &gave_up_sh;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     uint8_t *staging = smem + kStages * S::kStageBytes;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = CG == 1 ? 0 : cluster_rank();
 
     if (threadIdx.x == 0) {
@@ -214,7 +244,7 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
         }
         for (int h = 0; h < NH; ++h)
             for (int i = 0; i < 2; ++i) {
-                bar_init(smem_u32(&sum_full[h][i]), 1);
+                bar_init(smem_u32(&sum_full[h][i]), 2);  // the products, the scales
                 bar_init(smem_u32(&sum_empty[h][i]), 4 * CG);
             }
         bar_init(smem_u32(&drain_bar), 1);
@@ -228,23 +258,23 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
         cluster_sync();
     fence_after();
     const uint32_t tmem = tmem_sh;
-    const int64_t units = (int64_t)p.tiles_m * p.tiles_n * p.splits;
-    const int64_t first = blockIdx.x / CG, step = gridDim.x / CG;
+    const int units = p.units, first = blockIdx.x / CG, step = gridDim.x / CG;
 
     if (warp >= 4 * NH) {
         if (NH == 2)
-            registers_down<88>();
+            registers_down<72>();
         if (warp == 4 * NH) {
         // ---------------------------------------------------------- copies
-        if (lane == 0) {
-            int64_t it = 0;
+        if (elect_one()) {
+            int st = 0, issued = 0;
+            uint32_t phase = 1;  // an empty stage counts as released
             bool ok = true;
-            for (int64_t u = first; ok && u < units; u += step) {
+            for (int u = first; ok && u < units; u += step) {
                 const Unit w = unit_of(p, u);
-                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-                    const int st = (int)(it % kStages);
-                    const uint32_t round = (uint32_t)(it / kStages);
-                    if (!(ok = bar_wait(smem_u32(&empty_bar[st]), (round & 1) ^ 1, gave_up)))
+                const int row_a = w.m * S::kTileM + (int)rank * 128;
+                const int row_b = w.n * S::kTileN + (int)rank * S::kRowsB;
+                for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                    if (!(ok = bar_wait(smem_u32(&empty_bar[st]), phase, gave_up)))
                         break;
                     const uint32_t a = smem_u32(smem + st * S::kStageBytes), b = a + S::kBytesA;
                     uint32_t full = smem_u32(&full_bar[st]);
@@ -252,35 +282,43 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
                         bar_expect(full, CG * S::kStageBytes);
                     if (CG == 2)
                         full = map_to(full, 0);
-                    tma_load<CG>(a, &map_a, kb * 128, w.m * S::kTileM + (int)rank * 128, full);
+                    tma_load<CG>(a, &map_a, kb * 128, row_a, full);
 #pragma unroll
                     for (int h = 0; h < NH; ++h)
-                        tma_load<CG>(b + h * S::kRowsB * 128, &map_b, kb * 128,
-                                     w.n * S::kTileN + h * 128 + (int)rank * S::kRowsB, full);
+                        tma_load<CG>(b + h * S::kRowsB * 128, &map_b, kb * 128, row_b + h * 128, full);
+                    issued = issued < kStages ? issued + 1 : kStages;
+                    if (++st == kStages) {
+                        st = 0;
+                        phase ^= 1;
+                    }
                 }
             }
             if (!ok && rank == 0)  // copies in flight land before the CTA ends
-                for (int64_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+                for (int i = 0; i < issued; ++i) {
+                    if (--st < 0) {
+                        st = kStages - 1;
+                        phase ^= 1;
+                    }
                     for (int k = 0; k < kWaitLimit; ++k)
-                        if (bar_try(smem_u32(&full_bar[i % kStages]), (uint32_t)(i / kStages) & 1))
+                        if (bar_try(smem_u32(&full_bar[st]), phase ^ 1))
                             break;
+                }
         }
         } else if (warp == 4 * NH + 1) {
         // ---------------------------------------------------------- products
-        if (lane == 0 && rank == 0) {
-            int64_t it = 0;
+        if (rank == 0 && elect_one()) {
+            int st = 0, buf = 0;
+            uint32_t phase = 0, free_phase = 1;
             bool ok = true;
-            for (int64_t u = first; ok && u < units; u += step) {
+            for (int u = first; ok && u < units; u += step) {
                 const Unit w = unit_of(p, u);
-                for (int kb = w.kb0; ok && kb < w.kb1; ++kb, ++it) {
-                    const int st = (int)(it % kStages), buf = (int)(it & 1);
-                    if (!(ok = bar_wait(smem_u32(&full_bar[st]), (uint32_t)(it / kStages) & 1, gave_up)))
+                for (int kb = w.kb0; ok && kb < w.kb1; ++kb) {
+                    if (!(ok = bar_wait(smem_u32(&full_bar[st]), phase, gave_up)))
                         break;
                     const uint32_t a = smem_u32(smem + st * S::kStageBytes), b = a + S::kBytesA;
 #pragma unroll
                     for (int h = 0; h < NH; ++h) {
-                        if (!(ok = bar_wait(smem_u32(&sum_empty[h][buf]), ((uint32_t)(it / 2) & 1) ^ 1,
-                                                gave_up)))
+                        if (!(ok = bar_wait(smem_u32(&sum_empty[h][buf]), free_phase, gave_up)))
                             break;
                         fence_after();
                         const uint64_t da = smem_desc(a), db = smem_desc(b + h * S::kRowsB * 128);
@@ -291,6 +329,12 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
                     }
                     if (ok)
                         mma_commit<CG>(smem_u32(&empty_bar[st]));
+                    if (++st == kStages) {
+                        st = 0;
+                        phase ^= 1;
+                    }
+                    buf ^= 1;
+                    free_phase ^= buf == 0;
                 }
             }
             if (!ok) {  // products in flight end before tensor memory is freed
@@ -300,56 +344,86 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
                         break;
             }
         }
+        } else if (warp == 4 * NH + 2) {
+        // ---------------------------------------------------------- scales
+        auto copy_scales = [&](const Walk &k, int slot) {
+            if (k.more) {
+                const float *sa = p.sa + k.kb * p.ldsa, *sb = p.sb + k.kb * p.ldsb;
+                const int row = k.w.m * S::kTileM + (int)rank * 128 + lane;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    copy4(smem_u32(&scale_a[slot][i * 32 + lane]), row + i * 32 < p.m ? sa + row + i * 32 : p.sa,
+                          row + i * 32 < p.m);
+                if (TILE_B) {
+                    const int col = k.w.n * NH + lane;
+                    if (lane < NH)
+                        copy4(smem_u32(&scale_b[slot][lane]), col * 128 < p.n ? sb + col : p.sb, col * 128 < p.n);
+                } else {
+                    const int col = k.w.n * S::kTileN + lane;
+#pragma unroll
+                    for (int i = 0; i < 4 * NH; ++i)
+                        copy4(smem_u32(&scale_b[slot][i * 32 + lane]), col + i * 32 < p.n ? sb + col + i * 32 : p.sb,
+                              col + i * 32 < p.n);
+                }
+            }
+            copy_commit();
+        };
+        Walk use(p, first), load(p, first);
+        for (int i = 0; i < kAhead; ++i, load.next(p, step))
+            copy_scales(load, i);
+        int slot = 0, buf = 0;
+        uint32_t phase = 1;  // of the block that had this buffer before
+        for (; use.more; use.next(p, step)) {
+            copy_wait<kAhead - 1>();
+            bool ok = true;
+            for (int h = 0; h < NH; ++h)
+                ok = ok && bar_wait_warp(smem_u32(&sum_full[h][buf]), phase, gave_up);
+            if (!ok)
+                break;
+            __syncwarp();
+            if (lane == 0)
+                for (int h = 0; h < NH; ++h)
+                    bar_arrive<1>(smem_u32(&sum_full[h][buf]));
+            copy_scales(load, (slot + kAhead) % kRing);
+            load.next(p, step);
+            slot = (slot + 1) % kRing;
+            buf ^= 1;
+            phase ^= buf == 0;
+        }
         }
     } else {
         if (NH == 2)
-            registers_up<208>();
+            registers_up<216>();
         // ---------------------------------------------------------- scales and output
         const int h = warp >> 2, quad = warp & 3, t = threadIdx.x & 127, id = 1 + h;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         uint8_t *stage = staging + h * 2 * kStage;
-        int64_t it = 0;
+        int buf = 0;
+        uint32_t phase = 0;
         bool ok = true;
-        for (int64_t u = first; u < units; u += step) {
+        int slot = 0;
+        for (int u = first; u < units; u += step) {
             const Unit w = unit_of(p, u);
             const int m0 = w.m * S::kTileM + (int)rank * 128, n0 = w.n * S::kTileN + h * 128;
-            // this thread's row scale, and its column's (or the tile's), two blocks ahead
             const bool has_row = m0 + t < p.m;
-            const int col = TILE_B ? n0 / 128 : n0 + t;
-            const bool has_col = TILE_B ? n0 < p.n : n0 + t < p.n;
-            const float *psa = p.sa + m0 + t, *psb = p.sb + col;
-            auto row_scale = [&](int kb) { return has_row && kb < w.kb1 ? __ldg(psa + kb * p.ldsa) : 0.0f; };
-            auto col_scale_of = [&](int kb) { return has_col && kb < w.kb1 ? __ldg(psb + kb * p.ldsb) : 0.0f; };
-            float a0 = row_scale(w.kb0), a1 = row_scale(w.kb0 + 1);
-            float b0 = col_scale_of(w.kb0), b1 = col_scale_of(w.kb0 + 1);
-            uint64_t acc[64];
+            float acc[128];
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-                acc[i] = 0;
-            for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-                const int buf = (int)(it & 1);
-                const float a = a0, b = b0;
-                a0 = a1;
-                b0 = b1;
-                a1 = row_scale(kb + 2);
-                b1 = col_scale_of(kb + 2);
-                ok = ok && bar_wait_warp(smem_u32(&sum_full[h][buf]), (uint32_t)(it / 2) & 1, gave_up);
-                if (!TILE_B) {
-                    col_scale[h][buf][t] = b;
-                    ok = !barrier_or(id, 128, !ok);
-                }
-                if (!ok)
+            for (int i = 0; i < 128; ++i)
+                acc[i] = 0.0f;
+            for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                if (!(ok = bar_wait_warp(smem_u32(&sum_full[h][buf]), phase, gave_up)))
                     break;
                 fence_after();
-                const uint64_t s2 = TILE_B ? pack2(a * b, a * b) : pack2(a, a);
                 const uint32_t from = lanes + (uint32_t)((buf * NH + h) * 128);
-                uint32_t r[2][16];
-                tmem_ld16(from, r[0]);
+                uint32_t r[2][32];
+                tmem_ld32(from, r[0]);
+                const float ab = TILE_B ? scale_a[slot][t] * scale_b[slot][h] : scale_a[slot][t];
+                const float *sb = &scale_b[slot][TILE_B ? 0 : h * 128];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    tmem_wait(r[c & 1]);
-                    if (c < 7) {
-                        tmem_ld16(from + (c + 1) * 16, r[(c + 1) & 1]);
+                for (int c = 0; c < 4; ++c) {
+                    tmem_wait();
+                    if (c < 3) {
+                        tmem_ld32(from + (c + 1) * 32, r[(c + 1) & 1]);
                     } else {
                         fence_before();
                         if (lane == 0) {
@@ -360,14 +434,12 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint64_t part = pack2(r[c & 1][2 * i], r[c & 1][2 * i + 1]);
-                        uint64_t s = s2;
-                        if (!TILE_B)
-                            s = mul2(s2, *reinterpret_cast<const uint64_t *>(&col_scale[h][buf][c * 16 + 2 * i]));
-                        acc[c * 8 + i] = fma2(part, s, acc[c * 8 + i]);
-                    }
+                    for (int i = 0; i < 32; ++i)
+                        scale_add(acc[c * 32 + i], r[c & 1][i], TILE_B ? ab : ab * sb[c * 32 + i]);
                 }
+                slot = (slot + 1) % kRing;
+                buf ^= 1;
+                phase ^= buf == 0;
             }
             if (barrier_or(id, 128, !ok)) {
                 ok = false;
@@ -379,11 +451,8 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
                 float *mine = p.parts + ((int64_t)w.tile * p.splits + w.split) * (128 * 128) + t;
                 if (has_row)
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) {
-                        const float2 v = unpack2(acc[i]);
-                        __stcg(mine + (2 * i) * 128, v.x);
-                        __stcg(mine + (2 * i + 1) * 128, v.y);
-                    }
+                    for (int i = 0; i < 128; ++i)
+                        __stcg(mine + i * 128, acc[i]);
                 __threadfence();
                 barrier_of(id, 128);
                 if (t == 0) {
@@ -395,15 +464,13 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
                     continue;
                 const float *all = p.parts + (int64_t)w.tile * p.splits * (128 * 128) + t;
 #pragma unroll
-                for (int i = 0; i < 64; ++i)
-                    acc[i] = 0;
+                for (int i = 0; i < 128; ++i)
+                    acc[i] = 0.0f;
                 if (has_row)
                     for (int s = 0; s < p.splits; ++s, all += 128 * 128)
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) {
-                            const float2 v = unpack2(acc[i]);
-                            acc[i] = pack2(v.x + __ldcg(all + (2 * i) * 128), v.y + __ldcg(all + (2 * i + 1) * 128));
-                        }
+                        for (int i = 0; i < 128; ++i)
+                            acc[i] += __ldcg(all + i * 128);
                 if (t == 0)
                     p.counters[w.tile] = 0;
             }
@@ -506,7 +573,7 @@ static int launch_matmul(const CUtensorMap &a, const CUtensorMap &b, const CUten
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess)
         return cuda_error(e);
-    const int64_t units = (int64_t)p.tiles_m * p.tiles_n * p.splits;
+    const int64_t units = p.units;
     const int64_t most = device_sms() / CG;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((units < most ? units : most) * CG));
@@ -586,6 +653,10 @@ int zero_fp8_matmul(const void *a, int a_type, int64_t lda, const float *sa, int
     p.tiles_m = (int32_t)plan.tiles_m;
     p.tiles_n = (int32_t)plan.tiles_n;
     p.splits = plan.splits;
+    const int64_t units = plan.tiles_m * plan.tiles_n * plan.splits;
+    if (units > kMaxDim)
+        return ZERO_EINVAL;
+    p.units = (int32_t)units;
     p.out_type = out_type;
     p.add = add ? 1 : 0;
     p.instr = f8_instr(a_type == ZERO_T_E5M2, b_type == ZERO_T_E5M2, plan.pair ? 256 : 128, 128);

@@ -12,6 +12,16 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p)
     return (uint32_t)__cvta_generic_to_shared(p);
 }
 
+// True in one thread of a (whole) warp; the compiler then knows that the
+// branch has a single thread and keeps the operands of copies and products in
+// uniform registers.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
+}
+
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -58,12 +68,13 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar)
         asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// One poll; the thread sleeps up to about 2 us in it.
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;"
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;"
                  " selp.u32 %0, 1, 0, p; }"
-                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+                 : "=r"(ok) : "r"(bar), "r"(parity), "r"(2000) : "memory");
     return ok != 0;
 }
 
@@ -79,7 +90,7 @@ __device__ __forceinline__ void registers_down()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-constexpr int kWaitLimit = 1 << 23;  // polls, each of which may sleep: a second or more
+constexpr int kWaitLimit = 1 << 20;  // polls: at most about two seconds asleep
 
 // Waits for a barrier's phase; false when the polls run out or another role of
 // the CTA has given up (*gave_up, in shared memory).
@@ -90,7 +101,7 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     for (int i = 0; i < kWaitLimit; ++i) {
         if (bar_try(bar, parity))
             return true;
-        if ((i & 63) == 63 && *gave_up)
+        if (*gave_up)
             return false;
     }
     *gave_up = 1;
@@ -130,6 +141,19 @@ __device__ __forceinline__ void tma_add(const void *map, int32_t x, int32_t y, u
 {
     asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%1, %2}], [%3];"
                  ::"l"(map), "r"(x), "r"(y), "r"(src) : "memory");
+}
+
+// 4 bytes from global to shared memory without a register in between (zero where
+// `there` is false: nothing is read then), in groups of this thread.
+__device__ __forceinline__ void copy4(uint32_t dst, const float *src, bool there)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
@@ -213,59 +237,28 @@ __device__ __forceinline__ void mma_commit(uint32_t bar)
                      " [%0], %1;" ::"r"(bar), "h"((uint16_t)3) : "memory");
 }
 
-// 16 neighbouring columns of this thread's lane (the warp's 32 lanes together).
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t r[16])
+// 32 neighbouring columns of this thread's lane (the warp's 32 lanes together).
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t r[32])
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11,"
-                 " %12, %13, %14, %15}, [%16];"
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11,"
+                 " %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29,"
+                 " %30, %31}, [%32];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
                    "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-                   "=r"(r[14]), "=r"(r[15])
+                   "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+                   "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+                   "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
                  : "r"(addr));
 }
 
-// The loads so far are in their registers.  The registers pass through, so
-// that no use of them is moved ahead of the wait.
-__device__ __forceinline__ void tmem_wait(uint32_t r[16])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
-                   "+r"(r[14]), "+r"(r[15])
-                 :: "memory");
-}
+// The loads so far are in their registers; their first uses are volatile too
+// (scale_add), so none is moved ahead of this.
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// ------------------------------------------------------------------ pairs of fp32
-
-__device__ __forceinline__ uint64_t pack2(float a, float b)
+// acc += part * s, not moved ahead of the wait for `part`
+__device__ __forceinline__ void scale_add(float &acc, uint32_t part, float s)
 {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t x)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
+    asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(part)), "f"(s));
 }
 
 // A barrier among `count` threads; true where any of them passes `x`.
