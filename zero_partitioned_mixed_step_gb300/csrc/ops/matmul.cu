@@ -31,14 +31,10 @@ constexpr int kHead = 4096;        // bytes of the workspace ahead of the partia
 constexpr int kCounters = 256;     // offset of the tiles' counters (zero between calls)
 constexpr int kPlanSms = 152;      // the rule for splitting k counts on a GB300's SMs
 constexpr int kStage = 16 * 1024;  // bytes of one staging buffer of the output
-// The scales come through a ring in shared memory, kAhead blocks of k ahead
-// of their use, by a warp of their own.  (Loads into the epilogue threads'
-// registers two blocks ahead were waited for at every block: 1350 cycles a
-// block where the products take 512.)  A slot is written again when the sums
-// of the block three later (kRing - kAhead - 2) are complete: the products of
-// that block waited for every epilogue warp to have taken the sums of the block
-// after the slot's, so all are done with the slot's scales.
-constexpr int kRing = 8, kAhead = 3;
+// The scales come through a ring in shared memory, by a warp of their own, in
+// groups of four blocks of k.  (Loads into the epilogue threads' registers two
+// blocks ahead were waited for at every block: 1350 cycles a block.)
+constexpr int kGroup = 4, kGroups = 3;
 
 struct MatmulParams {
     const float *sa, *sb;
@@ -59,11 +55,12 @@ struct Shape {
     // copying one can give some of its own (168 x 384 = 216 x 256 + 72 x 128)
     static constexpr int kThreads = NH == 1 ? 224 : 384;
     static constexpr int kTileM = 128 * CG, kTileN = 128 * NH;
-    static constexpr int kRowsB = 128 / CG;  // of each 128 columns, in one CTA
+    static constexpr int kRowsB = 128 / CG;  // of each 128 rows of B, in one CTA
     static constexpr int kBytesA = 128 * 128, kBytesB = NH * kRowsB * 128;
     static constexpr int kStageBytes = kBytesA + kBytesB;
     static constexpr int kStages = (224 * 1024 - NH * 2 * kStage - 4096) / kStageBytes;
-    static constexpr int kColumns = 256 * NH;  // of tensor memory
+    static constexpr int kBufs = NH == 1 ? 4 : 2;               // sums of 128 x 128 for each group
+    static constexpr int kColumns = 128 * NH * kBufs;           // of tensor memory: all of it
     static constexpr int kSmem = 1024 + kStages * kStageBytes + NH * 2 * kStage;
 };
 
@@ -226,8 +223,10 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
     constexpr int kStages = S::kStages;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
-    __shared__ __align__(8) uint64_t sum_full[NH][2], sum_empty[NH][2], drain_bar;
-    __shared__ __align__(16) float scale_a[kRing][128], scale_b[kRing][TILE_B ? NH : NH * 128];
+    __shared__ __align__(8) uint64_t sum_full[NH][S::kBufs], sum_empty[NH][S::kBufs], drain_bar[NH];
+    __shared__ __align__(8) uint64_t scale_full[kGroups], scale_empty[kGroups];
+    __shared__ __align__(16) float scale_a[kGroups][kGroup][128];
+    __shared__ __align__(16) float scale_b[kGroups][kGroup][TILE_B ? NH : NH * 128];
     __shared__ uint32_t tmem_sh;
     __shared__ int gave_up_sh, last_sh;
     volatile int *gave_up = &gave_up_sh;
@@ -240,14 +239,19 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
         gave_up_sh = 0;
         for (int i = 0; i < kStages; ++i) {
             bar_init(smem_u32(&full_bar[i]), 1);
-            bar_init(smem_u32(&empty_bar[i]), 1);
+            bar_init(smem_u32(&empty_bar[i]), NH);
         }
-        for (int h = 0; h < NH; ++h)
-            for (int i = 0; i < 2; ++i) {
-                bar_init(smem_u32(&sum_full[h][i]), 2);  // the products, the scales
+        for (int i = 0; i < S::kBufs; ++i)
+            for (int h = 0; h < NH; ++h) {
+                bar_init(smem_u32(&sum_full[h][i]), 1);
                 bar_init(smem_u32(&sum_empty[h][i]), 4 * CG);
             }
-        bar_init(smem_u32(&drain_bar), 1);
+        for (int i = 0; i < kGroups; ++i) {
+            bar_init(smem_u32(&scale_full[i]), 1);
+            bar_init(smem_u32(&scale_empty[i]), 4 * NH);
+        }
+        for (int h = 0; h < NH; ++h)
+            bar_init(smem_u32(&drain_bar[h]), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 4 * NH + 1)
@@ -304,104 +308,104 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
                             break;
                 }
         }
-        } else if (warp == 4 * NH + 1) {
+        } else if (warp == 4 * NH + 1 || warp == 4 * NH + 3) {
         // ---------------------------------------------------------- products
+        // A warp for each half of the tile's columns: a poll of a barrier takes
+        // about 150 cycles, and one thread's polls for both halves took 790 a
+        // block.  (With one half there is no fourth warp.)
+        const int h = warp == 4 * NH + 1 ? 0 : 1;
         if (rank == 0 && elect_one()) {
+            const uint32_t instr = p.instr, sums = smem_u32(&sum_full[h][0]), frees = smem_u32(&sum_empty[h][0]);
             int st = 0, buf = 0;
             uint32_t phase = 0, free_phase = 1;
             bool ok = true;
             for (int u = first; ok && u < units; u += step) {
                 const Unit w = unit_of(p, u);
-                for (int kb = w.kb0; ok && kb < w.kb1; ++kb) {
-                    if (!(ok = bar_wait(smem_u32(&full_bar[st]), phase, gave_up)))
+                for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                    const bool full = bar_test(smem_u32(&full_bar[st]), phase);
+                    const bool free = bar_test(frees + buf * 8, free_phase);
+                    ok = (full || bar_wait(smem_u32(&full_bar[st]), phase, gave_up)) &&
+                         (free || bar_wait(frees + buf * 8, free_phase, gave_up));
+                    if (!ok)
                         break;
-                    const uint32_t a = smem_u32(smem + st * S::kStageBytes), b = a + S::kBytesA;
+                    fence_after();
+                    const uint32_t a = smem_u32(smem + st * S::kStageBytes);
+                    const uint64_t da = smem_desc(a), db = smem_desc(a + S::kBytesA + h * S::kRowsB * 128);
 #pragma unroll
-                    for (int h = 0; h < NH; ++h) {
-                        if (!(ok = bar_wait(smem_u32(&sum_empty[h][buf]), free_phase, gave_up)))
-                            break;
-                        fence_after();
-                        const uint64_t da = smem_desc(a), db = smem_desc(b + h * S::kRowsB * 128);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f8<CG>(tmem + (buf * NH + h) * 128, da + k * 2, db + k * 2, p.instr, k > 0);
-                        mma_commit<CG>(smem_u32(&sum_full[h][buf]));
-                    }
-                    if (ok)
-                        mma_commit<CG>(smem_u32(&empty_bar[st]));
+                    for (int k = 0; k < 4; ++k)
+                        mma_f8<CG>(tmem + (buf * NH + h) * 128, da + k * 2, db + k * 2, instr, k > 0);
+                    mma_commit<CG>(sums + buf * 8);
+                    mma_commit<CG>(smem_u32(&empty_bar[st]));
                     if (++st == kStages) {
                         st = 0;
                         phase ^= 1;
                     }
-                    buf ^= 1;
-                    free_phase ^= buf == 0;
+                    if (++buf == S::kBufs) {
+                        buf = 0;
+                        free_phase ^= 1;
+                    }
                 }
             }
             if (!ok) {  // products in flight end before tensor memory is freed
-                mma_commit<CG>(smem_u32(&drain_bar));
+                mma_commit<CG>(smem_u32(&drain_bar[h]));
                 for (int k = 0; k < kWaitLimit; ++k)
-                    if (bar_try(smem_u32(&drain_bar), 0))
+                    if (bar_try(smem_u32(&drain_bar[h]), 0))
                         break;
             }
         }
         } else if (warp == 4 * NH + 2) {
         // ---------------------------------------------------------- scales
-        auto copy_scales = [&](const Walk &k, int slot) {
-            if (k.more) {
+        int slot = 0;
+        uint32_t phase = 1;
+        Walk k(p, first);
+        while (k.more) {
+            if (!bar_wait_warp(smem_u32(&scale_empty[slot]), phase, gave_up))
+                break;
+            for (int i = 0; i < kGroup && k.more; ++i, k.next(p, step)) {
                 const float *sa = p.sa + k.kb * p.ldsa, *sb = p.sb + k.kb * p.ldsb;
                 const int row = k.w.m * S::kTileM + (int)rank * 128 + lane;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    copy4(smem_u32(&scale_a[slot][i * 32 + lane]), row + i * 32 < p.m ? sa + row + i * 32 : p.sa,
-                          row + i * 32 < p.m);
+                for (int j = 0; j < 4; ++j)
+                    copy4(smem_u32(&scale_a[slot][i][j * 32 + lane]), row + j * 32 < p.m ? sa + row + j * 32 : p.sa,
+                          row + j * 32 < p.m);
                 if (TILE_B) {
                     const int col = k.w.n * NH + lane;
                     if (lane < NH)
-                        copy4(smem_u32(&scale_b[slot][lane]), col * 128 < p.n ? sb + col : p.sb, col * 128 < p.n);
+                        copy4(smem_u32(&scale_b[slot][i][lane]), col * 128 < p.n ? sb + col : p.sb, col * 128 < p.n);
                 } else {
                     const int col = k.w.n * S::kTileN + lane;
 #pragma unroll
-                    for (int i = 0; i < 4 * NH; ++i)
-                        copy4(smem_u32(&scale_b[slot][i * 32 + lane]), col + i * 32 < p.n ? sb + col + i * 32 : p.sb,
-                              col + i * 32 < p.n);
+                    for (int j = 0; j < 4 * NH; ++j)
+                        copy4(smem_u32(&scale_b[slot][i][j * 32 + lane]),
+                              col + j * 32 < p.n ? sb + col + j * 32 : p.sb, col + j * 32 < p.n);
                 }
             }
             copy_commit();
-        };
-        Walk use(p, first), load(p, first);
-        for (int i = 0; i < kAhead; ++i, load.next(p, step))
-            copy_scales(load, i);
-        int slot = 0, buf = 0;
-        uint32_t phase = 1;  // of the block that had this buffer before
-        for (; use.more; use.next(p, step)) {
-            copy_wait<kAhead - 1>();
-            bool ok = true;
-            for (int h = 0; h < NH; ++h)
-                ok = ok && bar_wait_warp(smem_u32(&sum_full[h][buf]), phase, gave_up);
-            if (!ok)
-                break;
+            copy_wait<0>();
             __syncwarp();
             if (lane == 0)
-                for (int h = 0; h < NH; ++h)
-                    bar_arrive<1>(smem_u32(&sum_full[h][buf]));
-            copy_scales(load, (slot + kAhead) % kRing);
-            load.next(p, step);
-            slot = (slot + 1) % kRing;
-            buf ^= 1;
-            phase ^= buf == 0;
+                bar_arrive<1>(smem_u32(&scale_full[slot]));
+            if (++slot == kGroups) {
+                slot = 0;
+                phase ^= 1;
+            }
         }
         }
     } else {
         if (NH == 2)
             registers_up<216>();
-        // ---------------------------------------------------------- scales and output
+        // ---------------------------------------------------------- scaled sums and output
         const int h = warp >> 2, quad = warp & 3, t = threadIdx.x & 127, id = 1 + h;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         uint8_t *stage = staging + h * 2 * kStage;
-        int buf = 0;
-        uint32_t phase = 0;
+        const uint32_t full = smem_u32(&sum_full[h][0]), scale_there = smem_u32(&scale_full[0]);
+        const uint32_t scale_free = smem_u32(&scale_empty[0]);
+        uint32_t free = smem_u32(&sum_empty[h][0]);
+        if (CG == 2)
+            free = map_to(free, 0);
+        int buf = 0, slot = 0, in_group = 0;
+        uint32_t phase = 0, scale_phase = 0;
         bool ok = true;
-        int slot = 0;
         for (int u = first; u < units; u += step) {
             const Unit w = unit_of(p, u);
             const int m0 = w.m * S::kTileM + (int)rank * 128, n0 = w.n * S::kTileN + h * 128;
@@ -410,36 +414,72 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 128; ++i)
                 acc[i] = 0.0f;
+            // Per block: 4 x 32 columns through two register buffers.  (Loading
+            // the next block's first columns ahead of the loop's end keeps
+            // them in registers over it, and the compiler copies them there.)
+            uint32_t r[2][32];
+            auto column = [&](int c) { return lanes + (uint32_t)((buf * NH + h) * 128 + c * 32); };
+            bool ready = false;
             for (int kb = w.kb0; kb < w.kb1; ++kb) {
-                if (!(ok = bar_wait_warp(smem_u32(&sum_full[h][buf]), phase, gave_up)))
+                if (!ready)
+                    ok = bar_wait_warp(full + buf * 8, phase, gave_up) &&
+                         (in_group != 0 || bar_wait_warp(scale_there + slot * 8, scale_phase, gave_up));
+                if (!ok)
                     break;
                 fence_after();
-                const uint32_t from = lanes + (uint32_t)((buf * NH + h) * 128);
-                uint32_t r[2][32];
-                tmem_ld32(from, r[0]);
-                const float ab = TILE_B ? scale_a[slot][t] * scale_b[slot][h] : scale_a[slot][t];
-                const float *sb = &scale_b[slot][TILE_B ? 0 : h * 128];
+                tmem_ld32(column(0), r[0]);
+                tmem_ld32(column(1), r[1]);
+                // the block's scale of this thread's row (times the tile's)
+                const float ab = TILE_B ? scale_a[slot][in_group][t] * scale_b[slot][in_group][h]
+                                        : scale_a[slot][in_group][t];
+                const float4 *sb = reinterpret_cast<const float4 *>(&scale_b[slot][in_group][TILE_B ? 0 : h * 128]);
+                auto add = [&](int c) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_wait();
-                    if (c < 3) {
-                        tmem_ld32(from + (c + 1) * 32, r[(c + 1) & 1]);
-                    } else {
-                        fence_before();
-                        if (lane == 0) {
-                            uint32_t bar = smem_u32(&sum_empty[h][buf]);
-                            if (CG == 2)
-                                bar = map_to(bar, 0);
-                            bar_arrive<CG>(bar);
+                    for (int i = 0; i < 8; ++i) {
+                        float *o = acc + c * 32 + i * 4;
+                        const uint32_t *x = r[c & 1] + i * 4;
+                        if (TILE_B) {
+                            scale_add(o[0], x[0], ab);
+                            scale_add(o[1], x[1], ab);
+                            scale_add(o[2], x[2], ab);
+                            scale_add(o[3], x[3], ab);
+                        } else {
+                            const float4 s = sb[c * 8 + i];
+                            const float2 lo = mul2(ab, s.x, s.y), hi = mul2(ab, s.z, s.w);
+                            scale_add(o[0], x[0], lo.x);
+                            scale_add(o[1], x[1], lo.y);
+                            scale_add(o[2], x[2], hi.x);
+                            scale_add(o[3], x[3], hi.y);
                         }
                     }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        scale_add(acc[c * 32 + i], r[c & 1][i], TILE_B ? ab : ab * sb[c * 32 + i]);
+                };
+                const int next_buf = buf + 1 == S::kBufs ? 0 : buf + 1;
+                const uint32_t next_phase = phase ^ (next_buf == 0);
+                const int next_slot = slot + 1 == kGroups ? 0 : slot + 1;
+                const uint32_t next_scale_phase = scale_phase ^ (next_slot == 0);
+                const bool group_ends = in_group + 1 == kGroup;
+                tmem_wait();
+                add(0);
+                tmem_ld32(column(2), r[0]);
+                add(1);
+                tmem_ld32(column(3), r[1]);
+                tmem_wait();
+                fence_before();
+                bar_arrive_lane0<CG>(free + buf * 8, lane);
+                const bool peek = bar_test(full + next_buf * 8, next_phase) &&
+                                  (!group_ends || bar_test(scale_there + next_slot * 8, next_scale_phase));
+                add(2);
+                add(3);
+                ready = __all_sync(0xFFFFFFFFu, peek);
+                if (group_ends) {
+                    __syncwarp();
+                    bar_arrive_lane0<1>(scale_free + slot * 8, lane);
+                    slot = next_slot;
+                    scale_phase = next_scale_phase;
                 }
-                slot = (slot + 1) % kRing;
-                buf ^= 1;
-                phase ^= buf == 0;
+                in_group = group_ends ? 0 : in_group + 1;
+                buf = next_buf;
+                phase = next_phase;
             }
             if (barrier_or(id, 128, !ok)) {
                 ok = false;

@@ -68,13 +68,35 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar)
         asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// The same by the one thread of a warp that passes lane 0, without a branch.
+template <int CG>
+__device__ __forceinline__ void bar_arrive_lane0(uint32_t bar, int lane)
+{
+    if (CG == 1)
+        asm volatile("{ .reg .pred p; setp.eq.s32 p, %1, 0; @p mbarrier.arrive.shared::cta.b64 _, [%0]; }" ::"r"(bar),
+                     "r"(lane) : "memory");
+    else
+        asm volatile("{ .reg .pred p; setp.eq.s32 p, %1, 0; @p mbarrier.arrive.shared::cluster.b64 _, [%0]; }" ::"r"(bar),
+                     "r"(lane) : "memory");
+}
+
 // One poll; the thread sleeps up to about 2 us in it.
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;"
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;"
                  " selp.u32 %0, 1, 0, p; }"
-                 : "=r"(ok) : "r"(bar), "r"(parity), "r"(2000) : "memory");
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+
+// The same without sleeping.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;"
+                 " selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
 
@@ -96,8 +118,6 @@ constexpr int kWaitLimit = 1 << 20;  // polls: at most about two seconds asleep
 // the CTA has given up (*gave_up, in shared memory).
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up)
 {
-    if (bar_try(bar, parity))
-        return true;
     for (int i = 0; i < kWaitLimit; ++i) {
         if (bar_try(bar, parity))
             return true;
@@ -259,6 +279,14 @@ __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.syn
 __device__ __forceinline__ void scale_add(float &acc, uint32_t part, float s)
 {
     asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(part)), "f"(s));
+}
+
+__device__ __forceinline__ float2 mul2(float s, float a, float b)  // (s a, s b) in one instruction
+{
+    float2 r;
+    asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %2}; mov.b64 y, {%3, %4}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+        : "=f"(r.x), "=f"(r.y) : "f"(s), "f"(a), "f"(b));
+    return r;
 }
 
 // A barrier among `count` threads; true where any of them passes `x`.
