@@ -21,6 +21,7 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "ops.cuh"
 #include "tcgen05.cuh"
@@ -72,15 +73,21 @@ struct Unit {
 __device__ __forceinline__ Unit unit_of(const MatmulParams &p, int u)
 {
     Unit r;
-    r.split = u % p.splits;
-    r.tile = u / p.splits;
-    constexpr int kGroup = 8;
-    const int per = kGroup * p.tiles_n, g = r.tile / per, in = r.tile % per;
-    const int rows = min(kGroup, p.tiles_m - g * kGroup);
-    r.m = g * kGroup + in % rows;
+    r.split = 0;
+    r.tile = u;
+    r.kb0 = 0;
+    r.kb1 = p.kb;
+    if (p.splits > 1) {  // (32 bits: kb < 2^24, splits <= 152; a 64-bit division takes 500 cycles)
+        r.split = u % p.splits;
+        r.tile = u / p.splits;
+        r.kb0 = (int)((uint32_t)p.kb * (uint32_t)r.split / (uint32_t)p.splits);
+        r.kb1 = (int)((uint32_t)p.kb * (uint32_t)(r.split + 1) / (uint32_t)p.splits);
+    }
+    constexpr int kRows = 8;
+    const int per = kRows * p.tiles_n, g = r.tile / per, in = r.tile - g * per;
+    const int rows = min(kRows, p.tiles_m - g * kRows);
     r.n = in / rows;
-    r.kb0 = (int)((int64_t)p.kb * r.split / p.splits);
-    r.kb1 = (int)((int64_t)p.kb * (r.split + 1) / p.splits);
+    r.m = g * kRows + in - r.n * rows;
     return r;
 }
 
@@ -146,8 +153,9 @@ __device__ __forceinline__ uint4 pack16<f16>(const float *acc)
 }
 
 // 128 rows x 128 columns of sums (a thread one row) to the output by TMA
-// stores (or reductions), through two staging buffers of 128 bytes a row.
-// `id`: the group's barrier.
+// stores (or reductions), two staging buffers of 128 bytes a row at a time.
+// `id`: the group's barrier, which its threads have passed since thread 0 saw
+// the buffers' last stores done reading.
 template <class T>
 __device__ __forceinline__ void write_tma(const MatmulParams &p, const void *map, const float acc[128],
                                           uint8_t *stage, int id, int t, int m0, int n0)
@@ -155,40 +163,88 @@ __device__ __forceinline__ void write_tma(const MatmulParams &p, const void *map
     constexpr int kCols = 128 / (int)sizeof(T);  // columns of one staging buffer
     constexpr int kPiece = 16 / (int)sizeof(T);  // sums in 16 bytes
 #pragma unroll
-    for (int c = 0; c < 128 / kCols; ++c) {
-        uint8_t *buf = stage + (c & 1) * kStage;
-        const int x = n0 + c * kCols;
-        if (t == 0)
-            bulk_wait_read<1>();  // this buffer's last store has read it
-        barrier_of(id, 128);
+    for (int c = 0; c < 128 / kCols; c += 2) {
+        if (c > 0) {
+            if (t == 0)
+                bulk_wait_read<0>();
+            barrier_of(id, 128);
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            stage16(buf, t, i, pack16<T>(acc + (c * 8 + i) * kPiece));
+        for (int i = 0; i < 16; ++i)
+            stage16(stage + (i >> 3) * kStage, t, i & 7, pack16<T>(acc + (c * 8 + i) * kPiece));
         fence_async_shared();
         barrier_of(id, 128);
         if (t == 0) {
-            if (x < p.n && m0 < p.m) {
-                if (p.add)
-                    tma_add(map, x, m0, smem_u32(buf));
-                else
-                    tma_store(map, x, m0, smem_u32(buf));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int x = n0 + (c + i) * kCols;
+                if (x < p.n && m0 < p.m) {
+                    if (p.add)
+                        tma_add(map, x, m0, smem_u32(stage + i * kStage));
+                    else
+                        tma_store(map, x, m0, smem_u32(stage + i * kStage));
+                }
             }
             bulk_commit();
         }
     }
 }
 
-// The same element by element, neighbouring threads side by side, for rows
-// that no TMA store can write and for sums added in a half type; staged in
-// fp32, so that the sum with the old value is rounded once.
+// The same for rows that no TMA store can write (their starts are not on
+// 16-byte boundaries): the staged rows leave in the destination's own 16-byte
+// pieces, each gathered from the staging buffers, the ends element by element.
 template <class T>
-__device__ __forceinline__ void write_direct(const MatmulParams &p, const float acc[128], uint8_t *stage,
-                                             int id, int t, int m0, int n0)
+__device__ __forceinline__ void write_gather(const MatmulParams &p, const float acc[128], uint8_t *stage, int id,
+                                             int t, int m0, int n0)
+{
+    constexpr int kCols = 2 * kStage / 128 / (int)sizeof(T);  // columns staged at a time
+    constexpr int kPiece = 16 / (int)sizeof(T);
+    constexpr int kPieces = kCols / kPiece;  // of a row, and one more where the row starts inside a piece
+    constexpr int kPitch = kCols * (int)sizeof(T);
+#pragma unroll
+    for (int c = 0; c < 128; c += kCols) {
+        if (c > 0)
+            barrier_of(id, 128);  // the last readers are done
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            *reinterpret_cast<uint4 *>(stage + t * kPitch + ((i ^ (t & 7)) << 4)) = pack16<T>(acc + c + i * kPiece);
+        barrier_of(id, 128);
+        const int n = min(kCols, p.n - n0 - c);
+        for (int e = t; e < 128 * (kPieces + 1); e += 128) {
+            const int row = e / (kPieces + 1), piece = e - row * (kPieces + 1);
+            if (m0 + row >= p.m)
+                break;
+            T *o = static_cast<T *>(p.out) + (int64_t)(m0 + row) * p.ldo + n0 + c;
+            const int at = piece * kPiece - (int)(reinterpret_cast<uintptr_t>(o) / sizeof(T) % kPiece);
+            auto value = [&](int k) {
+                const int b = k * (int)sizeof(T);
+                return *reinterpret_cast<const T *>(stage + row * kPitch + (((b >> 4) ^ (row & 7)) << 4) + (b & 15));
+            };
+            if (at >= 0 && at + kPiece <= n) {
+                alignas(16) T v[kPiece];
+#pragma unroll
+                for (int k = 0; k < kPiece; ++k)
+                    v[k] = value(at + k);
+                *reinterpret_cast<uint4 *>(o + at) = *reinterpret_cast<const uint4 *>(v);
+            } else {
+                for (int k = max(at, 0); k < min(at + kPiece, n); ++k)
+                    o[k] = value(k);
+            }
+        }
+    }
+}
+
+// Sums added to old values that no TMA reduction can add (a half type, or rows
+// as above): staged in fp32, so that the sum is rounded once.
+template <class T>
+__device__ __forceinline__ void write_add(const MatmulParams &p, const float acc[128], uint8_t *stage, int id, int t,
+                                          int m0, int n0)
 {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         uint8_t *buf = stage + (c & 1) * kStage;
-        barrier_of(id, 128);  // its last readers are done
+        if (c > 0)
+            barrier_of(id, 128);  // its last readers are done
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             stage16(buf, t, i, pack16<float>(acc + (c * 8 + i) * 4));
@@ -199,7 +255,7 @@ __device__ __forceinline__ void write_direct(const MatmulParams &p, const float 
                 T *o = static_cast<T *>(p.out) + (int64_t)(m0 + row) * p.ldo + col;
                 const float v = *reinterpret_cast<const float *>(
                     buf + row * 128 + ((((t & 31) >> 2) ^ (row & 7)) << 4) + (t & 3) * 4);
-                *o = from_f32<T>(p.add ? to_f32(*o) + v : v);
+                *o = from_f32<T>(to_f32(*o) + v);
             }
     }
 }
@@ -210,8 +266,10 @@ __device__ __forceinline__ void write_tile(const MatmulParams &p, const void *ma
 {
     if (p.tma_out)
         write_tma<T>(p, map, acc, stage, id, t, m0, n0);
+    else if (p.add)
+        write_add<T>(p, acc, stage, id, t, m0, n0);
     else
-        write_direct<T>(p, acc, stage, id, t, m0, n0);
+        write_gather<T>(p, acc, stage, id, t, m0, n0);
 }
 
 template <int CG, int NH, bool TILE_B>
@@ -481,6 +539,8 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
                 buf = next_buf;
                 phase = next_phase;
             }
+            if (t == 0)
+                bulk_wait_read<0>();  // the staging buffers are free
             if (barrier_or(id, 128, !ok)) {
                 ok = false;
                 break;
@@ -536,6 +596,289 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
         atomicExch(p.error, 1);
 }
 
+// ------------------------------------------------------------------ few rows
+//
+// Up to 64 rows of a (single tokens): the weights' bytes are what counts.  The
+// roles of the operands change places, so that the 128 rows of a tensor-core
+// product are 128 rows of b and its columns the TN = 16, 32 or 64 rows of a:
+// a block's sums are TN columns of tensor memory (eight blocks of them in
+// flight) and TN registers of a thread.  Two CTAs to an SM, and k split so
+// that they fill the GPU.  16 x 4096 x 14336: 27 us with 128 columns, XX us here.
+template <int TN>
+struct Few {
+    static constexpr int kThreads = 224;
+    static constexpr int kBytesB = 128 * 128, kStageBytes = kBytesB + TN * 128;
+    static constexpr int kStages = 100 * 1024 / kStageBytes;
+    static constexpr int kBufs = TN == 64 ? 4 : 8;
+    static constexpr int kColumns = TN * kBufs;
+    static constexpr int kSmem = 1024 + kStages * kStageBytes;
+};
+
+template <int TN, bool TILE_B>
+__global__ void __launch_bounds__(Few<TN>::kThreads, 2)
+    matmul_few_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                      const __grid_constant__ MatmulParams p)
+{
+    using S = Few<TN>;
+    constexpr int kStages = S::kStages;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
+    __shared__ __align__(8) uint64_t sum_full[S::kBufs], sum_empty[S::kBufs], drain_bar;
+    __shared__ __align__(8) uint64_t scale_full[kGroups], scale_empty[kGroups];
+    __shared__ __align__(16) float scale_a[kGroups][kGroup][TN], scale_b[kGroups][kGroup][TILE_B ? 1 : 128];
+    __shared__ uint32_t tmem_sh;
+    __shared__ int gave_up_sh, last_sh;
+    volatile int *gave_up = &gave_up_sh;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        gave_up_sh = 0;
+        for (int i = 0; i < kStages; ++i) {
+            bar_init(smem_u32(&full_bar[i]), 1);
+            bar_init(smem_u32(&empty_bar[i]), 1);
+        }
+        for (int i = 0; i < S::kBufs; ++i) {
+            bar_init(smem_u32(&sum_full[i]), 1);
+            bar_init(smem_u32(&sum_empty[i]), 4);
+        }
+        for (int i = 0; i < kGroups; ++i) {
+            bar_init(smem_u32(&scale_full[i]), 1);
+            bar_init(smem_u32(&scale_empty[i]), 4);
+        }
+        bar_init(smem_u32(&drain_bar), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 5)
+        tmem_alloc<1>(smem_u32(&tmem_sh), S::kColumns);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_sh;
+    const int first = blockIdx.x, step = gridDim.x;  // unit_of: one row of tiles
+
+    if (warp == 4) {
+        // ---------------------------------------------------------- copies
+        if (elect_one()) {
+            int st = 0, issued = 0;
+            uint32_t phase = 1;
+            bool ok = true;
+            for (Walk k(p, first); k.more; k.next(p, step)) {
+                if (!(ok = bar_wait(smem_u32(&empty_bar[st]), phase, gave_up)))
+                    break;
+                const uint32_t b = smem_u32(smem + st * S::kStageBytes), full = smem_u32(&full_bar[st]);
+                bar_expect(full, S::kStageBytes);
+                tma_load<1>(b, &map_b, k.kb * 128, k.w.n * 128, full);
+                tma_load<1>(b + S::kBytesB, &map_a, k.kb * 128, 0, full);
+                issued = issued < kStages ? issued + 1 : kStages;
+                if (++st == kStages) {
+                    st = 0;
+                    phase ^= 1;
+                }
+            }
+            if (!ok)  // copies in flight land before the CTA ends
+                for (int i = 0; i < issued; ++i) {
+                    if (--st < 0) {
+                        st = kStages - 1;
+                        phase ^= 1;
+                    }
+                    for (int q = 0; q < kWaitLimit; ++q)
+                        if (bar_try(smem_u32(&full_bar[st]), phase ^ 1))
+                            break;
+                }
+        }
+    } else if (warp == 5) {
+        // ---------------------------------------------------------- products
+        if (elect_one()) {
+            int st = 0, buf = 0;
+            uint32_t phase = 0, free_phase = 1;
+            bool ok = true;
+            for (Walk k(p, first); k.more; k.next(p, step)) {
+                const bool full = bar_test(smem_u32(&full_bar[st]), phase);
+                const bool free = bar_test(smem_u32(&sum_empty[buf]), free_phase);
+                ok = (full || bar_wait(smem_u32(&full_bar[st]), phase, gave_up)) &&
+                     (free || bar_wait(smem_u32(&sum_empty[buf]), free_phase, gave_up));
+                if (!ok)
+                    break;
+                fence_after();
+                const uint32_t b = smem_u32(smem + st * S::kStageBytes);
+                const uint64_t db = smem_desc(b), da = smem_desc(b + S::kBytesB);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mma_f8<1>(tmem + buf * TN, db + i * 2, da + i * 2, p.instr, i > 0);
+                mma_commit<1>(smem_u32(&sum_full[buf]));
+                mma_commit<1>(smem_u32(&empty_bar[st]));
+                if (++st == kStages) {
+                    st = 0;
+                    phase ^= 1;
+                }
+                if (++buf == S::kBufs) {
+                    buf = 0;
+                    free_phase ^= 1;
+                }
+            }
+            if (!ok) {  // products in flight end before tensor memory is freed
+                mma_commit<1>(smem_u32(&drain_bar));
+                for (int q = 0; q < kWaitLimit; ++q)
+                    if (bar_try(smem_u32(&drain_bar), 0))
+                        break;
+            }
+        }
+    } else if (warp == 6) {
+        // ---------------------------------------------------------- scales
+        int slot = 0;
+        uint32_t phase = 1;
+        Walk k(p, first);
+        while (k.more) {
+            if (!bar_wait_warp(smem_u32(&scale_empty[slot]), phase, gave_up))
+                break;
+            for (int i = 0; i < kGroup && k.more; ++i, k.next(p, step)) {
+                const float *sa = p.sa + k.kb * p.ldsa, *sb = p.sb + k.kb * p.ldsb;
+                for (int j = lane; j < TN; j += 32)
+                    copy4(smem_u32(&scale_a[slot][i][j]), j < p.m ? sa + j : p.sa, j < p.m);
+                if (TILE_B) {
+                    if (lane == 0)
+                        copy4(smem_u32(&scale_b[slot][i][0]), sb + k.w.n, true);
+                } else {
+                    const int row = k.w.n * 128 + lane;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        copy4(smem_u32(&scale_b[slot][i][j * 32 + lane]), row + j * 32 < p.n ? sb + row + j * 32 : p.sb,
+                              row + j * 32 < p.n);
+                }
+            }
+            copy_commit();
+            copy_wait<0>();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive<1>(smem_u32(&scale_full[slot]));
+            if (++slot == kGroups) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+    } else {
+        // ---------------------------------------------------------- scaled sums and output
+        const int t = threadIdx.x;
+        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        int buf = 0, slot = 0, in_group = 0;
+        uint32_t phase = 0, scale_phase = 0;
+        bool ok = true;
+        for (int u = first; u < p.units; u += step) {
+            const Unit w = unit_of(p, u);
+            const int row = w.n * 128 + t;  // of b, a column of the output
+            float acc[TN];
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+                acc[i] = 0.0f;
+            for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                if (in_group == 0)
+                    ok = bar_wait_warp(smem_u32(&scale_full[slot]), scale_phase, gave_up);
+                ok = ok && bar_wait_warp(smem_u32(&sum_full[buf]), phase, gave_up);
+                if (!ok)
+                    break;
+                fence_after();
+                const float b = scale_b[slot][in_group][TILE_B ? 0 : t];
+                const float4 *sa = reinterpret_cast<const float4 *>(scale_a[slot][in_group]);
+                constexpr int kLoad = TN < 32 ? 16 : 32;
+#pragma unroll
+                for (int c = 0; c < TN; c += kLoad) {
+                    uint32_t r[kLoad];
+                    if (kLoad == 16)
+                        tmem_ld16(lanes + (uint32_t)(buf * TN + c), r);
+                    else
+                        tmem_ld32(lanes + (uint32_t)(buf * TN + c), r);
+                    tmem_wait();
+                    if (c + kLoad == TN) {
+                        fence_before();
+                        bar_arrive_lane0<1>(smem_u32(&sum_empty[buf]), lane);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kLoad; i += 4) {
+                        const float4 s = sa[(c + i) / 4];
+                        const float2 lo = mul2(b, s.x, s.y), hi = mul2(b, s.z, s.w);
+                        scale_add(acc[c + i], r[i], lo.x);
+                        scale_add(acc[c + i + 1], r[i + 1], lo.y);
+                        scale_add(acc[c + i + 2], r[i + 2], hi.x);
+                        scale_add(acc[c + i + 3], r[i + 3], hi.y);
+                    }
+                }
+                if (++in_group == kGroup) {
+                    in_group = 0;
+                    __syncwarp();
+                    bar_arrive_lane0<1>(smem_u32(&scale_empty[slot]), lane);
+                    if (++slot == kGroups) {
+                        slot = 0;
+                        scale_phase ^= 1;
+                    }
+                }
+                if (++buf == S::kBufs) {
+                    buf = 0;
+                    phase ^= 1;
+                }
+            }
+            if (barrier_or(1, 128, !ok)) {
+                ok = false;
+                break;
+            }
+            if (p.splits > 1) {
+                // this part's sums to the workspace; the tile's last part adds
+                // all of them in ascending order
+                float *mine = p.parts + ((int64_t)w.tile * p.splits + w.split) * (TN * 128) + t;
+#pragma unroll
+                for (int i = 0; i < TN; ++i)
+                    if (i < p.m)
+                        __stcg(mine + i * 128, acc[i]);
+                __threadfence();
+                barrier_of(1, 128);
+                if (t == 0) {
+                    last_sh = atomicAdd(p.counters + w.tile, 1u) == (uint32_t)p.splits - 1;
+                    __threadfence();
+                }
+                barrier_of(1, 128);
+                if (!last_sh)
+                    continue;
+                const float *all = p.parts + (int64_t)w.tile * p.splits * (TN * 128) + t;
+#pragma unroll
+                for (int i = 0; i < TN; ++i)
+                    acc[i] = 0.0f;
+                for (int s = 0; s < p.splits; ++s, all += TN * 128)
+#pragma unroll
+                    for (int i = 0; i < TN; ++i)
+                        if (i < p.m)
+                            acc[i] += __ldcg(all + i * 128);
+                if (t == 0)
+                    p.counters[w.tile] = 0;
+            }
+            if (row < p.n) {
+                auto put = [&](auto *o) {
+                    using T = std::remove_reference_t<decltype(*o)>;
+#pragma unroll
+                    for (int i = 0; i < TN; ++i)
+                        if (i < p.m) {
+                            T *at = o + (int64_t)i * p.ldo + row;
+                            *at = from_f32<T>(p.add ? to_f32(*at) + acc[i] : acc[i]);
+                        }
+                };
+                if (p.out_type == ZERO_T_BF16)
+                    put(static_cast<bf16 *>(p.out));
+                else if (p.out_type == ZERO_T_F16)
+                    put(static_cast<f16 *>(p.out));
+                else
+                    put(static_cast<float *>(p.out));
+            }
+        }
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 5)
+        tmem_free<1>(tmem, S::kColumns);
+    if (threadIdx.x == 0 && gave_up_sh)
+        atomicExch(p.error, 1);
+}
+
 // ------------------------------------------------------------------ host
 
 using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
@@ -574,32 +917,38 @@ static int encode(CUtensorMap *map, CUtensorMapDataType type, int bytes, const v
     return r == CUDA_SUCCESS ? ZERO_OK : ZERO_EINVAL;
 }
 
-// How a product is cut: pairs of CTAs on 256x256 tiles where there are enough
-// of them for the SMs, else single CTAs on 128x128 tiles with k split so that
-// the parts fill the SMs.
+// How a product is cut: up to 64 rows, tiles of 128 rows of b with all of a's;
+// else pairs of CTAs on 256x256 tiles where there are enough of them for the
+// SMs; else single CTAs on 128x128 tiles.  Where the tiles are few, k is split
+// so that the parts fill the SMs (two CTAs to an SM with few rows).
 struct Plan {
+    int few;  // columns of the few-rows kernel's tiles, or 0
     bool pair;
     int64_t tiles_m, tiles_n;
     int splits;
+    int64_t part;  // elements of a part's sums
 };
 static Plan plan_of(int64_t m, int64_t n, int64_t k)
 {
     Plan r{};
     const int64_t kb = ceil_div(k, kBlock);
-    if (ceil_div(m, 256) * ceil_div(n, 256) >= kPlanSms / 2) {
+    r.splits = 1;
+    if (m > 64 && ceil_div(m, 256) * ceil_div(n, 256) >= kPlanSms / 2) {
         r.pair = true;
         r.tiles_m = ceil_div(m, 256);
         r.tiles_n = ceil_div(n, 256);
-        r.splits = 1;
         return r;
     }
-    r.tiles_m = ceil_div(m, 128);
+    r.few = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 0;
+    r.tiles_m = r.few ? 1 : ceil_div(m, 128);
     r.tiles_n = ceil_div(n, 128);
+    r.part = (int64_t)(r.few ? r.few : 128) * 128;
     const int64_t tiles = r.tiles_m * r.tiles_n;
-    int64_t s = kPlanSms / tiles;
+    int64_t s = (r.few ? 2 : 1) * kPlanSms / tiles;
     if (s > kb / 4)  // a part is worth its sums' way through memory from four blocks on
         s = kb / 4;
-    r.splits = (int)(s < 1 ? 1 : s);
+    if (s > 1)
+        r.splits = (int)s;
     return r;
 }
 
@@ -629,6 +978,20 @@ static int launch_matmul(const CUtensorMap &a, const CUtensorMap &b, const CUten
     return e == cudaSuccess ? launch_status() : cuda_error(e);
 }
 
+template <int TN>
+static int launch_few(const CUtensorMap &a, const CUtensorMap &b, const MatmulParams &p, bool tile_b,
+                      cudaStream_t stream)
+{
+    using S = Few<TN>;
+    auto kernel = tile_b ? matmul_few_kernel<TN, true> : matmul_few_kernel<TN, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess)
+        return cuda_error(e);
+    const int most = 2 * device_sms();
+    kernel<<<p.units < most ? p.units : most, S::kThreads, S::kSmem, stream>>>(a, b, p);
+    return launch_status();
+}
+
 }  // namespace zo
 
 using namespace zo;
@@ -640,8 +1003,8 @@ size_t zero_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k)
     if (bad_dim(m) || bad_dim(n) || bad_dim(k))
         return 0;
     const Plan plan = plan_of(m, n, k);
-    return (size_t)kHead + (plan.splits > 1 ? (size_t)(plan.tiles_m * plan.tiles_n * plan.splits) * 128 * 128 * 4
-                                            : 0);
+    return (size_t)kHead +
+           (plan.splits > 1 ? (size_t)(plan.tiles_m * plan.tiles_n * plan.splits * plan.part) * sizeof(float) : 0);
 }
 
 int zero_fp8_matmul(const void *a, int a_type, int64_t lda, const float *sa, int64_t ldsa,
@@ -699,20 +1062,27 @@ int zero_fp8_matmul(const void *a, int a_type, int64_t lda, const float *sa, int
     p.units = (int32_t)units;
     p.out_type = out_type;
     p.add = add ? 1 : 0;
-    p.instr = f8_instr(a_type == ZERO_T_E5M2, b_type == ZERO_T_E5M2, plan.pair ? 256 : 128, 128);
+    const int fa = a_type == ZERO_T_E5M2, fb = b_type == ZERO_T_E5M2;
+    p.instr = plan.few ? f8_instr(fb, fa, 128, plan.few) : f8_instr(fa, fb, plan.pair ? 256 : 128, 128);
     // a TMA store (or reduction) of whole boxes; half types are added in fp32 and rounded once
     p.tma_out = rows_aligned(out, ldo, ob, 16) && (!add || out_type == ZERO_T_F32);
     CUtensorMap ma, mb, mo{};
-    rc = encode(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a, m, k, lda, 128);
+    rc = encode(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a, m, k, lda, plan.few ? plan.few : 128);
     if (!rc)
         rc = encode(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, b, n, k, ldb, plan.pair ? 64 : 128);
-    if (!rc && p.tma_out)
+    if (!rc && p.tma_out && !plan.few)
         rc = encode(&mo, out_type == ZERO_T_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                          : out_type == ZERO_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                     ob, out, m, n, ldo, 128);
     if (rc)
         return rc;
+    if (plan.few == 16)
+        return launch_few<16>(ma, mb, p, b_tile != 0, stream);
+    if (plan.few == 32)
+        return launch_few<32>(ma, mb, p, b_tile != 0, stream);
+    if (plan.few == 64)
+        return launch_few<64>(ma, mb, p, b_tile != 0, stream);
     return plan.pair ? launch_matmul<2, 2>(ma, mb, mo, p, b_tile != 0, stream)
                      : launch_matmul<1, 1>(ma, mb, mo, p, b_tile != 0, stream);
 }
