@@ -602,8 +602,10 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
 // roles of the operands change places, so that the 128 rows of a tensor-core
 // product are 128 rows of b and its columns the TN = 16, 32 or 64 rows of a:
 // a block's sums are TN columns of tensor memory (eight blocks of them in
-// flight) and TN registers of a thread.  Two CTAs to an SM, and k split so
-// that they fill the GPU.  16 x 4096 x 14336: 27 us with 128 columns, XX us here.
+// flight) and TN registers of a thread.  Two CTAs to an SM, and k split over
+// the CTAs of a cluster so that they fill the GPU; the parts' sums meet in
+// distributed shared memory (through global memory, with the last CTA adding
+// them, took 16 x 4096 x 14336 from XX to 19.0 us).
 template <int TN>
 struct Few {
     static constexpr int kThreads = 224;
@@ -613,6 +615,23 @@ struct Few {
     static constexpr int kColumns = TN * kBufs;
     static constexpr int kSmem = 1024 + kStages * kStageBytes;
 };
+
+// One element of the output: x, or the old value and x.
+__device__ __forceinline__ void put_one(const MatmulParams &p, int64_t at, float x)
+{
+    auto put = [&](auto *o) {
+        using T = std::remove_reference_t<decltype(*o)>;
+        *o = from_f32<T>(p.add ? to_f32(*o) + x : x);
+    };
+    if (p.out_type == ZERO_T_BF16)
+        put(static_cast<bf16 *>(p.out) + at);
+    else if (p.out_type == ZERO_T_F16)
+        put(static_cast<f16 *>(p.out) + at);
+    else
+        put(static_cast<float *>(p.out) + at);
+}
+
+constexpr int kMaxSplits = 8;  // CTAs of a cluster
 
 template <int TN, bool TILE_B>
 __global__ void __launch_bounds__(Few<TN>::kThreads, 2)
@@ -627,9 +646,11 @@ __global__ void __launch_bounds__(Few<TN>::kThreads, 2)
     __shared__ __align__(8) uint64_t scale_full[kGroups], scale_empty[kGroups];
     __shared__ __align__(16) float scale_a[kGroups][kGroup][TN], scale_b[kGroups][kGroup][TILE_B ? 1 : 128];
     __shared__ uint32_t tmem_sh;
-    __shared__ int gave_up_sh, last_sh;
+    __shared__ int gave_up_sh;
     volatile int *gave_up = &gave_up_sh;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    float *part = reinterpret_cast<float *>(smem);  // over the stages, once they are done with
+    static_assert(TN * 128 * 4 <= S::kStages * S::kStageBytes, "the sums fit the stages");
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -821,53 +842,39 @@ __global__ void __launch_bounds__(Few<TN>::kThreads, 2)
                 ok = false;
                 break;
             }
-            if (p.splits > 1) {
-                // this part's sums to the workspace; the tile's last part adds
-                // all of them in ascending order
-                float *mine = p.parts + ((int64_t)w.tile * p.splits + w.split) * (TN * 128) + t;
+            if (p.splits > 1) {  // the one unit of this CTA: its sums for the cluster
 #pragma unroll
                 for (int i = 0; i < TN; ++i)
                     if (i < p.m)
-                        __stcg(mine + i * 128, acc[i]);
-                __threadfence();
-                barrier_of(1, 128);
-                if (t == 0) {
-                    last_sh = atomicAdd(p.counters + w.tile, 1u) == (uint32_t)p.splits - 1;
-                    __threadfence();
-                }
-                barrier_of(1, 128);
-                if (!last_sh)
-                    continue;
-                const float *all = p.parts + (int64_t)w.tile * p.splits * (TN * 128) + t;
+                        part[i * 128 + t] = acc[i];
+            } else if (row < p.n) {
 #pragma unroll
                 for (int i = 0; i < TN; ++i)
-                    acc[i] = 0.0f;
-                for (int s = 0; s < p.splits; ++s, all += TN * 128)
-#pragma unroll
-                    for (int i = 0; i < TN; ++i)
-                        if (i < p.m)
-                            acc[i] += __ldcg(all + i * 128);
-                if (t == 0)
-                    p.counters[w.tile] = 0;
-            }
-            if (row < p.n) {
-                auto put = [&](auto *o) {
-                    using T = std::remove_reference_t<decltype(*o)>;
-#pragma unroll
-                    for (int i = 0; i < TN; ++i)
-                        if (i < p.m) {
-                            T *at = o + (int64_t)i * p.ldo + row;
-                            *at = from_f32<T>(p.add ? to_f32(*at) + acc[i] : acc[i]);
-                        }
-                };
-                if (p.out_type == ZERO_T_BF16)
-                    put(static_cast<bf16 *>(p.out));
-                else if (p.out_type == ZERO_T_F16)
-                    put(static_cast<f16 *>(p.out));
-                else
-                    put(static_cast<float *>(p.out));
+                    if (i < p.m)
+                        put_one(p, (int64_t)i * p.ldo + row, acc[i]);
             }
         }
+    }
+    if (p.splits > 1) {
+        // the parts in ascending order, each CTA for every splits-th row of a
+        __syncwarp();
+        cluster_sync();
+        const Unit w = unit_of(p, first);
+        const int row = w.n * 128 + (int)threadIdx.x;
+        if (threadIdx.x < 128 && row < p.n && !gave_up_sh)
+            for (int i = w.split; i < p.m; i += p.splits) {
+                const uint32_t at = smem_u32(part + i * 128 + threadIdx.x);
+                float x[kMaxSplits];
+#pragma unroll
+                for (int s = 0; s < kMaxSplits; ++s)
+                    x[s] = s < p.splits ? load_cluster(map_to(at, (uint32_t)s)) : 0.0f;
+                float sum = 0.0f;
+#pragma unroll
+                for (int s = 0; s < kMaxSplits; ++s)
+                    sum += x[s];
+                put_one(p, (int64_t)i * p.ldo + row, sum);
+            }
+        cluster_sync();  // nobody ends while its sums are being read
     }
     __syncwarp();
     fence_before();
@@ -926,7 +933,7 @@ struct Plan {
     bool pair;
     int64_t tiles_m, tiles_n;
     int splits;
-    int64_t part;  // elements of a part's sums
+    int64_t part;  // elements of a part's sums in the workspace
 };
 static Plan plan_of(int64_t m, int64_t n, int64_t k)
 {
@@ -942,14 +949,29 @@ static Plan plan_of(int64_t m, int64_t n, int64_t k)
     r.few = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 0;
     r.tiles_m = r.few ? 1 : ceil_div(m, 128);
     r.tiles_n = ceil_div(n, 128);
-    r.part = (int64_t)(r.few ? r.few : 128) * 128;
+    r.part = r.few ? 0 : 128 * 128;
     const int64_t tiles = r.tiles_m * r.tiles_n;
     int64_t s = (r.few ? 2 : 1) * kPlanSms / tiles;
-    if (s > kb / 4)  // a part is worth its sums' way through memory from four blocks on
+    if (s > kb / 4)  // a part is worth its sums' way to the others from four blocks on
         s = kb / 4;
+    if (r.few && s > kMaxSplits)
+        s = kMaxSplits;
     if (s > 1)
         r.splits = (int)s;
     return r;
+}
+
+// Lets a kernel use that much shared memory, once for each device (bits of `ready`).
+static cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &ready)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (ready.load(std::memory_order_acquire) >> dev & 1)))
+        return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64)
+        ready.fetch_or(UINT64_C(1) << dev, std::memory_order_acq_rel);
+    return e;
 }
 
 template <int CG, int NH>
@@ -959,7 +981,8 @@ static int launch_matmul(const CUtensorMap &a, const CUtensorMap &b, const CUten
     using S = Shape<CG, NH>;
     auto kernel = tile_b ? matmul_kernel<CG, NH, true> : matmul_kernel<CG, NH, false>;
     static_assert(S::kSmem <= 227 * 1024 - 4096, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    static std::atomic<uint64_t> ready[2];
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), S::kSmem, ready[tile_b]);
     if (e != cudaSuccess)
         return cuda_error(e);
     const int64_t units = p.units;
@@ -984,12 +1007,24 @@ static int launch_few(const CUtensorMap &a, const CUtensorMap &b, const MatmulPa
 {
     using S = Few<TN>;
     auto kernel = tile_b ? matmul_few_kernel<TN, true> : matmul_few_kernel<TN, false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    static std::atomic<uint64_t> ready[2];
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), S::kSmem, ready[tile_b]);
     if (e != cudaSuccess)
         return cuda_error(e);
     const int most = 2 * device_sms();
-    kernel<<<p.units < most ? p.units : most, S::kThreads, S::kSmem, stream>>>(a, b, p);
-    return launch_status();
+    cudaLaunchConfig_t cfg{};
+    // clusters hold one unit to a CTA; else the CTAs walk the units
+    cfg.gridDim = dim3((unsigned)(p.splits > 1 || p.units < most ? p.units : most));
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {(unsigned)p.splits, 1, 1};
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, a, b, p);
+    return e == cudaSuccess ? launch_status() : cuda_error(e);
 }
 
 }  // namespace zo

@@ -42,6 +42,14 @@ __device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank)
     return r;
 }
 
+// A float of another CTA's shared memory (an address from map_to).
+__device__ __forceinline__ float load_cluster(uint32_t addr)
+{
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+    return x;
+}
+
 // ------------------------------------------------------------------ mbarriers
 
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)

@@ -31,10 +31,26 @@ _TYPE = {torch.float16: T_F16, torch.bfloat16: T_BF16, torch.float32: T_F32,
          torch.float8_e4m3fn: T_E4M3, torch.float8_e5m2: T_E5M2}
 
 
-def _stream(stream, device: torch.device) -> int:
-    if stream is not None:
-        return stream.cuda_stream
+# The calls below are made once for each layer and product of a step, so the
+# marshalling counts: tensors' attributes are read once, and the current device
+# and stream come from torch's own bindings without objects around them.
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _raw_stream(device: int) -> int:
     return torch.cuda.current_stream(device).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+def _stream(stream, device: int) -> int:
+    return _raw_stream(device) if stream is None else stream.cuda_stream
+
+
+def _current() -> int:
+    """The current device's index (-1 without a device: no tensor matches it)."""
+    return _device() if torch.cuda.is_initialized() else -1
 
 
 def _type(t: torch.Tensor) -> int:
@@ -44,39 +60,39 @@ def _type(t: torch.Tensor) -> int:
     return code
 
 
-def _on_device(t: torch.Tensor) -> int:
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError("CUDA tensor of the current device expected")
-    return t.data_ptr()
+def _where(name: str = "") -> None:
+    raise ValueError(f"{name or 'tensor'}: CUDA tensor of the current device expected")
 
 
-def _flat(t: Optional[torch.Tensor]) -> Optional[int]:
+def _flat(t: Optional[torch.Tensor], dev: int) -> Optional[int]:
     if t is None:
         return None
     if not t.is_contiguous():
         raise ValueError("contiguous tensor expected")
-    return _on_device(t)
+    if t.get_device() != dev or dev < 0:
+        _where()
+    return t.data_ptr()
 
 
-def _matrix(t: Optional[torch.Tensor], rows: int, cols: int, name: str,
-            dtypes=None) -> Tuple[Optional[int], int]:
+def _matrix(t: torch.Tensor, rows: int, cols: int, name: str, dtypes, dev: int) -> Tuple[int, int]:
     """(pointer, row stride) of a [rows, cols] matrix with contiguous rows."""
-    if t is None:
-        return None, 0
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
-    if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
-        raise ValueError(f"{name}: contiguous rows expected, strides {t.stride()}")
-    if dtypes is not None and t.dtype not in dtypes:
+    if t.dtype not in dtypes:
         raise TypeError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    # torch gives a single row any stride
-    return _on_device(t), max(t.stride(0), cols) if rows > 1 else _row_stride(t, cols)
+    ld, step = t.stride()
+    if rows <= 1:
+        # torch gives a single row any stride; no second row is ever reached, so
+        # the next multiple of 16 elements serves every alignment rule
+        ld = (cols + 15) // 16 * 16
+    if step != 1 and cols > 1 or ld < cols:
+        raise ValueError(f"{name}: contiguous rows expected, strides {t.stride()}")
+    if t.get_device() != dev or dev < 0:
+        _where(name)
+    return t.data_ptr(), ld
 
 
-def _row_stride(t: torch.Tensor, cols: int) -> int:
-    """A stride for a matrix of one row: no second row is ever reached, so the
-    next multiple of 16 elements serves every alignment rule."""
-    return (cols + 15) // 16 * 16
+_NONE = (None, 0)
 
 
 def _blocks(n: int) -> int:
@@ -99,7 +115,8 @@ class TensorList:
     def __init__(self, tensors: Sequence[torch.Tensor]):
         self.tensors = list(tensors)
         n = self.n = len(self.tensors)
-        self.ptr = (ctypes.c_void_p * max(n, 1))(*[_flat(t) for t in self.tensors])
+        dev = self.device = _current()
+        self.ptr = (ctypes.c_void_p * max(n, 1))(*[_flat(t, dev) for t in self.tensors])
         self.numel = (ctypes.c_int64 * max(n, 1))(*[t.numel() for t in self.tensors])
         self.type = (ctypes.c_int32 * max(n, 1))(*[_type(t) for t in self.tensors])
 
@@ -134,32 +151,36 @@ def zero_tensors_norm(tensors: Tensors, inv_scale: float, stat: torch.Tensor, ws
                       tensor_sumsq: Optional[torch.Tensor] = None, stream=None) -> None:
     """The global norm of the tensors times inv_scale into ``stat``;
     ``tensor_sumsq``: one float64 per tensor, each tensor's sum of squares."""
-    l = tensor_list(tensors)
-    if stat.numel() * stat.element_size() < ctypes.sizeof(TensorsStat):
+    l, dev = tensor_list(tensors), _current()
+    if l.device != dev:
+        _where("tensors")
+    if stat.nbytes < 16:
         raise ValueError("stat: 16 bytes expected (new_tensors_stat)")
     if tensor_sumsq is not None and (tensor_sumsq.dtype != torch.float64
                                      or tensor_sumsq.numel() != l.n):
         raise ValueError("tensor_sumsq: one float64 for each tensor expected")
     check("zero_tensors_norm",
-          lib().zero_tensors_norm(l.n, l.ptr, l.numel, l.type, inv_scale, _flat(tensor_sumsq),
-                                  _flat(stat), _flat(ws), ws.numel() * ws.element_size(),
-                                  _stream(stream, stat.device)))
+          lib().zero_tensors_norm(l.n, l.ptr, l.numel, l.type, inv_scale,
+                                  _flat(tensor_sumsq, dev), _flat(stat, dev), _flat(ws, dev),
+                                  ws.nbytes, _stream(stream, dev)))
 
 
 def zero_tensors_clip(tensors: Tensors, out: Optional[Tensors], inv_scale: float, max_norm: float,
                       stat: torch.Tensor, stream=None) -> None:
     """out = tensors * inv_scale * min(1, max_norm / (norm + 1e-6)), in place
     with ``out`` None; max_norm 0 does not clip."""
-    l = tensor_list(tensors)
+    l, dev = tensor_list(tensors), _current()
     o = tensor_list(out) if out is not None else None
-    if o is not None and (o.n != l.n or any(a != b for a, b in zip(o.numel, l.numel))):
+    if l.device != dev or o is not None and o.device != dev:
+        _where("tensors")
+    if o is not None and (o.n != l.n or bytes(o.numel) != bytes(l.numel)):
         raise ValueError("out: as many tensors of the same sizes expected")
-    if stat.numel() * stat.element_size() < ctypes.sizeof(TensorsStat):
+    if stat.nbytes < 16:
         raise ValueError("stat: 16 bytes expected (new_tensors_stat)")
     check("zero_tensors_clip",
           lib().zero_tensors_clip(l.n, l.ptr, l.numel, l.type, o.ptr if o is not None else None,
                                   o.type if o is not None else None, inv_scale, max_norm,
-                                  _flat(stat), _stream(stream, stat.device)))
+                                  _flat(stat, dev), _stream(stream, dev)))
 
 
 # ----------------------------------------------------------------- 8-bit matrices
@@ -181,20 +202,21 @@ def zero_fp8_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     (q, s), and its transpose, blocks along x's rows, into (qt, st)."""
     if x.dim() != 2:
         raise ValueError("x: matrix expected")
-    rows, cols = x.shape
-    px, ldx = _matrix(x, rows, cols, "x", _FLOAT)
+    (rows, cols), dev = x.shape, _current()
+    px, ldx = _matrix(x, rows, cols, "x", _FLOAT, dev)
     if (q is None) != (s is None) or (qt is None) != (st is None) or (q is None and qt is None):
         raise ValueError("(q, s), (qt, st) or both expected")
     if q is not None and qt is not None and q.dtype != qt.dtype:
         raise TypeError("q and qt: one 8-bit type expected")
-    pq, ldq = _matrix(q, rows, cols, "q", _F8)
-    ps, lds = _matrix(s, _blocks(cols), _blocks(rows) if tile else rows, "s", _F32)
-    pqt, ldqt = _matrix(qt, cols, rows, "qt", _F8)
-    pst, ldst = _matrix(st, _blocks(rows), _blocks(cols) if tile else cols, "st", _F32)
+    kb, rb = _blocks(cols), _blocks(rows)
+    pq, ldq = _matrix(q, rows, cols, "q", _F8, dev) if q is not None else _NONE
+    ps, lds = _matrix(s, kb, rb if tile else rows, "s", _F32, dev) if q is not None else _NONE
+    pqt, ldqt = _matrix(qt, cols, rows, "qt", _F8, dev) if qt is not None else _NONE
+    pst, ldst = _matrix(st, rb, kb if tile else cols, "st", _F32, dev) if qt is not None else _NONE
     check("zero_fp8_quantize",
-          lib().zero_fp8_quantize(px, _type(x), rows, cols, ldx, _type(q if q is not None else qt),
-                                  int(tile), pq, ldq, ps, lds, pqt, ldqt, pst, ldst,
-                                  _stream(stream, x.device)))
+          lib().zero_fp8_quantize(px, _TYPE[x.dtype], rows, cols, ldx,
+                                  _TYPE[(q if q is not None else qt).dtype], tile, pq, ldq, ps, lds,
+                                  pqt, ldqt, pst, ldst, _stream(stream, dev)))
 
 
 def zero_fp8_matmul_workspace_bytes(m: int, n: int, k: int) -> int:
@@ -211,17 +233,18 @@ def zero_fp8_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torc
     b's, by their shape, for 128x128 tiles or 1x128 blocks."""
     if a.dim() != 2 or b.dim() != 2:
         raise ValueError("a, b: matrices expected")
-    (m, k), n = a.shape, b.shape[0]
-    pa, lda = _matrix(a, m, k, "a", _F8)
-    pb, ldb = _matrix(b, n, k, "b", _F8)
-    psa, ldsa = _matrix(sa, _blocks(k), m, "sa", _F32)
+    (m, k), n, dev = a.shape, b.shape[0], _current()
+    pa, lda = _matrix(a, m, k, "a", _F8, dev)
+    pb, ldb = _matrix(b, n, k, "b", _F8, dev)
+    kb = _blocks(k)
+    psa, ldsa = _matrix(sa, kb, m, "sa", _F32, dev)
     tile = sb.dim() == 2 and sb.shape[1] != n
-    psb, ldsb = _matrix(sb, _blocks(k), _blocks(n) if tile else n, "sb", _F32)
-    po, ldo = _matrix(out, m, n, "out", _FLOAT)
+    psb, ldsb = _matrix(sb, kb, _blocks(n) if tile else n, "sb", _F32, dev)
+    po, ldo = _matrix(out, m, n, "out", _FLOAT, dev)
     check("zero_fp8_matmul",
-          lib().zero_fp8_matmul(pa, _type(a), lda, psa, ldsa, pb, _type(b), ldb, psb, ldsb,
-                                int(tile), po, _type(out), ldo, m, n, k, int(add), _flat(ws),
-                                ws.numel() * ws.element_size(), _stream(stream, out.device)))
+          lib().zero_fp8_matmul(pa, _TYPE[a.dtype], lda, psa, ldsa, pb, _TYPE[b.dtype], ldb, psb, ldsb,
+                                tile, po, _TYPE[out.dtype], ldo, m, n, k, add, _flat(ws, dev),
+                                ws.nbytes, _stream(stream, dev)))
 
 
 # ----------------------------------------------------------------- root-mean-square norm
@@ -235,20 +258,23 @@ def zero_rmsnorm_fp8(x: torch.Tensor, w: torch.Tensor, eps: float,
     x's type and, in 8 bits with a scale for each 1x128 block, into (q, s)."""
     if x.dim() != 2:
         raise ValueError("x: matrix expected")
-    rows, cols = x.shape
+    (rows, cols), dev = x.shape, _current()
     if w.numel() != cols or rstd is not None and (rstd.numel() != rows
                                                   or rstd.dtype != torch.float32):
         raise ValueError("w: one element for each column, rstd: one fp32 for each row expected")
-    px, ldx = _matrix(x, rows, cols, "x", _HALF)
-    pr, ldr = _matrix(residual, rows, cols, "residual", (x.dtype,))
-    ph, ldh = _matrix(h, rows, cols, "h", (x.dtype,))
-    py, ldy = _matrix(y, rows, cols, "y", (x.dtype,))
-    pq, ldq = _matrix(q, rows, cols, "q", _F8)
-    ps, lds = _matrix(s, _blocks(cols), rows, "s", _F32)
+    if (q is None) != (s is None):
+        raise ValueError("q and s: both or neither expected")
+    dt = (x.dtype,)
+    px, ldx = _matrix(x, rows, cols, "x", _HALF, dev)
+    pr, ldr = _matrix(residual, rows, cols, "residual", dt, dev) if residual is not None else _NONE
+    ph, ldh = _matrix(h, rows, cols, "h", dt, dev) if h is not None else _NONE
+    py, ldy = _matrix(y, rows, cols, "y", dt, dev) if y is not None else _NONE
+    pq, ldq = _matrix(q, rows, cols, "q", _F8, dev) if q is not None else _NONE
+    ps, lds = _matrix(s, _blocks(cols), rows, "s", _F32, dev) if q is not None else _NONE
     check("zero_rmsnorm_fp8",
-          lib().zero_rmsnorm_fp8(px, ldx, pr, ldr, _flat(w), _type(w), _type(x), rows, cols, eps,
-                                 ph, ldh, py, ldy, _type(q) if q is not None else T_E4M3, pq, ldq,
-                                 ps, lds, _flat(rstd), _stream(stream, x.device)))
+          lib().zero_rmsnorm_fp8(px, ldx, pr, ldr, _flat(w, dev), _type(w), _TYPE[x.dtype], rows, cols,
+                                 eps, ph, ldh, py, ldy, _TYPE[q.dtype] if q is not None else T_E4M3,
+                                 pq, ldq, ps, lds, _flat(rstd, dev), _stream(stream, dev)))
 
 
 def zero_rmsnorm_workspace_bytes(rows: int, cols: int) -> int:
@@ -267,20 +293,20 @@ def zero_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, w: torch.Tensor, rs
     with the gradient ``dres`` that reaches h by the residual path added."""
     if dy.dim() != 2:
         raise ValueError("dy: matrix expected")
-    rows, cols = dy.shape
+    (rows, cols), dev = dy.shape, _current()
     if w.numel() != cols or dw is not None and dw.numel() != cols:
         raise ValueError("w, dw: one element for each column expected")
     if rstd.numel() != rows or rstd.dtype != torch.float32:
         raise ValueError("rstd: one fp32 for each row expected")
     if dw is not None and ws is None:
         raise ValueError("ws: a workspace expected (zero_rmsnorm_workspace_bytes)")
-    pdy, lddy = _matrix(dy, rows, cols, "dy", _HALF)
-    ph, ldh = _matrix(h, rows, cols, "h", (dy.dtype,))
-    pdr, lddr = _matrix(dres, rows, cols, "dres", (dy.dtype,))
-    pdx, lddx = _matrix(dx, rows, cols, "dx", (dy.dtype,))
+    dt = (dy.dtype,)
+    pdy, lddy = _matrix(dy, rows, cols, "dy", _HALF, dev)
+    ph, ldh = _matrix(h, rows, cols, "h", dt, dev)
+    pdr, lddr = _matrix(dres, rows, cols, "dres", dt, dev) if dres is not None else _NONE
+    pdx, lddx = _matrix(dx, rows, cols, "dx", dt, dev)
     check("zero_rmsnorm_backward",
-          lib().zero_rmsnorm_backward(pdy, lddy, ph, ldh, _flat(w), _type(w), _flat(rstd), pdr,
-                                      lddr, _type(dy), rows, cols, pdx, lddx, _flat(dw),
-                                      _type(dw) if dw is not None else T_F32, int(add_dw),
-                                      _flat(ws), ws.numel() * ws.element_size() if ws is not None
-                                      else 0, _stream(stream, dy.device)))
+          lib().zero_rmsnorm_backward(pdy, lddy, ph, ldh, _flat(w, dev), _type(w), _flat(rstd, dev), pdr,
+                                      lddr, _TYPE[dy.dtype], rows, cols, pdx, lddx, _flat(dw, dev),
+                                      _type(dw) if dw is not None else T_F32, add_dw, _flat(ws, dev),
+                                      ws.nbytes if ws is not None else 0, _stream(stream, dev)))
