@@ -199,7 +199,8 @@ __device__ __forceinline__ void write_gather(const MatmulParams &p, const float 
 {
     constexpr int kCols = 2 * kStage / 128 / (int)sizeof(T);  // columns staged at a time
     constexpr int kPiece = 16 / (int)sizeof(T);
-    constexpr int kPieces = kCols / kPiece;  // of a row, and one more where the row starts inside a piece
+    constexpr int kPieces = kCols / kPiece;  // of a row: 16
+    static_assert(kPieces == 16, "16 threads to a row");
     constexpr int kPitch = kCols * (int)sizeof(T);
 #pragma unroll
     for (int c = 0; c < 128; c += kCols) {
@@ -210,25 +211,37 @@ __device__ __forceinline__ void write_gather(const MatmulParams &p, const float 
             *reinterpret_cast<uint4 *>(stage + t * kPitch + ((i ^ (t & 7)) << 4)) = pack16<T>(acc + c + i * kPiece);
         barrier_of(id, 128);
         const int n = min(kCols, p.n - n0 - c);
-        for (int e = t; e < 128 * (kPieces + 1); e += 128) {
-            const int row = e / (kPieces + 1), piece = e - row * (kPieces + 1);
-            if (m0 + row >= p.m)
-                break;
-            T *o = static_cast<T *>(p.out) + (int64_t)(m0 + row) * p.ldo + n0 + c;
-            const int at = piece * kPiece - (int)(reinterpret_cast<uintptr_t>(o) / sizeof(T) % kPiece);
-            auto value = [&](int k) {
-                const int b = k * (int)sizeof(T);
-                return *reinterpret_cast<const T *>(stage + row * kPitch + (((b >> 4) ^ (row & 7)) << 4) + (b & 15));
-            };
-            if (at >= 0 && at + kPiece <= n) {
+        auto value = [&](int row, int k) {
+            const int b = k * (int)sizeof(T);
+            return *reinterpret_cast<const T *>(stage + row * kPitch + (((b >> 4) ^ (row & 7)) << 4) + (b & 15));
+        };
+        auto head_of = [&](const T *o) {  // elements ahead of the row's first whole piece
+            return (int)((uintptr_t)(-(intptr_t)reinterpret_cast<uintptr_t>(o)) / sizeof(T) % kPiece);
+        };
+        T *first = static_cast<T *>(p.out) + (int64_t)m0 * p.ldo + n0 + c;
+        // whole pieces: 16 threads to a row
+        T *o = first + (int64_t)(t >> 4) * p.ldo;
+#pragma unroll 4
+        for (int row = t >> 4; row < 128; row += 8, o += 8 * p.ldo) {
+            const int at = head_of(o) + (t & 15) * kPiece;
+            if (m0 + row < p.m && at + kPiece <= n) {
                 alignas(16) T v[kPiece];
 #pragma unroll
                 for (int k = 0; k < kPiece; ++k)
-                    v[k] = value(at + k);
+                    v[k] = value(row, at + k);
                 *reinterpret_cast<uint4 *>(o + at) = *reinterpret_cast<const uint4 *>(v);
-            } else {
-                for (int k = max(at, 0); k < min(at + kPiece, n); ++k)
-                    o[k] = value(k);
+            }
+        }
+        // the rows' ends: a thread to a row
+        if (m0 + t < p.m && n > 0) {
+            o = first + (int64_t)t * p.ldo;
+            const int head = min(head_of(o), n), tail = head + (n - head) / kPiece * kPiece;
+#pragma unroll
+            for (int k = 0; k < kPiece - 1; ++k) {
+                if (k < head)
+                    o[k] = value(t, k);
+                if (tail + k < n)
+                    o[tail + k] = value(t, tail + k);
             }
         }
     }

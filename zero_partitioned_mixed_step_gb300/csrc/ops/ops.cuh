@@ -11,6 +11,7 @@
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
+#include <cstring>
 
 #include "zerostep_ops.h"
 
@@ -100,43 +101,125 @@ __device__ __forceinline__ float rounded(float x)
     return to_f32(from_f32<T>(x));
 }
 
-// Eight neighbouring elements as they lie in memory.
+// Eight neighbouring elements, kept in 32-bit words (halves two to a word: as
+// an array of halves the compiler gives each a register of its own).
 template <class T>
-struct alignas(sizeof(T) * 8 < 16 ? sizeof(T) * 8 : 16) Pack8 {
-    T v[8];
+struct Raw8 {
+    static constexpr int kWords = 2 * (int)sizeof(T);
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ float at(int i) const
+    {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(w[i]);
+        else if constexpr (Type<T>::code == ZERO_T_BF16)
+            return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+        else
+            return __half2float(__ushort_as_half((unsigned short)(w[i >> 1] >> (16 * (i & 1)))));
+    }
 };
 
-// Eight elements from p, of which the first n exist (the others read as 0).
-// `wide`: p is 16-byte aligned (a rule on the whole matrix).
+template <class T>
+__device__ __forceinline__ uint32_t word_of(float a, float b)  // two halves, rounded
+{
+    if constexpr (Type<T>::code == ZERO_T_BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+// Eight elements from p, of which the first n exist (the others are zeros).
+template <class T>
+__device__ __forceinline__ Raw8<T> load_raw(const T *p, int n, bool wide)
+{
+    Raw8<T> r;
+    if (wide && n >= 8) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(p);
+#pragma unroll
+        for (int i = 0; i < Raw8<T>::kWords / 4; ++i) {
+            const uint4 x = q[i];
+            r.w[4 * i] = x.x;
+            r.w[4 * i + 1] = x.y;
+            r.w[4 * i + 2] = x.z;
+            r.w[4 * i + 3] = x.w;
+        }
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            r.w[i] = i < n ? reinterpret_cast<const uint32_t *>(p)[i] : 0u;
+    } else {
+        const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r.w[i] = (2 * i < n ? (uint32_t)q[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)q[2 * i + 1] << 16 : 0u);
+    }
+    return r;
+}
+
+// Eight existing elements from a 16-byte aligned p, used once (LAST) or again soon.
+template <bool LAST, class T>
+__device__ __forceinline__ Raw8<T> load_full(const T *p)
+{
+    Raw8<T> r;
+    const uint4 *q = reinterpret_cast<const uint4 *>(p);
+#pragma unroll
+    for (int i = 0; i < Raw8<T>::kWords / 4; ++i) {
+        const uint4 x = LAST ? __ldcs(q + i) : __ldg(q + i);
+        r.w[4 * i] = x.x;
+        r.w[4 * i + 1] = x.y;
+        r.w[4 * i + 2] = x.z;
+        r.w[4 * i + 3] = x.w;
+    }
+    return r;
+}
+
+template <class T>
+__device__ __forceinline__ void store_raw(T *p, int n, bool wide, const Raw8<T> &r)
+{
+    static_assert(sizeof(T) == 2, "halves");
+    if (wide && n >= 8) {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    } else {
+        uint16_t *q = reinterpret_cast<uint16_t *>(p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n)
+                q[i] = (uint16_t)(r.w[i >> 1] >> (16 * (i & 1)));
+    }
+}
+
+// The same as fp32 values.  `wide`: p is 16-byte aligned (a rule on the whole matrix).
 template <class T>
 __device__ __forceinline__ void load8(const T *p, int n, bool wide, float x[8])
 {
-    if (wide && n >= 8) {
-        const Pack8<T> r = *reinterpret_cast<const Pack8<T> *>(p);
+    const Raw8<T> r = load_raw(p, n, wide);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            x[i] = to_f32(r.v[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            x[i] = i < n ? to_f32(p[i]) : 0.0f;
-    }
+    for (int i = 0; i < 8; ++i)
+        x[i] = r.at(i);
 }
 
 template <class T>
 __device__ __forceinline__ void store8(T *p, int n, bool wide, const float x[8])
 {
-    if (wide && n >= 8) {
-        Pack8<T> r;
+    if constexpr (sizeof(T) == 4) {
+        if (wide && n >= 8) {
+            reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+            reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            r.v[i] = from_f32<T>(x[i]);
-        *reinterpret_cast<Pack8<T> *>(p) = r;
+            for (int i = 0; i < 8; ++i)
+                if (i < n)
+                    p[i] = x[i];
+        }
     } else {
+        Raw8<T> r;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n)
-                p[i] = from_f32<T>(x[i]);
+        for (int i = 0; i < 4; ++i)
+            r.w[i] = word_of<T>(x[2 * i], x[2 * i + 1]);
+        store_raw(p, n, wide, r);
     }
 }
 
@@ -171,6 +254,22 @@ struct F8Type<ZERO_T_E5M2> {
 // A magnitude's bits order as the magnitude does, with infinity above every
 // number and NaN above infinity: an integer maximum over them carries both.
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// Magnitudes of a type's elements as order-preserving bits, two halves at a
+// time (the same integer order as fp32's), and their largest as fp32 bits.
+template <class T>
+struct Amax {  // a half type
+    uint32_t two = 0;
+    __device__ __forceinline__ void add(uint32_t pair) { two = __vmaxu2(two, pair & 0x7FFF7FFFu); }
+    __device__ __forceinline__ void add(const Amax &o) { two = __vmaxu2(two, o.two); }
+    __device__ __forceinline__ uint32_t bits() const
+    {
+        const uint16_t one = (uint16_t)max(two & 0xFFFFu, two >> 16);
+        T x;
+        memcpy(&x, &one, 2);
+        return magnitude(to_f32(x));
+    }
+};
 
 // The scale of a block whose largest magnitude is amax (as bits).
 template <int F8>

@@ -26,10 +26,58 @@ struct QuantParams {
     int32_t row_tiles;
 };
 
+// A thread's 8x8 patch as it lies in memory.  Halves stay packed: half the
+// registers, so that three CTAs fit an SM, and their magnitudes are compared
+// two at a time.
+template <class T>
+struct Patch {
+    Raw8<T> row[8];
+
+    __device__ __forceinline__ float at(int i, int j) const { return row[i].at(j); }
+    __device__ __forceinline__ uint32_t row_amax(int i) const
+    {
+        if constexpr (sizeof(T) == 2) {
+            Amax<T> a;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                a.add(row[i].w[k]);
+            return a.bits();
+        } else {
+            uint32_t a = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                a = max(a, magnitude(at(i, j)));
+            return a;
+        }
+    }
+    // columns 2k and 2k + 1
+    __device__ __forceinline__ uint2 column_amax(int k) const
+    {
+        if constexpr (sizeof(T) == 2) {
+            Amax<T> a;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                a.add(row[i].w[k]);
+            Amax<T> lo, hi;
+            lo.two = a.two & 0xFFFFu;
+            hi.two = a.two >> 16;
+            return make_uint2(lo.bits(), hi.bits());
+        } else {
+            uint2 a = make_uint2(0, 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                a.x = max(a.x, magnitude(at(i, 2 * k)));
+                a.y = max(a.y, magnitude(at(i, 2 * k + 1)));
+            }
+            return a;
+        }
+    }
+};
+
 // TILE: one scale per tile.  TRANS: the transposed form is wanted (q may be
 // too: p.q says so).
 template <class T, int F8, bool TILE, bool TRANS>
-__global__ void __launch_bounds__(kQThreads) quantize_kernel(const QuantParams p)
+__global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 3 : 2) quantize_kernel(const QuantParams p)
 {
     __shared__ uint32_t amax_sh[16][kBlock];  // a row group's amax of each column
     __shared__ float inv_sh[kBlock];
@@ -41,19 +89,17 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const QuantParams p
     const int nr = (int)min((int64_t)8, p.rows - r0);
     const T *x = static_cast<const T *>(p.x) + r0 * p.ldx + c0;
 
-    float v[8][8];
+    Patch<T> v;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        load8(x + i * p.ldx, i < nr ? nc : 0, p.wide_x, v[i]);
+        v.row[i] = load_raw(x + i * p.ldx, i < nr ? nc : 0, p.wide_x);
 
-    float inv_row[8];
+    float inv_tile = 0.0f;
     if (TILE) {
         uint32_t a = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                a = max(a, magnitude(v[i][j]));
+            a = max(a, v.row_amax(i));
         a = max_over<32>(a);
         if ((threadIdx.x & 31) == 0)
             amax_sh[0][threadIdx.x >> 5] = a;
@@ -63,38 +109,39 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const QuantParams p
         for (int w = 0; w < kQThreads / 32; ++w)
             a = max(a, amax_sh[0][w]);
         const float s = block_scale<F8>(a);
-        const float inv = __fdiv_rn(1.0f, s);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            inv_row[i] = inv;
+        inv_tile = __fdiv_rn(1.0f, s);
         if (threadIdx.x == 0) {
             if (p.q)
                 p.s[tc * p.lds + tr] = s;
             if (TRANS)
                 p.st[tr * p.ldst + tc] = s;
         }
-    } else if (p.q) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t a = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                a = max(a, magnitude(v[i][j]));
-            a = max_over<16>(a);
-            const float s = block_scale<F8>(a);
-            inv_row[i] = __fdiv_rn(1.0f, s);
-            if (cg == i && i < nr)  // 8 lanes of the row group write 8 rows
-                p.s[tc * p.lds + r0 + i] = s;
-        }
     }
     if (p.q) {
+        // a row's amax is over the 16 lanes of its row group; lane i keeps row
+        // i's, so that its scale is formed once
+        uint32_t mine = 0;
+        if (!TILE) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t a = max_over<16>(v.row_amax(i));
+                if ((cg & 7) == i)
+                    mine = a;
+            }
+        }
+        float inv_mine = 0.0f;
+        if (!TILE) {
+            const float s = block_scale<F8>(mine);
+            inv_mine = __fdiv_rn(1.0f, s);
+            if (cg < 8 && cg < nr)
+                p.s[tc * p.lds + r0 + cg] = s;
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            uint2 o;
-            o.x = pack4<F8>(v[i][0] * inv_row[i], v[i][1] * inv_row[i], v[i][2] * inv_row[i],
-                            v[i][3] * inv_row[i]);
-            o.y = pack4<F8>(v[i][4] * inv_row[i], v[i][5] * inv_row[i], v[i][6] * inv_row[i],
-                            v[i][7] * inv_row[i]);
+            const float inv = TILE ? inv_tile : __shfl_sync(0xFFFFFFFFu, inv_mine, i, 16);
+            const uint2 o = make_uint2(
+                pack4<F8>(v.at(i, 0) * inv, v.at(i, 1) * inv, v.at(i, 2) * inv, v.at(i, 3) * inv),
+                pack4<F8>(v.at(i, 4) * inv, v.at(i, 5) * inv, v.at(i, 6) * inv, v.at(i, 7) * inv));
             if (i < nr)
                 store8b(p.q + (r0 + i) * p.ldq + c0, nc, p.wide_q, o);
         }
@@ -105,13 +152,8 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const QuantParams p
     if (!TILE) {
         // the columns' amax over the tile's 128 rows
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            uint32_t a = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                a = max(a, magnitude(v[i][j]));
-            amax_sh[rg][cg * 8 + j] = a;
-        }
+        for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint2 *>(&amax_sh[rg][cg * 8 + 2 * k]) = v.column_amax(k);
         __syncthreads();
         if (threadIdx.x < kBlock) {
             uint32_t a = 0;
@@ -132,11 +174,10 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const QuantParams p
     // different banks.
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float inv = TILE ? inv_row[0] : inv_sh[cg * 8 + j];
-        uint2 o;
-        o.x = pack4<F8>(v[0][j] * inv, v[1][j] * inv, v[2][j] * inv, v[3][j] * inv);
-        o.y = pack4<F8>(v[4][j] * inv, v[5][j] * inv, v[6][j] * inv, v[7][j] * inv);
-        t_sh[cg * 8 + j][rg ^ cg] = o;
+        const float inv = TILE ? inv_tile : inv_sh[cg * 8 + j];
+        t_sh[cg * 8 + j][rg ^ cg] = make_uint2(
+            pack4<F8>(v.at(0, j) * inv, v.at(1, j) * inv, v.at(2, j) * inv, v.at(3, j) * inv),
+            pack4<F8>(v.at(4, j) * inv, v.at(5, j) * inv, v.at(6, j) * inv, v.at(7, j) * inv));
     }
     __syncthreads();
     // 16 threads write a column's 128 rows

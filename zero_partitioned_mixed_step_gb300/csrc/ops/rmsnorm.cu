@@ -95,24 +95,36 @@ __device__ __forceinline__ void put_y(const NormParams &p, int64_t row, int64_t 
     }
 }
 
+// h's unit: x, or x + r rounded; written where it is wanted.
+template <class H>
+__device__ __forceinline__ Raw8<H> sum_h(const NormParams &p, int64_t row, int64_t c, int n, Raw8<H> x,
+                                         const Raw8<H> &r)
+{
+    if (p.r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x.w[i] = word_of<H>(x.at(2 * i) + r.at(2 * i), x.at(2 * i + 1) + r.at(2 * i + 1));
+    if (p.h && n > 0)
+        store_raw(static_cast<H *>(p.h) + row * p.ldh + c, n, p.wide, x);
+    return x;
+}
+
 template <class H>
 __device__ __forceinline__ void load_h(const NormParams &p, int64_t row, int64_t c, int n, float h[8])
 {
-    load8(static_cast<const H *>(p.x) + row * p.ldx + c, n, p.wide, h);
-    if (p.r) {
-        float r[8];
-        load8(static_cast<const H *>(p.r) + row * p.ldr + c, n, p.wide, r);
+    Raw8<H> r{};
+    if (p.r)
+        r = load_raw(static_cast<const H *>(p.r) + row * p.ldr + c, n, p.wide);
+    const Raw8<H> x = sum_h(p, row, c, n, load_raw(static_cast<const H *>(p.x) + row * p.ldx + c, n, p.wide), r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            h[i] = rounded<H>(h[i] + r[i]);
-    }
-    if (p.h && n > 0)
-        store8(static_cast<H *>(p.h) + row * p.ldh + c, n, p.wide, h);
+    for (int i = 0; i < 8; ++i)
+        h[i] = x.at(i);
 }
 
 // T threads to a row, V units of 8 elements to a thread; CTAs of max(T, 256).
+// h, which is of a half type, stays packed between its two uses.
 template <class H, int F8, int T, int V>
-__global__ void __launch_bounds__(T > 256 ? T : 256) rmsnorm_kernel(const NormParams p)
+__global__ void __launch_bounds__(T > 256 ? T : 256, T > 512 ? 1 : T > 256 ? 2 : 5) rmsnorm_kernel(const NormParams p)
 {
     constexpr int kCta = T > 256 ? T : 256;
     constexpr int kRows = kCta / T;
@@ -120,18 +132,24 @@ __global__ void __launch_bounds__(T > 256 ? T : 256) rmsnorm_kernel(const NormPa
     const int t = threadIdx.x % T, k = threadIdx.x / T;
     const int64_t row = (int64_t)blockIdx.x * kRows + k;
     const bool live = row < p.rows;
-    float h[V][8];
+    Raw8<H> h[V], r[V];
     float sq = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int64_t c = (int64_t)(v * T + t) * 8;
-        load_h<H>(p, live ? row : 0, c, live ? in_row(p.cols, c) : 0, h[v]);
+        const int n = live ? in_row(p.cols, c) : 0;
+        h[v] = load_raw(static_cast<const H *>(p.x) + (live ? row : 0) * p.ldx + c, n, p.wide);
+        if (p.r)
+            r[v] = load_raw(static_cast<const H *>(p.r) + (live ? row : 0) * p.ldr + c, n, p.wide);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+        const int64_t c = (int64_t)(v * T + t) * 8;
+        h[v] = sum_h(p, live ? row : 0, c, live ? in_row(p.cols, c) : 0, h[v], r[v]);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            sq = fmaf(h[v][i], h[v][i], sq);
+            sq = fmaf(h[v].at(i), h[v].at(i), sq);
+    }
     sq = row_sum<T>(sq, slots[k]);
     const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(sq * p.inv_cols + p.eps));
     if (live && t == 0 && p.rstd)
@@ -139,7 +157,11 @@ __global__ void __launch_bounds__(T > 256 ? T : 256) rmsnorm_kernel(const NormPa
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int64_t c = (int64_t)(v * T + t) * 8;
-        put_y<H, F8>(p, live ? row : 0, c, live ? in_row(p.cols, c) : 0, h[v], rstd);
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = h[v].at(i);
+        put_y<H, F8>(p, live ? row : 0, c, live ? in_row(p.cols, c) : 0, x, rstd);
     }
 }
 
@@ -211,64 +233,68 @@ struct BackParams {
     int32_t w_type;
 };
 
-// A CTA takes every gridDim.x-th row, a thread the same columns of each, so
-// dw's sums over the CTA's rows stay in registers.
-template <class H, int V, int T>
-__global__ void __launch_bounds__(T) rmsnorm_backward_kernel(const BackParams p)
+// A CTA takes every gridDim.x-th row, a thread the same 8 columns of each, so
+// dw's sums over the CTA's rows stay in registers; the next row is loaded
+// before this one is reduced.
+template <class H, int T>
+__global__ void __launch_bounds__(T, 1024 / T) rmsnorm_backward_kernel(const BackParams p)
 {
-    __shared__ float slot[T / 32];
-    float w[V][8], dw[V][8];
+    __shared__ float slot[2][T / 32 < 2 ? 2 : T / 32];
+    const int64_t c = (int64_t)threadIdx.x * 8;
+    const int n = in_row(p.cols, c);
+    float w[8], dw[8];
+    load_w(p.w, p.w_type, c, n, p.wide, w);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int64_t c = (int64_t)(v * T + threadIdx.x) * 8;
-        load_w(p.w, p.w_type, c, in_row(p.cols, c), p.wide, w[v]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            dw[v][i] = 0.0f;
-    }
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const float rstd = p.rstd[row];
-        float dy[V][8], h[V][8];
+    for (int i = 0; i < 8; ++i)
+        dw[i] = 0.0f;
+    Raw8<H> dy_next{}, h_next{}, dr_next{};
+    float rstd_next = 0.0f;
+    auto fetch = [&](int64_t row) {
+        if (row >= p.rows)
+            return;
+        dy_next = load_raw(static_cast<const H *>(p.dy) + row * p.lddy + c, n, p.wide);
+        h_next = load_raw(static_cast<const H *>(p.h) + row * p.ldh + c, n, p.wide);
+        if (p.dr)
+            dr_next = load_raw(static_cast<const H *>(p.dr) + row * p.lddr + c, n, p.wide);
+        rstd_next = p.rstd[row];
+    };
+    fetch(blockIdx.x);
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+        // the packed halves are kept and xhat and g formed again at their
+        // second use: two CTAs of 512 threads fit an SM
+        const float rstd = rstd_next;
+        const Raw8<H> dy = dy_next, h = h_next, dr = dr_next;
         float dot = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int64_t c = (int64_t)(v * T + threadIdx.x) * 8;
-            const int n = in_row(p.cols, c);
-            load8(static_cast<const H *>(p.dy) + row * p.lddy + c, n, p.wide, dy[v]);
-            load8(static_cast<const H *>(p.h) + row * p.ldh + c, n, p.wide, h[v]);
+        for (int i = 0; i < 8; ++i) {
+            const float xhat = h.at(i) * rstd, d = dy.at(i);
+            dw[i] = fmaf(d, xhat, dw[i]);
+            dot = fmaf(d * w[i], xhat, dot);
         }
+        fetch(row + gridDim.x);
+        dot = sum_over<32>(dot);
+        if (T > 32) {  // two slots in turn: one barrier a row
+            if ((threadIdx.x & 31) == 0)
+                slot[turn][threadIdx.x >> 5] = dot;
+            __syncthreads();
+            dot = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                h[v][i] *= rstd;  // xhat
-                dw[v][i] = fmaf(dy[v][i], h[v][i], dw[v][i]);
-                dy[v][i] *= w[v][i];
-                dot = fmaf(dy[v][i], h[v][i], dot);
-            }
-        const float m = row_sum<T>(dot, slot) * p.inv_cols;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int64_t c = (int64_t)(v * T + threadIdx.x) * 8;
-            const int n = in_row(p.cols, c);
+            for (int i = 0; i < T / 32; ++i)
+                dot += slot[turn][i];
+        }
+        const float m = dot * p.inv_cols;
+        if (n > 0) {
             float dx[8];
-            if (p.dr)
-                load8(static_cast<const H *>(p.dr) + row * p.lddr + c, n, p.wide, dx);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                dx[i] = rstd * (dy[v][i] - h[v][i] * m) + (p.dr ? dx[i] : 0.0f);
-            if (n > 0)
-                store8(static_cast<H *>(p.dx) + row * p.lddx + c, n, p.wide, dx);
+                dx[i] = rstd * (dy.at(i) * w[i] - h.at(i) * rstd * m) + (p.dr ? dr.at(i) : 0.0f);
+            store8(static_cast<H *>(p.dx) + row * p.lddx + c, n, p.wide, dx);
         }
     }
     if (p.part)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int64_t c = (int64_t)(v * T + threadIdx.x) * 8;
-            const int n = in_row(p.cols, c);
-            for (int i = 0; i < n; ++i)
-                p.part[(int64_t)blockIdx.x * p.cols + c + i] = dw[v][i];
-        }
+        for (int i = 0; i < n; ++i)
+            p.part[(int64_t)blockIdx.x * p.cols + c + i] = dw[i];
 }
 
 // Rows too long for the registers: dw's sums live in the workspace between
@@ -318,26 +344,26 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_long_kernel(const BackP
     }
 }
 
-// dw from the CTAs' sums: 32 columns to a CTA, its 8 warps take every eighth
+// dw from the CTAs' sums: 32 columns to a CTA, its 32 warps take every 32nd
 // sum, then the warps in order.
 template <class W>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
     dw_kernel(const float *part, int64_t parts, int64_t cols, W *dw, int add)
 {
-    __shared__ float sh[8][32];
+    __shared__ float sh[32][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (c < cols)
 #pragma unroll 8
-        for (int64_t k = warp; k < parts; k += 8)
+        for (int64_t k = warp; k < parts; k += 32)
             s += part[k * cols + c];
     sh[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < cols) {
         s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w)
+        for (int w = 0; w < 32; ++w)
             s += sh[w][lane];
         dw[c] = from_f32<W>(add ? to_f32(dw[c]) + s : s);
     }
@@ -359,15 +385,15 @@ static int launch_backward(const BackParams &p, int64_t parts, cudaStream_t stre
         return launch_status();
     };
     if (p.cols <= 256)
-        return go(rmsnorm_backward_kernel<H, 1, 32>, 32);
+        return go(rmsnorm_backward_kernel<H, 32>, 32);
     if (p.cols <= 1024)
-        return go(rmsnorm_backward_kernel<H, 1, 128>, 128);
+        return go(rmsnorm_backward_kernel<H, 128>, 128);
     if (p.cols <= 2048)
-        return go(rmsnorm_backward_kernel<H, 1, 256>, 256);
+        return go(rmsnorm_backward_kernel<H, 256>, 256);
     if (p.cols <= 4096)
-        return go(rmsnorm_backward_kernel<H, 1, 512>, 512);
+        return go(rmsnorm_backward_kernel<H, 512>, 512);
     if (p.cols <= 8192)
-        return go(rmsnorm_backward_kernel<H, 1, 1024>, 1024);
+        return go(rmsnorm_backward_kernel<H, 1024>, 1024);
     return go(rmsnorm_backward_long_kernel<H>, 1024);
 }
 
@@ -496,7 +522,7 @@ int zero_rmsnorm_backward(const void *dy, int64_t lddy, const void *h, int64_t l
     if (!dw)
         return ZERO_OK;
     auto finish = [&](auto *out) {
-        dw_kernel<<<(unsigned)ceil_div(cols, 32), 256, 0, stream>>>(p.part, rows > 0 ? parts : 0, cols,
+        dw_kernel<<<(unsigned)ceil_div(cols, 32), 1024, 0, stream>>>(p.part, rows > 0 ? parts : 0, cols,
                                                                   out, add_dw ? 1 : 0);
         return launch_status();
     };

@@ -20,6 +20,7 @@ namespace zo {
 
 constexpr int kThreads = 256;
 constexpr int kUnit = 8;                  // elements of one wide access
+constexpr int kBatch = 4;                 // wide accesses of a thread in flight
 constexpr int64_t kMinChunk = 4096;       // elements
 constexpr int64_t kTargetChunks = 16384;  // of a whole list
 constexpr int kCapacity = 1024;           // tensors per launch
@@ -102,16 +103,27 @@ __device__ __forceinline__ float2 sum_chunk(const T *p, int64_t n, float inv)
     for (int i = 0; i < kUnit; ++i)
         acc[i] = 0.0f;
     const bool wide = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
-#pragma unroll 4
-    for (int64_t u = threadIdx.x; u * kUnit < n; u += kThreads) {
-        const int64_t left = n - u * kUnit;
-        float x[kUnit];
-        load8(p + u * kUnit, left < kUnit ? (int)left : kUnit, wide, x);
+    auto add = [&](const Raw8<T> &x) {
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
-            const float g = __fmul_rn(x[i], inv);
+            const float g = __fmul_rn(x.at(i), inv);
             acc[i] = fmaf(g, g, acc[i]);
         }
+    };
+    int64_t u = threadIdx.x;
+    if (wide)  // kBatch loads in flight
+        for (; (u + (kBatch - 1) * kThreads + 1) * kUnit <= n; u += kBatch * kThreads) {
+            Raw8<T> x[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                x[k] = load_full<false>(p + (u + k * kThreads) * kUnit);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                add(x[k]);
+        }
+    for (; u * kUnit < n; u += kThreads) {
+        const int64_t left = n - u * kUnit;
+        add(load_raw(p + u * kUnit, left < kUnit ? (int)left : kUnit, wide));
     }
     float2 s = make_float2(acc[0], 0.0f);
 #pragma unroll
@@ -268,13 +280,41 @@ __global__ void __launch_bounds__(kThreads)
 
 // ------------------------------------------------------------------ clip
 
+// Eight scaled elements to a 16-byte aligned p; nothing reads them here again.
+template <class U, class T>
+__device__ __forceinline__ void put(U *p, const Raw8<T> &x, float f)
+{
+    uint32_t w[Raw8<U>::kWords];
+    if constexpr (sizeof(U) == 4)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = __float_as_uint(__fmul_rn(x.at(i), f));
+    else
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = word_of<U>(__fmul_rn(x.at(2 * i), f), __fmul_rn(x.at(2 * i + 1), f));
+#pragma unroll
+    for (int i = 0; i < Raw8<U>::kWords / 4; ++i)
+        __stcs(reinterpret_cast<uint4 *>(p) + i, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+}
+
 template <class T, class U>
 __device__ __forceinline__ void scale_chunk(const T *p, U *o, int64_t n, float f)
 {
     const bool wide = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
     const bool wide_out = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
-#pragma unroll 4
-    for (int64_t u = threadIdx.x; u * kUnit < n; u += kThreads) {
+    int64_t u = threadIdx.x;
+    if (wide && wide_out)
+        for (; (u + (kBatch - 1) * kThreads + 1) * kUnit <= n; u += kBatch * kThreads) {
+            Raw8<T> x[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                x[k] = load_full<true>(p + (u + k * kThreads) * kUnit);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                put(o + (u + k * kThreads) * kUnit, x[k], f);
+        }
+    for (; u * kUnit < n; u += kThreads) {
         const int64_t left = n - u * kUnit;
         const int m = left < kUnit ? (int)left : kUnit;
         float x[kUnit];
@@ -300,10 +340,12 @@ __global__ void __launch_bounds__(kThreads)
         c = fminf(1.0f, __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f)));
     }
     const float f = __fmul_rn(inv, c);
-    const int t = find_tensor(l, blockIdx.x);
+    // from the list's end backwards: what the norm read last is still in L2
+    const uint32_t chunk = gridDim.x - 1 - blockIdx.x;
+    const int t = find_tensor(l, chunk);
     if (f == 1.0f && l.out[t] == l.x[t])
         return;  // in place and unchanged
-    const int64_t at = (int64_t)(blockIdx.x - l.first[t]) * l.chunk;
+    const int64_t at = (int64_t)(chunk - l.first[t]) * l.chunk;
     const int64_t left = l.numel[t] - at;
     const int64_t n = left < l.chunk ? left : l.chunk;
     by_type(l.type[t], l.x[t], at, [&](auto *p) {
