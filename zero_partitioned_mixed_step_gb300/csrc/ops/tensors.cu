@@ -22,7 +22,7 @@ constexpr int kThreads = 256;
 constexpr int kUnit = 8;                  // elements of one wide access
 constexpr int kBatch = 4;                 // wide accesses of a thread in flight
 constexpr int64_t kMinChunk = 4096;       // elements
-constexpr int64_t kTargetChunks = 16384;  // of a whole list
+constexpr int64_t kTargetChunks = 8192;  // of a whole list
 constexpr int kCapacity = 1024;           // tensors per launch
 constexpr int kHeader = 256;              // bytes of the workspace ahead of the chunk sums
 
