@@ -50,14 +50,22 @@ struct MatmulParams {
     uint32_t instr;
 };
 
-template <int CG, int NH>
+template <int CG, int NH, bool TILE_B>
 struct Shape {
     // two groups leave no registers to spare: whole warpgroups, so that the
     // copying one can give some of its own (168 x 384 = 216 x 256 + 72 x 128)
     static constexpr int kThreads = NH == 1 ? 224 : 384;
     static constexpr int kTileM = 128 * CG, kTileN = 128 * NH;
-    static constexpr int kRowsB = 128 / CG;  // of each 128 rows of B, in one CTA
-    static constexpr int kBytesA = 128 * 128, kBytesB = NH * kRowsB * 128;
+    // Tensor-core products (and warps that issue them) for a block: one for
+    // each group, so that one group's columns are ready while the other's are
+    // being made, or one for all columns, which reads A from shared memory
+    // once.  Where a block's scaling is short (a scale for the tile) the first
+    // is faster, where it is long (one for each column) the second:
+    // 8192x14336x4096 395 and 422 us, 14336x4096x8192 into fp32 598 and 565.
+    static constexpr int kProducts = TILE_B ? NH : 1;
+    static constexpr int kN = kTileN / kProducts;  // columns of a product
+    static constexpr int kRowsB = kN / CG;         // of a product's rows of B, in one CTA
+    static constexpr int kBytesA = 128 * 128, kBytesB = kProducts * kRowsB * 128;
     static constexpr int kStageBytes = kBytesA + kBytesB;
     static constexpr int kStages = (224 * 1024 - NH * 2 * kStage - 4096) / kStageBytes;
     static constexpr int kBufs = NH == 1 ? 4 : 2;               // sums of 128 x 128 for each group
@@ -286,15 +294,15 @@ __device__ __forceinline__ void write_tile(const MatmulParams &p, const void *ma
 }
 
 template <int CG, int NH, bool TILE_B>
-__global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
+__global__ void __launch_bounds__(Shape<CG, NH, TILE_B>::kThreads, 1)
     matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                   const __grid_constant__ CUtensorMap map_out, const __grid_constant__ MatmulParams p)
 {
-    using S = Shape<CG, NH>;
-    constexpr int kStages = S::kStages;
+    using S = Shape<CG, NH, TILE_B>;
+    constexpr int kStages = S::kStages, P = S::kProducts;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
-    __shared__ __align__(8) uint64_t sum_full[NH][S::kBufs], sum_empty[NH][S::kBufs], drain_bar[NH];
+    __shared__ __align__(8) uint64_t sum_full[P][S::kBufs], sum_empty[P][S::kBufs], drain_bar[P];
     __shared__ __align__(8) uint64_t scale_full[kGroups], scale_empty[kGroups];
     __shared__ __align__(16) float scale_a[kGroups][kGroup][128];
     __shared__ __align__(16) float scale_b[kGroups][kGroup][TILE_B ? NH : NH * 128];
@@ -310,18 +318,18 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
         gave_up_sh = 0;
         for (int i = 0; i < kStages; ++i) {
             bar_init(smem_u32(&full_bar[i]), 1);
-            bar_init(smem_u32(&empty_bar[i]), NH);
+            bar_init(smem_u32(&empty_bar[i]), P);
         }
         for (int i = 0; i < S::kBufs; ++i)
-            for (int h = 0; h < NH; ++h) {
+            for (int h = 0; h < P; ++h) {
                 bar_init(smem_u32(&sum_full[h][i]), 1);
-                bar_init(smem_u32(&sum_empty[h][i]), 4 * CG);
+                bar_init(smem_u32(&sum_empty[h][i]), 4 * CG * NH / P);
             }
         for (int i = 0; i < kGroups; ++i) {
             bar_init(smem_u32(&scale_full[i]), 1);
             bar_init(smem_u32(&scale_empty[i]), 4 * NH);
         }
-        for (int h = 0; h < NH; ++h)
+        for (int h = 0; h < P; ++h)
             bar_init(smem_u32(&drain_bar[h]), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -359,8 +367,8 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
                         full = map_to(full, 0);
                     tma_load<CG>(a, &map_a, kb * 128, row_a, full);
 #pragma unroll
-                    for (int h = 0; h < NH; ++h)
-                        tma_load<CG>(b + h * S::kRowsB * 128, &map_b, kb * 128, row_b + h * 128, full);
+                    for (int h = 0; h < P; ++h)
+                        tma_load<CG>(b + h * S::kRowsB * 128, &map_b, kb * 128, row_b + h * S::kN, full);
                     issued = issued < kStages ? issued + 1 : kStages;
                     if (++st == kStages) {
                         st = 0;
@@ -379,11 +387,10 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
                             break;
                 }
         }
-        } else if (warp == 4 * NH + 1 || warp == 4 * NH + 3) {
+        } else if (warp == 4 * NH + 1 || (P == 2 && warp == 4 * NH + 3)) {
         // ---------------------------------------------------------- products
-        // A warp for each half of the tile's columns: a poll of a barrier takes
-        // about 150 cycles, and one thread's polls for both halves took 790 a
-        // block.  (With one half there is no fourth warp.)
+        // A warp for each of the block's products: a poll of a barrier takes about
+        // 150 cycles, and one thread's polls for two took 790 a block.
         const int h = warp == 4 * NH + 1 ? 0 : 1;
         if (rank == 0 && elect_one()) {
             const uint32_t instr = p.instr, sums = smem_u32(&sum_full[h][0]), frees = smem_u32(&sum_empty[h][0]);
@@ -404,7 +411,7 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
                     const uint64_t da = smem_desc(a), db = smem_desc(a + S::kBytesA + h * S::kRowsB * 128);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_f8<CG>(tmem + (buf * NH + h) * 128, da + k * 2, db + k * 2, instr, k > 0);
+                        mma_f8<CG>(tmem + buf * S::kTileN + h * S::kN, da + k * 2, db + k * 2, instr, k > 0);
                     mma_commit<CG>(sums + buf * 8);
                     mma_commit<CG>(smem_u32(&empty_bar[st]));
                     if (++st == kStages) {
@@ -469,9 +476,10 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
         const int h = warp >> 2, quad = warp & 3, t = threadIdx.x & 127, id = 1 + h;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         uint8_t *stage = staging + h * 2 * kStage;
-        const uint32_t full = smem_u32(&sum_full[h][0]), scale_there = smem_u32(&scale_full[0]);
+        const int product = P == 1 ? 0 : h;
+        const uint32_t full = smem_u32(&sum_full[product][0]), scale_there = smem_u32(&scale_full[0]);
         const uint32_t scale_free = smem_u32(&scale_empty[0]);
-        uint32_t free = smem_u32(&sum_empty[h][0]);
+        uint32_t free = smem_u32(&sum_empty[product][0]);
         if (CG == 2)
             free = map_to(free, 0);
         int buf = 0, slot = 0, in_group = 0;
@@ -485,10 +493,9 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 128; ++i)
                 acc[i] = 0.0f;
-            // Per block: 4 x 32 columns through two register buffers.  (Loading
-            // the next block's first columns ahead of the loop's end keeps
-            // them in registers over it, and the compiler copies them there.)
-            uint32_t r[2][32];
+            // Per block: 4 x 32 columns through registers.  (Loading the next
+            // block's first columns ahead of the loop's end keeps them in
+            // registers over it, and the compiler copies them there.)
             auto column = [&](int c) { return lanes + (uint32_t)((buf * NH + h) * 128 + c * 32); };
             bool ready = false;
             for (int kb = w.kb0; kb < w.kb1; ++kb) {
@@ -498,49 +505,67 @@ __global__ void __launch_bounds__(Shape<CG, NH>::kThreads, 1)
                 if (!ok)
                     break;
                 fence_after();
-                tmem_ld32(column(0), r[0]);
-                tmem_ld32(column(1), r[1]);
-                // the block's scale of this thread's row (times the tile's)
-                const float ab = TILE_B ? scale_a[slot][in_group][t] * scale_b[slot][in_group][h]
-                                        : scale_a[slot][in_group][t];
-                const float4 *sb = reinterpret_cast<const float4 *>(&scale_b[slot][in_group][TILE_B ? 0 : h * 128]);
-                auto add = [&](int c) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float *o = acc + c * 32 + i * 4;
-                        const uint32_t *x = r[c & 1] + i * 4;
-                        if (TILE_B) {
-                            scale_add(o[0], x[0], ab);
-                            scale_add(o[1], x[1], ab);
-                            scale_add(o[2], x[2], ab);
-                            scale_add(o[3], x[3], ab);
-                        } else {
-                            const float4 s = sb[c * 8 + i];
-                            const float2 lo = mul2(ab, s.x, s.y), hi = mul2(ab, s.z, s.w);
-                            scale_add(o[0], x[0], lo.x);
-                            scale_add(o[1], x[1], lo.y);
-                            scale_add(o[2], x[2], hi.x);
-                            scale_add(o[3], x[3], hi.y);
-                        }
-                    }
-                };
+                const float *sa_row = &scale_a[slot][in_group][t];
                 const int next_buf = buf + 1 == S::kBufs ? 0 : buf + 1;
                 const uint32_t next_phase = phase ^ (next_buf == 0);
                 const int next_slot = slot + 1 == kGroups ? 0 : slot + 1;
                 const uint32_t next_scale_phase = scale_phase ^ (next_slot == 0);
                 const bool group_ends = in_group + 1 == kGroup;
-                tmem_wait();
-                add(0);
-                tmem_ld32(column(2), r[0]);
-                add(1);
-                tmem_ld32(column(3), r[1]);
-                tmem_wait();
-                fence_before();
-                bar_arrive_lane0<CG>(free + buf * 8, lane);
-                const bool peek = bar_test(full + next_buf * 8, next_phase) &&
-                                  (!group_ends || bar_test(scale_there + next_slot * 8, next_scale_phase));
-                add(2);
-                add(3);
+                bool peek = false;
+                auto release = [&] {  // every column is in registers
+                    fence_before();
+                    bar_arrive_lane0<CG>(free + buf * 8, lane);
+                    peek = bar_test(full + next_buf * 8, next_phase) &&
+                           (!group_ends || bar_test(scale_there + next_slot * 8, next_scale_phase));
+                };
+                if (TILE_B) {
+                    // one scale for all: two register buffers of 32 columns
+                    uint32_t r[2][32];
+                    tmem_ld32(column(0), r[0]);
+                    tmem_ld32(column(1), r[1]);
+                    const float ab = *sa_row * scale_b[slot][in_group][h];
+                    auto add = [&](int c) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            scale_add(acc[c * 32 + i], r[c & 1][i], ab);
+                    };
+                    tmem_wait();
+                    add(0);
+                    tmem_ld32(column(2), r[0]);
+                    add(1);
+                    tmem_ld32(column(3), r[1]);
+                    tmem_wait();
+                    release();
+                    add(2);
+                    add(3);
+                } else {
+                    // a scale for each column: the other buffer's registers hold
+                    // 32 of them, loaded while the sums are on their way (read
+                    // at their use, each load was waited for)
+                    const float a = *sa_row;
+                    const float4 *sb = reinterpret_cast<const float4 *>(&scale_b[slot][in_group][h * 128]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t r[32];
+                        tmem_ld32(column(c), r);
+                        float4 s[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            s[i] = sb[c * 8 + i];
+                        tmem_wait();
+                        if (c == 3)
+                            release();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 lo = mul2(a, s[i].x, s[i].y), hi = mul2(a, s[i].z, s[i].w);
+                            float *o = acc + c * 32 + i * 4;
+                            scale_add(o[0], r[i * 4], lo.x);
+                            scale_add(o[1], r[i * 4 + 1], lo.y);
+                            scale_add(o[2], r[i * 4 + 2], hi.x);
+                            scale_add(o[3], r[i * 4 + 3], hi.y);
+                        }
+                    }
+                }
                 ready = __all_sync(0xFFFFFFFFu, peek);
                 if (group_ends) {
                     __syncwarp();
@@ -974,6 +999,13 @@ static Plan plan_of(int64_t m, int64_t n, int64_t k)
     return r;
 }
 
+// The operands as the tensor maps need them.
+struct Operands {
+    const void *a, *b;
+    int64_t lda, ldb, k;
+    int a_type, b_type;
+};
+
 // Lets a kernel use that much shared memory, once for each device (bits of `ready`).
 static cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &ready)
 {
@@ -987,15 +1019,26 @@ static cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_
     return e;
 }
 
-template <int CG, int NH>
-static int launch_matmul(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o, const MatmulParams &p,
-                         bool tile_b, cudaStream_t stream)
+template <int CG, int NH, bool TILE_B>
+static int launch_matmul(MatmulParams p, const Operands &o, cudaStream_t stream)
 {
-    using S = Shape<CG, NH>;
-    auto kernel = tile_b ? matmul_kernel<CG, NH, true> : matmul_kernel<CG, NH, false>;
+    using S = Shape<CG, NH, TILE_B>;
+    auto kernel = matmul_kernel<CG, NH, TILE_B>;
+    p.instr = f8_instr(o.a_type == ZERO_T_E5M2, o.b_type == ZERO_T_E5M2, S::kTileM, S::kN);
+    CUtensorMap a, b, out{};
+    int rc = encode(&a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, o.a, p.m, o.k, o.lda, 128);
+    if (!rc)
+        rc = encode(&b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, o.b, p.n, o.k, o.ldb, S::kRowsB);
+    if (!rc && p.tma_out)
+        rc = encode(&out, p.out_type == ZERO_T_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                          : p.out_type == ZERO_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                    type_bytes(p.out_type), p.out, p.m, p.n, p.ldo, 128);
+    if (rc)
+        return rc;
     static_assert(S::kSmem <= 227 * 1024 - 4096, "shared memory");
-    static std::atomic<uint64_t> ready[2];
-    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), S::kSmem, ready[tile_b]);
+    static std::atomic<uint64_t> ready;
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), S::kSmem, ready);
     if (e != cudaSuccess)
         return cuda_error(e);
     const int64_t units = p.units;
@@ -1010,18 +1053,24 @@ static int launch_matmul(const CUtensorMap &a, const CUtensorMap &b, const CUten
     attr.val.clusterDim = {CG, 1, 1};
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, a, b, o, p);
+    e = cudaLaunchKernelEx(&cfg, kernel, a, b, out, p);
     return e == cudaSuccess ? launch_status() : cuda_error(e);
 }
 
-template <int TN>
-static int launch_few(const CUtensorMap &a, const CUtensorMap &b, const MatmulParams &p, bool tile_b,
-                      cudaStream_t stream)
+template <int TN, bool TILE_B>
+static int launch_few(MatmulParams p, const Operands &o, cudaStream_t stream)
 {
     using S = Few<TN>;
-    auto kernel = tile_b ? matmul_few_kernel<TN, true> : matmul_few_kernel<TN, false>;
-    static std::atomic<uint64_t> ready[2];
-    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), S::kSmem, ready[tile_b]);
+    auto kernel = matmul_few_kernel<TN, TILE_B>;
+    p.instr = f8_instr(o.b_type == ZERO_T_E5M2, o.a_type == ZERO_T_E5M2, 128, TN);
+    CUtensorMap a, b;
+    int rc = encode(&a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, o.a, p.m, o.k, o.lda, TN);
+    if (!rc)
+        rc = encode(&b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, o.b, p.n, o.k, o.ldb, 128);
+    if (rc)
+        return rc;
+    static std::atomic<uint64_t> ready;
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), S::kSmem, ready);
     if (e != cudaSuccess)
         return cuda_error(e);
     const int most = 2 * device_sms();
@@ -1038,6 +1087,18 @@ static int launch_few(const CUtensorMap &a, const CUtensorMap &b, const MatmulPa
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kernel, a, b, p);
     return e == cudaSuccess ? launch_status() : cuda_error(e);
+}
+
+template <bool TILE_B>
+static int launch(const Plan &plan, const MatmulParams &p, const Operands &o, cudaStream_t stream)
+{
+    switch (plan.few) {
+    case 16: return launch_few<16, TILE_B>(p, o, stream);
+    case 32: return launch_few<32, TILE_B>(p, o, stream);
+    case 64: return launch_few<64, TILE_B>(p, o, stream);
+    default: break;
+    }
+    return plan.pair ? launch_matmul<2, 2, TILE_B>(p, o, stream) : launch_matmul<1, 1, TILE_B>(p, o, stream);
 }
 
 }  // namespace zo
@@ -1110,29 +1171,10 @@ int zero_fp8_matmul(const void *a, int a_type, int64_t lda, const float *sa, int
     p.units = (int32_t)units;
     p.out_type = out_type;
     p.add = add ? 1 : 0;
-    const int fa = a_type == ZERO_T_E5M2, fb = b_type == ZERO_T_E5M2;
-    p.instr = plan.few ? f8_instr(fb, fa, 128, plan.few) : f8_instr(fa, fb, plan.pair ? 256 : 128, 128);
     // a TMA store (or reduction) of whole boxes; half types are added in fp32 and rounded once
     p.tma_out = rows_aligned(out, ldo, ob, 16) && (!add || out_type == ZERO_T_F32);
-    CUtensorMap ma, mb, mo{};
-    rc = encode(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a, m, k, lda, plan.few ? plan.few : 128);
-    if (!rc)
-        rc = encode(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, b, n, k, ldb, plan.pair ? 64 : 128);
-    if (!rc && p.tma_out && !plan.few)
-        rc = encode(&mo, out_type == ZERO_T_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                         : out_type == ZERO_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                    ob, out, m, n, ldo, 128);
-    if (rc)
-        return rc;
-    if (plan.few == 16)
-        return launch_few<16>(ma, mb, p, b_tile != 0, stream);
-    if (plan.few == 32)
-        return launch_few<32>(ma, mb, p, b_tile != 0, stream);
-    if (plan.few == 64)
-        return launch_few<64>(ma, mb, p, b_tile != 0, stream);
-    return plan.pair ? launch_matmul<2, 2>(ma, mb, mo, p, b_tile != 0, stream)
-                     : launch_matmul<1, 1>(ma, mb, mo, p, b_tile != 0, stream);
+    const Operands o{a, b, lda, ldb, k, a_type, b_type};
+    return b_tile ? launch<true>(plan, p, o, stream) : launch<false>(plan, p, o, stream);
 }
 
 }  // extern "C"
