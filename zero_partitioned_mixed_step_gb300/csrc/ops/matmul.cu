@@ -199,57 +199,60 @@ __device__ __forceinline__ void write_tma(const MatmulParams &p, const void *map
 }
 
 // The same for rows that no TMA store can write (their starts are not on
-// 16-byte boundaries): the staged rows leave in the destination's own 16-byte
-// pieces, each gathered from the staging buffers, the ends element by element.
+// 16-byte boundaries).  Each thread stages its row turned by the row's own
+// distance from a boundary, so that the destination's 16-byte pieces lie whole
+// in the staged words; the rows' ends leave element by element.  (Gathering
+// the pieces from rows staged as they are took 8 two-byte reads for each:
+// 1021x50257x769 109 us, 9X here.)
 template <class T>
-__device__ __forceinline__ void write_gather(const MatmulParams &p, const float acc[128], uint8_t *stage, int id,
+__device__ __forceinline__ void write_turned(const MatmulParams &p, const float acc[128], uint8_t *stage, int id,
                                              int t, int m0, int n0)
 {
-    constexpr int kCols = 2 * kStage / 128 / (int)sizeof(T);  // columns staged at a time
     constexpr int kPiece = 16 / (int)sizeof(T);
-    constexpr int kPieces = kCols / kPiece;  // of a row: 16
-    static_assert(kPieces == 16, "16 threads to a row");
-    constexpr int kPitch = kCols * (int)sizeof(T);
+    constexpr int kCols = 16 * kPiece;  // columns at a time: 64 words of a row
+    uint32_t *words = reinterpret_cast<uint32_t *>(stage);
+    // word w of a row lies where 32 rows' same words meet different banks
+    auto word = [&](int row, int w) -> uint32_t & { return words[row * 64 + (w ^ (row & 31))]; };
+    auto off_boundary = [&](const T *o) { return (int)(reinterpret_cast<uintptr_t>(o) / sizeof(T) % kPiece); };
+    T *first = static_cast<T *>(p.out) + (int64_t)m0 * p.ldo + n0;
 #pragma unroll
-    for (int c = 0; c < 128; c += kCols) {
+    for (int c = 0; c < 128; c += kCols, first += kCols) {
         if (c > 0)
             barrier_of(id, 128);  // the last readers are done
+        const int turn = off_boundary(first + (int64_t)t * p.ldo);
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-            *reinterpret_cast<uint4 *>(stage + t * kPitch + ((i ^ (t & 7)) << 4)) = pack16<T>(acc + c + i * kPiece);
+            for (int i = 0; i < 64; ++i)
+                word(t, (i + turn) & 63) = __float_as_uint(acc[c + i]);
+        } else {
+            const bool odd = turn & 1;
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+                word(t, (i + (turn >> 1)) & 63) = word_of<T>(odd ? acc[(2 * i + 127) & 127] : acc[2 * i],
+                                                             odd ? acc[2 * i] : acc[2 * i + 1]);
+        }
         barrier_of(id, 128);
         const int n = min(kCols, p.n - n0 - c);
-        auto value = [&](int row, int k) {
-            const int b = k * (int)sizeof(T);
-            return *reinterpret_cast<const T *>(stage + row * kPitch + (((b >> 4) ^ (row & 7)) << 4) + (b & 15));
-        };
-        auto head_of = [&](const T *o) {  // elements ahead of the row's first whole piece
-            return (int)((uintptr_t)(-(intptr_t)reinterpret_cast<uintptr_t>(o)) / sizeof(T) % kPiece);
-        };
-        T *first = static_cast<T *>(p.out) + (int64_t)m0 * p.ldo + n0 + c;
-        // whole pieces: 16 threads to a row
         T *o = first + (int64_t)(t >> 4) * p.ldo;
+        const int lane = t & 15;
 #pragma unroll 4
         for (int row = t >> 4; row < 128; row += 8, o += 8 * p.ldo) {
-            const int at = head_of(o) + (t & 15) * kPiece;
-            if (m0 + row < p.m && at + kPiece <= n) {
-                alignas(16) T v[kPiece];
-#pragma unroll
-                for (int k = 0; k < kPiece; ++k)
-                    v[k] = value(row, at + k);
-                *reinterpret_cast<uint4 *>(o + at) = *reinterpret_cast<const uint4 *>(v);
-            }
-        }
-        // the rows' ends: a thread to a row
-        if (m0 + t < p.m && n > 0) {
-            o = first + (int64_t)t * p.ldo;
-            const int head = min(head_of(o), n), tail = head + (n - head) / kPiece * kPiece;
-#pragma unroll
-            for (int k = 0; k < kPiece - 1; ++k) {
-                if (k < head)
-                    o[k] = value(t, k);
-                if (tail + k < n)
-                    o[tail + k] = value(t, tail + k);
+            if (m0 + row >= p.m || n <= 0)
+                continue;
+            const int at = off_boundary(o), begin = lane * kPiece - at;  // this thread's piece
+            if (begin >= 0 && begin + kPiece <= n)
+                *reinterpret_cast<uint4 *>(o + begin) =
+                    make_uint4(word(row, lane * 4), word(row, lane * 4 + 1), word(row, lane * 4 + 2),
+                               word(row, lane * 4 + 3));
+            // one of the at most 2 (kPiece - 1) elements outside whole pieces
+            const int head = min((kPiece - at) % kPiece, n), tail = head + (n - head) / kPiece * kPiece;
+            const int k = lane < 8 ? lane : tail + lane - 8;
+            if (lane < 8 ? lane < head : k < n) {
+                const int place = (k + at) & (kCols - 1);
+                if constexpr (sizeof(T) == 4)
+                    o[k] = __uint_as_float(word(row, place));
+                else
+                    reinterpret_cast<uint16_t *>(o)[k] = (uint16_t)(word(row, place >> 1) >> (16 * (place & 1)));
             }
         }
     }
@@ -290,7 +293,7 @@ __device__ __forceinline__ void write_tile(const MatmulParams &p, const void *ma
     else if (p.add)
         write_add<T>(p, acc, stage, id, t, m0, n0);
     else
-        write_gather<T>(p, acc, stage, id, t, m0, n0);
+        write_turned<T>(p, acc, stage, id, t, m0, n0);
 }
 
 template <int CG, int NH, bool TILE_B>
