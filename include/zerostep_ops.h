@@ -22,8 +22,8 @@
  * row's end and the next row are neither read nor written.  An input may not
  * overlap an output unless its description allows it.  A pointer must be
  * aligned to its element; rows that start on 16-byte boundaries run with wide
- * accesses (zero_fp8_matmul requires them).  Sizes are 0 .. 2^31 - 1 per
- * dimension and offsets are formed in 64 bits.  All calls can be captured in
+ * accesses (zero_fp8_matmul requires them).  Sizes are 0 .. 2^31 - 1025
+ * per dimension and offsets are formed in 64 bits.  All calls can be captured in
  * a CUDA graph.  Results do not depend on the launch shape or on other work
  * on the GPU: no floating-point atomics, sums in a fixed order.
  *
@@ -35,9 +35,9 @@
  * be short.  s = max(amax / qmax, 2^-126), amax the largest magnitude of the
  * block and qmax the type's largest value (448 and 57344); q is X / s rounded
  * to nearest even (formed as X * (1 / s) in fp32).  A block of zeros has q = 0.
- * A block that holds a NaN or an infinity has s = NaN or infinity and stands
- * for NaN throughout (infinity where only some of it is: q * s is NaN there
- * too), so that what is computed from it is not finite and the step skips.
+ * A block that holds a NaN or an infinity has s = NaN or infinity, and q * s is
+ * NaN throughout it, so that what is computed from it is not finite and the
+ * step skips.
  */
 #ifndef ZEROSTEP_OPS_H
 #define ZEROSTEP_OPS_H
@@ -140,7 +140,9 @@ ZERO_API size_t zero_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k)
  *   weights' gradient:    a = transposed gradients [out, tokens],
  *                         b = transposed activations [in, tokens], both in 1x128 blocks
  *  a, b: 16-byte aligned, lda and ldb multiples of 16 (ZERO_EALIGN).
- *  k = 0 gives out = 0 (or leaves it, with add).
+ *  k = 0 gives out = 0 (or leaves it, with add).  A sum added to an fp32 out
+ *    whose rows start on 16-byte boundaries is flushed to zero where it is below
+ *    fp32's smallest normal number.
  */
 ZERO_API int zero_fp8_matmul(const void *a, int a_type, int64_t lda, const float *sa, int64_t ldsa,
                              const void *b, int b_type, int64_t ldb, const float *sb, int64_t ldsb,
@@ -157,7 +159,8 @@ ZERO_API int zero_fp8_matmul(const void *a, int a_type, int64_t lda, const float
  *  q, s: y (before its rounding to `type`) in 8 bits with a scale for each
  *    1x128 block, or both NULL.
  *  rstd: [rows] fp32, for the backward pass, or NULL.
- *  cols >= 1; eps >= 0.
+ *  cols >= 1; eps >= 0.  The squares are summed in fp32: a row whose squares
+ *    overflow it has rstd = 0.
  */
 ZERO_API int zero_rmsnorm_fp8(const void *x, int64_t ldx, const void *residual, int64_t ldr,
                               const void *w, int w_type, int type, int64_t rows, int64_t cols,

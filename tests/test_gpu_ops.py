@@ -300,15 +300,41 @@ def test_matmul_adds(m, n, k, to):
     check_product(out, a, sa, b, sb, before)
 
 
-@pytest.mark.parametrize("pad", [1, 3, 16])
-def test_matmul_output_strides_leave_the_gaps(pad):
-    m, n, k = 130, 259, 200
+@pytest.mark.parametrize("to", [F16, F32])
+@pytest.mark.parametrize("pad", [1, 2, 3, 5, 16])
+@pytest.mark.parametrize("m,n,k", [(50, 259, 200), (130, 259, 200), (2561, 2323, 130)])
+def test_matmul_output_strides_leave_the_gaps(m, n, k, pad, to):
     a, sa = operand(1, m, k, E4M3, False)
-    b, sb = operand(2, n, k, E4M3, True)
-    out = strided(torch.zeros(m, n, device="cuda", dtype=BF16), pad, 5.0)
+    b, sb = operand(2, n, k, E4M3, m > 1000)
+    out = strided(torch.zeros(m, n, device="cuda", dtype=to), pad, 5.0)
     zs.zero_fp8_matmul(a, sa, b, sb, out, workspace(m, n, k))
     check_product(out, a, sa, b, sb)
     assert (gap(out) == 5.0).all()
+
+
+@pytest.mark.parametrize("shift", [1, 2, 3, 7])
+def test_matmul_into_an_unaligned_output(shift):
+    m, n, k = 200, 300, 300
+    a, sa = operand(1, m, k, E4M3, False)
+    b, sb = operand(2, n, k, E4M3, True)
+    flat = torch.full((m * n + 16,), 5.0, dtype=BF16, device="cuda")
+    out = flat[shift:shift + m * n].view(m, n)
+    zs.zero_fp8_matmul(a, sa, b, sb, out, workspace(m, n, k))
+    check_product(out, a, sa, b, sb)
+    assert (flat[:shift] == 5).all() and (flat[shift + m * n:] == 5).all()
+
+
+def test_matmul_of_sizes_that_change_the_kernel():
+    """Each side of the rules on the rows and on the number of tiles."""
+    for m, n, k, tile in [(15, 700, 1000, True), (16, 700, 1000, False), (17, 700, 1000, True), (32, 130, 5000, False),
+                          (33, 130, 5000, True), (64, 513, 2000, False), (65, 513, 2000, True), (256, 19 * 256, 200, True),
+                          (256, 19 * 256 + 1, 200, False), (1024, 19 * 256, 200, False), (1025, 19 * 256, 200, True)]:
+        a, sa = operand(m, m, k, E4M3, False)
+        b, sb = operand(n, n, k, E5M2, tile)
+        out, ws = torch.empty(m, n, device="cuda"), workspace(m, n, k)
+        zs.zero_fp8_matmul(a, sa, b, sb, out, ws)
+        check_product(out, a, sa, b, sb)
+        assert int(ws[:4].sum()) == 0
 
 
 def test_matmul_reads_no_padding():

@@ -130,7 +130,7 @@ def test_matmul_refuses(lib):
                                    n, k, 0, ws, ws_bytes, None)
 
     assert call(at=BF16) == EINVAL and call(bt=F32) == EINVAL and call(ot=E4M3) == EINVAL
-    assert call(m=-1) == EINVAL and call(n=1 << 31) == EINVAL and call(k=-1) == EINVAL
+    assert call(m=-1) == EINVAL and call(n=(1 << 31) - 1) == EINVAL and call(k=-1) == EINVAL
     assert call(tile=2) == EINVAL and call(ws=None) == EINVAL and call(a=None) == EINVAL
     assert call(lda=255) == EINVAL and call(ldb=240) == EINVAL and call(ldo=129) == EINVAL
     assert call(ldsa=7) == EINVAL and call(ldsb=1) == EINVAL and call(tile=0) == EINVAL

@@ -19,7 +19,7 @@ namespace zo {
 
 constexpr int kBlock = 128;             // elements that share a scale
 constexpr float kTinyScale = 0x1p-126f;  // the smallest scale (and the largest 1 / s is 2^126)
-constexpr int64_t kMaxDim = INT64_C(0x7FFFFFFF);
+constexpr int64_t kMaxDim = INT64_C(0x7FFFFFFF) - 1024;  // a tile's end still fits 32 bits
 
 // ------------------------------------------------------------------ host
 
