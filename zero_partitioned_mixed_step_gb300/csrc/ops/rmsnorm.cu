@@ -219,7 +219,11 @@ struct BackParams {
     const void *dy, *h, *w, *dr;
     const float *rstd;
     void *dx;
-    float *part;  // [gridDim.x][cols] sums of dw
+    // [gridDim.x][cols] sums of dw.  Where 8 divides cols, the columns with c %
+    // 8 = 0 first, then those with 1 and so on, so that a warp's stores are side
+    // by side; else in order.  Column c is at c / 8 * unit + c % 8 * step.
+    float *part;
+    int64_t unit, step;
     int64_t lddy, ldh, lddr, lddx;
     int64_t rows, cols;
     float inv_cols;
@@ -230,9 +234,12 @@ struct BackParams {
 // A CTA takes every gridDim.x-th row, a thread the same 8 columns of each, so
 // dw's sums over the CTA's rows stay in registers.  The next row is on its way
 // while this one is reduced, and the halves stay packed, so that 1024 threads
-// fit an SM.  A row costs one barrier and two shuffled sums.  (8192x4096: 71.7
-// us without the next row's loads, 54.0 with them, 4.9 TB/s; two rows to a
-// barrier with 512 threads to an SM 54.6, three rows ahead 69.8.)
+// fit an SM.  A row costs one barrier and two shuffled sums.  The sums of dw go
+// out with a warp's 32 threads side by side, and dw's own kernel is launched
+// meanwhile.  8192x4096: 44.2 us without dw, 6.1 TB/s, and 47.7 with it, 5.6
+// TB/s (in column order and launched after the pass 54.0).  The next row's
+// loads took 18 us off; three rows ahead in registers cost 16, in a ring of
+// asynchronous copies 1; two rows to a barrier, 512 threads to an SM, 0.6.
 template <class H, int T>
 __global__ void __launch_bounds__(T, 1024 / T) rmsnorm_backward_kernel(const BackParams p)
 {
@@ -284,9 +291,10 @@ __global__ void __launch_bounds__(T, 1024 / T) rmsnorm_backward_kernel(const Bac
             store8(static_cast<H *>(p.dx) + row * p.lddx + c, n, p.wide, dx);
         }
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // dw's launch may begin
     if (p.part)
         for (int i = 0; i < n; ++i)
-            p.part[(int64_t)blockIdx.x * p.cols + c + i] = dw[i];
+            p.part[blockIdx.x * p.cols + threadIdx.x * p.unit + i * p.step] = dw[i];
 }
 
 // Rows too long for the registers: dw's sums live in the workspace between
@@ -299,7 +307,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_long_kernel(const BackP
     if (part)
         for (int64_t c = threadIdx.x * 8; c < p.cols; c += 1024 * 8)
             for (int i = 0; i < in_row(p.cols, c); ++i)
-                part[c + i] = 0.0f;
+                part[c / 8 * p.unit + i * p.step] = 0.0f;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
         const float rstd = p.rstd[row];
         const H *pdy = static_cast<const H *>(p.dy) + row * p.lddy;
@@ -314,8 +322,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_long_kernel(const BackP
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float xhat = h[i] * rstd;
-                if (part && i < n)
-                    part[c + i] = fmaf(dy[i], xhat, part[c + i]);
+                if (part && i < n) {
+                    float *sum = part + c / 8 * p.unit + i * p.step;
+                    *sum = fmaf(dy[i], xhat, *sum);
+                }
                 dot = fmaf(dy[i] * w[i], xhat, dot);
             }
         }
@@ -337,29 +347,56 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_long_kernel(const BackP
     }
 }
 
-// dw from the CTAs' sums: 32 columns to a CTA, its 32 warps take every 32nd
-// sum, then the warps in order.
-template <class W>
-__global__ void __launch_bounds__(1024)
-    dw_kernel(const float *part, int64_t parts, int64_t cols, W *dw, int add)
+// dw from the CTAs' sums: 8 places to a CTA, whose groups of 8 threads take
+// the sums in turn, then the warps in order.  Its launch does not wait for the
+// pass over the rows: its CTAs come as that pass's leave, and wait here.
+template <int kDwThreads, class W>
+__global__ void __launch_bounds__(kDwThreads)
+    dw_kernel(const float *part, int64_t parts, int64_t cols, int64_t step, W *dw, int add)
 {
-    __shared__ float sh[32][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    constexpr int kGroups = kDwThreads / 8;
+    __shared__ float sh[kGroups][8];
+    const int at = threadIdx.x & 7, group = threadIdx.x >> 3;
+    const int64_t place = (int64_t)blockIdx.x * 8 + at;
     float s = 0.0f;
-    if (c < cols)
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the sums are written and seen
+    if (place < cols)
 #pragma unroll 8
-        for (int64_t k = warp; k < parts; k += 32)
-            s += part[k * cols + c];
-    sh[warp][lane] = s;
+        for (int64_t k = group; k < parts; k += kGroups)
+            s += part[k * cols + place];
+    s += __shfl_xor_sync(0xFFFFFFFFu, s, 8);
+    s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
+    if ((threadIdx.x & 31) < 8)
+        sh[threadIdx.x >> 5][at] = s;
     __syncthreads();
-    if (warp == 0 && c < cols) {
+    if (threadIdx.x < 8 && place < cols) {
+        const int64_t c = step == 1 ? place : place % step * 8 + place / step;
         s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 32; ++w)
-            s += sh[w][lane];
+        for (int w = 0; w < kDwThreads / 32; ++w)
+            s += sh[w][at];
         dw[c] = from_f32<W>(add ? to_f32(dw[c]) + s : s);
     }
+}
+
+// Many sums of few columns want the threads of a CTA, few sums of many columns
+// the CTAs: 1216 sums of 1024 columns 17.7 us with 1024 threads (the whole
+// backward), 19.8 with 256; 304 of 4096 50.0 and 47.7; 152 of 8192 52.7 and 49.2.
+template <int kDwThreads, class W>
+static int launch_dw(const BackParams &p, int64_t sums, W *dw, int add, cudaStream_t stream)
+{
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ceil_div(p.cols, 8));
+    cfg.blockDim = dim3(kDwThreads);
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, dw_kernel<kDwThreads, W>, (const float *)p.part, sums,
+                                             p.cols, p.step, dw, add ? 1 : 0);
+    return e == cudaSuccess ? ZERO_OK : cuda_error(e);
 }
 
 // CTAs of the backward pass (and sums of dw in the workspace): a rule on the
@@ -501,6 +538,8 @@ int zero_rmsnorm_backward(const void *dy, int64_t lddy, const void *h, int64_t l
     p.lddx = lddx;
     p.rows = rows;
     p.cols = cols;
+    p.unit = cols % 8 == 0 ? 1 : 8;
+    p.step = cols % 8 == 0 ? cols / 8 : 1;
     p.inv_cols = 1.0f / (float)cols;
     p.w_type = w_type;
     p.wide = rows_aligned(dy, lddy, b, 16) && rows_aligned(h, ldh, b, 16) &&
@@ -514,10 +553,10 @@ int zero_rmsnorm_backward(const void *dy, int64_t lddy, const void *h, int64_t l
     }
     if (!dw)
         return ZERO_OK;
+    const int64_t sums = rows > 0 ? parts : 0;
     auto finish = [&](auto *out) {
-        dw_kernel<<<(unsigned)ceil_div(cols, 32), 1024, 0, stream>>>(p.part, rows > 0 ? parts : 0, cols,
-                                                                  out, add_dw ? 1 : 0);
-        return launch_status();
+        return sums > 512 ? launch_dw<1024>(p, sums, out, add_dw, stream)
+                          : launch_dw<256>(p, sums, out, add_dw, stream);
     };
     if (dw_type == ZERO_T_F16)
         return finish(static_cast<f16 *>(dw));
