@@ -270,7 +270,8 @@ def check_product(out, a, sa, b, sb, before=None):
 
 SIZES = [(1, 1, 1), (1, 8, 16), (1, 4096, 1024), (2, 129, 127), (16, 256, 128), (17, 1000, 129), (64, 384, 2048),
          (100, 257, 333), (128, 128, 128), (129, 255, 640), (255, 1, 300), (256, 512, 1024), (300, 1031, 769),
-         (1, 7, 20000), (513, 640, 4096), (2304, 2500, 300), (4097, 1290, 257), (2560, 2560, 1024)]
+         (1, 7, 20000), (513, 640, 4096), (2304, 2500, 300), (4097, 1290, 257), (2560, 2560, 1024), (1025, 2500, 300), (2304, 1290, 257),
+         (3001, 2567, 300), (4096, 2304, 640)]
 
 
 @pytest.mark.parametrize("tile", [True, False])
@@ -290,7 +291,8 @@ def test_matmul(m, n, k, tile):
 
 
 @pytest.mark.parametrize("to", [F16, BF16, F32])
-@pytest.mark.parametrize("m,n,k", [(3, 5, 7), (100, 300, 200), (256, 256, 512), (9, 640, 4000), (2400, 2504, 256)])
+@pytest.mark.parametrize("m,n,k", [(3, 5, 7), (100, 300, 200), (256, 256, 512), (9, 640, 4000), (2400, 2504, 256),
+                                   (1300, 2504, 256)])
 def test_matmul_adds(m, n, k, to):
     a, sa = operand(1, m, k, E5M2, False)
     b, sb = operand(2, n, k, E4M3, False)
@@ -302,7 +304,8 @@ def test_matmul_adds(m, n, k, to):
 
 @pytest.mark.parametrize("to", [F16, F32])
 @pytest.mark.parametrize("pad", [1, 2, 3, 5, 16])
-@pytest.mark.parametrize("m,n,k", [(50, 259, 200), (130, 259, 200), (2561, 2323, 130)])
+@pytest.mark.parametrize("m,n,k", [(50, 259, 200), (130, 259, 200), (2561, 2323, 130),
+                                   (1281, 2323, 130)])
 def test_matmul_output_strides_leave_the_gaps(m, n, k, pad, to):
     a, sa = operand(1, m, k, E4M3, False)
     b, sb = operand(2, n, k, E4M3, m > 1000)
@@ -328,7 +331,9 @@ def test_matmul_of_sizes_that_change_the_kernel():
     """Each side of the rules on the rows and on the number of tiles."""
     for m, n, k, tile in [(15, 700, 1000, True), (16, 700, 1000, False), (17, 700, 1000, True), (32, 130, 5000, False),
                           (33, 130, 5000, True), (64, 513, 2000, False), (65, 513, 2000, True), (256, 19 * 256, 200, True),
-                          (256, 19 * 256 + 1, 200, False), (1024, 19 * 256, 200, False), (1025, 19 * 256, 200, True)]:
+                          (256, 19 * 256 + 1, 200, False), (1024, 19 * 256, 200, False), (1025, 19 * 256, 200, True),
+                          (1024, 9 * 256, 200, True), (1024, 10 * 256, 200, True), (2048, 19 * 256, 200, False),
+                          (2049, 19 * 256, 200, True)]:
         a, sa = operand(m, m, k, E4M3, False)
         b, sb = operand(n, n, k, E5M2, tile)
         out, ws = torch.empty(m, n, device="cuda"), workspace(m, n, k)

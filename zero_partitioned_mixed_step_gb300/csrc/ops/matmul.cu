@@ -6,18 +6,29 @@
 // over k: each block's products go to tensor memory on their own (four
 // tcgen05 products of 32 bytes of k), from where the epilogue warps take them
 // into registers, acc = fma(part, sa * sb, acc).  Tensor memory holds two
-// blocks' sums, so the products of one block run while the last one's are
-// being scaled.
+// blocks' sums of 256 columns, so the products of one block run while the last
+// one's are being scaled.
 //
 // A CTA (or a pair of them on neighbouring SMs, which share B) has
 //   NH groups of four epilogue warps, each for 128 rows x 128 columns,
-//   a warp whose first thread issues the TMA copies into a ring of stages
-//   (128 rows of A and NH * 128 of B, 128 bytes of k each), and
-//   a warp whose first thread issues the products.
+//   a warp one of whose threads issues the TMA copies into a ring of stages
+//   (128 rows of A and NH * 128 of B over the pair, 128 bytes of k each),
+//   a warp or two with a thread that issues the products, and
+//   a warp that brings the scales.
 // The CTAs are persistent and walk the tiles.  All waits are bounded: the
 // role that gives up marks the workspace's error word, the others follow, the
 // copies and products in flight are waited for (again bounded) and tensor
 // memory is freed.
+//
+// What bounds it: a block of 256x256x128 is 512 cycles of products, and takes
+// about 930, since tensor memory has no room for a third block: the product
+// warp sees a buffer free only a barrier's poll (150 cycles) and a commit (300)
+// after it is.  8192x14336x4096 into bf16, a scale for a tile of b: 392 us, 2.45
+// PFLOP/s.  With a scale for each column of b the scaling itself, 128 products
+// and 128 sums of a thread for each block, is the longer:
+// 14336x4096x8192 added in fp32, 563 us, 1.71 PFLOP/s.
+//   1021x50257x769 into bf16, rows not on 16 bytes: 99 us (7 blocks of k to a
+//   tile: the output's way out is more than half of it)
 #include <cuda.h>
 
 #include <atomic>
@@ -467,7 +478,7 @@ __global__ void __launch_bounds__(Shape<CG, NH, TILE_B>::kThreads, 1)
             copy_wait<0>();
             __syncwarp();
             if (lane == 0)
-                bar_arrive<1>(smem_u32(&scale_full[slot]));
+                bar_arrive(smem_u32(&scale_full[slot]));
             if (++slot == kGroups) {
                 slot = 0;
                 phase ^= 1;
@@ -816,7 +827,7 @@ __global__ void __launch_bounds__(Few<TN>::kThreads, 2)
             copy_wait<0>();
             __syncwarp();
             if (lane == 0)
-                bar_arrive<1>(smem_u32(&scale_full[slot]));
+                bar_arrive(smem_u32(&scale_full[slot]));
             if (++slot == kGroups) {
                 slot = 0;
                 phase ^= 1;
@@ -969,9 +980,16 @@ static int encode(CUtensorMap *map, CUtensorMapDataType type, int bytes, const v
 }
 
 // How a product is cut: up to 64 rows, tiles of 128 rows of b with all of a's;
-// else pairs of CTAs on 256x256 tiles where there are enough of them for the
-// SMs; else single CTAs on 128x128 tiles.  Where the tiles are few, k is split
-// so that the parts fill the SMs (two CTAs to an SM with few rows).
+// else pairs of CTAs on 256x256 tiles or single CTAs on 128x128 tiles, by the
+// rounds that each takes on a GB300's SMs, a pair's as 3/2 of a single's (14.6
+// and 9.6 us for 4096 of k).  Where the tiles are few, k is split so that the
+// parts fill the SMs (two CTAs to an SM with few rows).  With k = 4096:
+//   1024x4096    pairs, 1 round, 24.7 us    singles, 2 rounds, 27.5
+//   2048x2560    pairs, 2 rounds, 39.2      singles, 3 rounds, 37.2
+//   2048x5120    pairs, 3 rounds, 55.5      singles, 5 rounds, 59.6
+//   128x50257    pairs, 3 rounds, 60.1      singles, 3 rounds, 46
+//   64x4096      12.4 with few rows' tiles, 14.6 with 128x128; unsplit 18.6
+//   512x1024x8192  18.6, unsplit 26.7;  16x4096x14336  16.7, unsplit 33.0
 struct Plan {
     int few;  // columns of the few-rows kernel's tiles, or 0
     bool pair;
@@ -984,7 +1002,9 @@ static Plan plan_of(int64_t m, int64_t n, int64_t k)
     Plan r{};
     const int64_t kb = ceil_div(k, kBlock);
     r.splits = 1;
-    if (m > 64 && ceil_div(m, 256) * ceil_div(n, 256) >= kPlanSms / 2) {
+    const int64_t pair_waves = ceil_div(ceil_div(m, 256) * ceil_div(n, 256), kPlanSms / 2);
+    const int64_t single_waves = ceil_div(ceil_div(m, 128) * ceil_div(n, 128), kPlanSms);
+    if (m > 64 && 3 * pair_waves < 2 * single_waves) {
         r.pair = true;
         r.tiles_m = ceil_div(m, 256);
         r.tiles_n = ceil_div(n, 256);

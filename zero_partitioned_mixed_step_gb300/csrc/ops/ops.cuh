@@ -94,12 +94,6 @@ __device__ __forceinline__ float from_f32<float>(float x)
 {
     return x;
 }
-// x rounded to T and back
-template <class T>
-__device__ __forceinline__ float rounded(float x)
-{
-    return to_f32(from_f32<T>(x));
-}
 
 // Eight neighbouring elements, kept in 32-bit words (halves two to a word: as
 // an array of halves the compiler gives each a register of its own).
@@ -261,7 +255,6 @@ template <class T>
 struct Amax {  // a half type
     uint32_t two = 0;
     __device__ __forceinline__ void add(uint32_t pair) { two = __vmaxu2(two, pair & 0x7FFF7FFFu); }
-    __device__ __forceinline__ void add(const Amax &o) { two = __vmaxu2(two, o.two); }
     __device__ __forceinline__ uint32_t bits() const
     {
         const uint16_t one = (uint16_t)max(two & 0xFFFFu, two >> 16);

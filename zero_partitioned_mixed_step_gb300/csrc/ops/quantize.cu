@@ -13,7 +13,7 @@
 // have to cover, and the ALU (half busy: two conversions and a rounding for
 // each element and form).
 //   8192x4096 bf16, both forms:  28.4 us, 4.8 TB/s (0.71 of the copy rate)
-//   14336x4096 fp32, 128x128 tiles, both forms:  41.6 us, 5.6 TB/s (0.83)
+//   14336x4096 bf16, 128x128 tiles, both forms:  41.6 us, 5.6 TB/s (0.83)
 #include "ops.cuh"
 
 namespace zo {

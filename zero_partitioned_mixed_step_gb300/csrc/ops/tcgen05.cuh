@@ -63,20 +63,17 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
                  : "memory");
 }
 
-// An arrival at a barrier of this CTA or, with CG = 2, of the pair's first
-// one.  What it orders is tensor memory (by the tcgen05 fences), so CTA scope
-// is enough: a release at cluster scope waits for the thread's other stores,
-// which measured three times the whole product's time.
-template <int CG>
+// An arrival at a barrier of this CTA.
 __device__ __forceinline__ void bar_arrive(uint32_t bar)
 {
-    if (CG == 1)
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-    else
-        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// The same by the one thread of a warp that passes lane 0, without a branch.
+// An arrival by the one thread of a warp that passes lane 0, without a branch,
+// at a barrier of this CTA or, with CG = 2, of the pair's first one (an address
+// from map_to).  What it orders is tensor memory (by the tcgen05 fences), so
+// CTA scope is enough: a release at cluster scope waits for the thread's other
+// stores, which measured three times the whole product's time.
 template <int CG>
 __device__ __forceinline__ void bar_arrive_lane0(uint32_t bar, int lane)
 {
@@ -88,7 +85,8 @@ __device__ __forceinline__ void bar_arrive_lane0(uint32_t bar, int lane)
                      "r"(lane) : "memory");
 }
 
-// One poll; the thread sleeps up to about 2 us in it.
+// One poll, about 150 cycles; the hardware may suspend the thread in it for a
+// time of its own choice.
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
@@ -98,7 +96,7 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
-// The same without sleeping.
+// The same, never suspended.
 __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
@@ -120,7 +118,9 @@ __device__ __forceinline__ void registers_down()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-constexpr int kWaitLimit = 1 << 20;  // polls: at most about two seconds asleep
+// Polls before a wait gives up: some 80 ms at 150 cycles each, where the longest
+// wait that ends is for a few blocks of a tile, microseconds.
+constexpr int kWaitLimit = 1 << 20;
 
 // Waits for a barrier's phase; false when the polls run out or another role of
 // the CTA has given up (*gave_up, in shared memory).
