@@ -23,12 +23,12 @@
 // What bounds it: a block of 256x256x128 is 512 cycles of products, and takes
 // about 930, since tensor memory has no room for a third block: the product
 // warp sees a buffer free only a barrier's poll (150 cycles) and a commit (300)
-// after it is.  8192x14336x4096 into bf16, a scale for a tile of b: 392 us, 2.45
+// after it is.  8192x14336x4096 into bf16, a scale for a tile of b: 395 us, 2.43
 // PFLOP/s.  With a scale for each column of b the scaling itself, 128 products
 // and 128 sums of a thread for each block, is the longer:
-// 14336x4096x8192 added in fp32, 563 us, 1.71 PFLOP/s.
-//   1021x50257x769 into bf16, rows not on 16 bytes: 99 us (7 blocks of k to a
-//   tile: the output's way out is more than half of it)
+// 14336x4096x8192 added in fp32, 555 us, 1.73 PFLOP/s.
+// 1021x50257x769 into bf16, rows not on 16 bytes: 85 us; a tile has 7 blocks of
+// k, and its output's way out, which nothing hides, is half of its time.
 #include <cuda.h>
 
 #include <atomic>
@@ -214,7 +214,9 @@ __device__ __forceinline__ void write_tma(const MatmulParams &p, const void *map
 // distance from a boundary, so that the destination's 16-byte pieces lie whole
 // in the staged words; the rows' ends leave element by element.  (Gathering
 // the pieces from rows staged as they are took 8 two-byte reads for each:
-// 1021x50257x769 109 us, 99 here; 50256 columns, by TMA, 58.)
+// 1021x50257x769 109 us, 85 here, 82 without the ends; 50256 columns, by TMA,
+// 58.  Words in an order that conflicted in the banks, and each row's distance
+// formed anew: 100.)
 template <class T>
 __device__ __forceinline__ void write_turned(const MatmulParams &p, const float acc[128], uint8_t *stage, int id,
                                              int t, int m0, int n0)
@@ -222,48 +224,54 @@ __device__ __forceinline__ void write_turned(const MatmulParams &p, const float 
     constexpr int kPiece = 16 / (int)sizeof(T);
     constexpr int kCols = 16 * kPiece;  // columns at a time: 64 words of a row
     uint32_t *words = reinterpret_cast<uint32_t *>(stage);
-    // word w of a row lies where 32 rows' same words meet different banks
-    auto word = [&](int row, int w) -> uint32_t & { return words[row * 64 + (w ^ (row & 31))]; };
+    // A row's 16 pieces change places by its number, so that 32 rows' same words
+    // meet different banks: the turns of 8 (4) rows in a row are all different
+    // where rows have an odd length, and these rows' order is what is left.
+    auto shuffle = [](int row) { return sizeof(T) == 4 ? row >> 2 & 7 : (row >> 3 & 3) | (row & 1) << 2; };
     auto off_boundary = [&](const T *o) { return (int)(reinterpret_cast<uintptr_t>(o) / sizeof(T) % kPiece); };
     T *first = static_cast<T *>(p.out) + (int64_t)m0 * p.ldo + n0;
 #pragma unroll
     for (int c = 0; c < 128; c += kCols, first += kCols) {
         if (c > 0)
             barrier_of(id, 128);  // the last readers are done
-        const int turn = off_boundary(first + (int64_t)t * p.ldo);
-        if constexpr (sizeof(T) == 4) {
+        uint32_t *mine = words + t * 64;
+        const int mix = shuffle(t), turn = off_boundary(first + (int64_t)t * p.ldo);
+        const int shift = sizeof(T) == 4 ? turn : turn >> 1;
+        const bool odd = sizeof(T) == 2 && (turn & 1);
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-                word(t, (i + turn) & 63) = __float_as_uint(acc[c + i]);
-        } else {
-            const bool odd = turn & 1;
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-                word(t, (i + (turn >> 1)) & 63) = word_of<T>(odd ? acc[(2 * i + 127) & 127] : acc[2 * i],
-                                                             odd ? acc[2 * i] : acc[2 * i + 1]);
+        for (int i = 0; i < 64; ++i) {
+            const int w = (i + shift) & 63;
+            uint32_t x;
+            if constexpr (sizeof(T) == 4)
+                x = __float_as_uint(acc[c + i]);
+            else
+                x = word_of<T>(odd ? acc[(2 * i + 127) & 127] : acc[2 * i], odd ? acc[2 * i] : acc[2 * i + 1]);
+            mine[(((w >> 2) ^ mix) << 2) + (w & 3)] = x;
         }
         barrier_of(id, 128);
-        const int n = min(kCols, p.n - n0 - c);
-        T *o = first + (int64_t)(t >> 4) * p.ldo;
-        const int lane = t & 15;
-#pragma unroll 4
-        for (int row = t >> 4; row < 128; row += 8, o += 8 * p.ldo) {
-            if (m0 + row >= p.m || n <= 0)
-                continue;
-            const int at = off_boundary(o), begin = lane * kPiece - at;  // this thread's piece
-            if (begin >= 0 && begin + kPiece <= n)
-                *reinterpret_cast<uint4 *>(o + begin) =
-                    make_uint4(word(row, lane * 4), word(row, lane * 4 + 1), word(row, lane * 4 + 2),
-                               word(row, lane * 4 + 3));
-            // one of the at most 2 (kPiece - 1) elements outside whole pieces
-            const int head = min((kPiece - at) % kPiece, n), tail = head + (n - head) / kPiece * kPiece;
-            const int k = lane < 8 ? lane : tail + lane - 8;
-            if (lane < 8 ? lane < head : k < n) {
-                const int place = (k + at) & (kCols - 1);
+        // a thread reads every eighth row, whose turns are all the same
+        const int lane = t & 15, row0 = t >> 4;
+        T *to = first + (int64_t)row0 * p.ldo;
+        const int at = off_boundary(to), begin = lane * kPiece - at;  // this thread's piece
+        const int n = min(kCols, p.n - n0 - c), rows = n > 0 ? min(128, p.m - m0) : 0;
+        const bool whole = begin >= 0 && begin + kPiece <= n;
+        // one of the at most 2 (kPiece - 1) elements outside whole pieces
+        const int head = min((kPiece - at) % kPiece, n), tail = head + (n - head) / kPiece * kPiece;
+        const int k = lane < 8 ? lane : tail + lane - 8, place = (k + at) & (kCols - 1);
+        const int word = place * (int)sizeof(T) >> 2;
+        const bool edge = lane < 8 ? lane < head : k < n;
+#pragma unroll 16
+        for (int row = row0; row < rows; row += 8, to += 8 * p.ldo) {
+            const uint32_t *from = words + row * 64;
+            const int mixed = shuffle(row);
+            if (whole)
+                *reinterpret_cast<uint4 *>(to + begin) = *reinterpret_cast<const uint4 *>(from + ((lane ^ mixed) << 2));
+            if (edge) {
+                const uint32_t x = from[(((word >> 2) ^ mixed) << 2) + (word & 3)];
                 if constexpr (sizeof(T) == 4)
-                    o[k] = __uint_as_float(word(row, place));
+                    to[k] = __uint_as_float(x);
                 else
-                    reinterpret_cast<uint16_t *>(o)[k] = (uint16_t)(word(row, place >> 1) >> (16 * (place & 1)));
+                    reinterpret_cast<uint16_t *>(to)[k] = (uint16_t)(x >> (16 * (place & 1)));
             }
         }
     }
