@@ -112,6 +112,22 @@ def test_norm_finds_what_is_not_finite(bad, dtype):
     assert zs.read_tensors_stat(ok).found_inf == 0
 
 
+@pytest.mark.parametrize("sizes", [[9000] * 1100, [3_000_001] * 5, [7] * 600, [50_000, 40_000]])
+def test_norm_and_clip_in_a_row(sizes):
+    """In place, each norm's reader and the next norm's writer back to back, short lists and long ones."""
+    xs = zs.tensor_list([normal(i, (n,), F32) for i, n in enumerate(sizes)])
+    ws = torch.zeros(zs.zero_tensors_workspace_bytes(xs), dtype=torch.uint8, device="cuda")
+    limits = [16.0, 8.0, 2.0, 0.5, 0.25]
+    stats = [zs.new_tensors_stat() for _ in limits + [0]]
+    for stat, limit in zip(stats, limits):
+        zs.zero_tensors_norm(xs, 1.0, stat, ws)
+        zs.zero_tensors_clip(xs, None, 1.0, limit, stat)
+    zs.zero_tensors_norm(xs, 1.0, stats[-1], ws)
+    for stat, limit in zip(stats[1:], limits):
+        # the 1e-6 beside a norm of 0.5 or more, the factor's and the elements' roundings, the norm's own
+        assert abs(zs.read_tensors_stat(stat).norm - limit) <= limit * (2e-6 + 24 * U)
+
+
 @pytest.mark.parametrize("max_norm", [0.0, 0.25, 1e9])
 @pytest.mark.parametrize("out_dtype", [F16, BF16, F32, None])
 def test_clip(max_norm, out_dtype):
