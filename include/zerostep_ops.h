@@ -34,7 +34,9 @@
  * with X[r, c] ~ q[r, c] * s.  The last block of a row and the last tile may
  * be short.  s = max(amax / qmax, 2^-126), amax the largest magnitude of the
  * block and qmax the type's largest value (448 and 57344); q is X / s rounded
- * to nearest even (formed as X * (1 / s) in fp32).  A block of zeros has q = 0.
+ * to fp32 and then to the type, to nearest even (of fp32 elements, and where amax
+ * is 2^117 or more, a few in 1e8 meet the fp32 quotient's neighbour).  A block of
+ * zeros has q = 0.
  * A block that holds a NaN or an infinity has s = NaN or infinity, and q * s is
  * NaN throughout it, so that what is computed from it is not finite and the
  * step skips.

@@ -1,0 +1,98 @@
+"""The operators around the step where rounding, range, lengths and sharing of
+buffers are at their edges."""
+import pytest
+import torch
+
+import zero_partitioned_mixed_step_gb300 as zs
+from ops_reference import QMAX, TINY, blocks
+from test_gpu_ops import BF16, E4M3, E5M2, F16, F32, gen, normal
+
+pytestmark = pytest.mark.gpu
+
+
+# ----------------------------------------------------------------- 8-bit blocks
+
+def divided(x, f8, tile):
+    """x's 8-bit form by fp32 divisions: every bit is determined."""
+    r, k = x.shape
+    a = torch.zeros(blocks(r) * 128, blocks(k) * 128, device="cuda")
+    a[:r, :k] = x.float().abs()
+    a = a.view(-1, blocks(k), 128).amax(2)[:r]
+    if tile:
+        a = torch.nn.functional.pad(a, (0, 0, 0, -r % 128)).view(-1, 128, blocks(k)).amax(1)
+    s = (a / torch.full_like(a, QMAX[f8])).clamp_min(TINY)  # (by a number, torch multiplies by its reciprocal)
+    at = s.repeat_interleave(128, 1)[:, :k]
+    at = at.repeat_interleave(128, 0)[:r] if tile else at
+    return (x.float() / at).to(f8), s.t().contiguous()
+
+
+def same_bits(a, b):
+    """Equal as numbers, zeros with their signs, NaNs in the same places."""
+    nan = a.float().isnan()
+    assert torch.equal(nan, b.float().isnan())
+    ba, bb = (t.contiguous().view(torch.uint8) for t in (a, b))
+    if a.element_size() == 1:
+        assert torch.equal(ba[~nan], bb[~nan])
+    else:
+        assert torch.equal(a[~nan], b[~nan])
+
+
+KINDS = {
+    "normal": lambda g, n: torch.randn(n, device="cuda", generator=g),
+    # few bits: quotients that are the middle between two 8-bit values are common
+    "few bits": lambda g, n: torch.randint(-16, 17, n, device="cuda", generator=g) * 0.125,
+    "tiny": lambda g, n: torch.randn(n, device="cuda", generator=g) * 2.0 ** -100,
+    "subnormal": lambda g, n: torch.randn(n, device="cuda", generator=g) * 2.0 ** -124,
+    "huge": lambda g, n: torch.randn(n, device="cuda", generator=g).clamp(-3, 3) * 2.0 ** 126,
+    "spread": lambda g, n: torch.exp2(torch.rand(n, device="cuda", generator=g) * 60 - 40),
+}
+
+
+@pytest.mark.parametrize("tile", [False, True])
+@pytest.mark.parametrize("dtype,f8", [(BF16, E4M3), (F16, E4M3), (F32, E4M3), (BF16, E5M2), (F16, E5M2), (F32, E5M2)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_quantize_rounds_the_quotient(kind, dtype, f8, tile):
+    x = KINDS[kind](gen(7), (300, 1000))
+    x[17, 200:240] = -0.0
+    x = x.to(dtype)
+    if dtype == F16:
+        x[x.isinf()] = 1.0
+    q, s = zs.fp8_empty(300, 1000, f8, tile)
+    qt, st = zs.fp8_empty(1000, 300, f8, tile)
+    zs.zero_fp8_quantize(x, q, s, qt, st, tile=tile)
+    for got, got_s, want in ((q, s, divided(x, f8, tile)), (qt, st, divided(x.t(), f8, tile))):
+        assert torch.equal(got_s, want[1])
+        same_bits(got, want[0])
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("tile", [False, True])
+def test_quantize_divides_what_is_not_finite(bad, tile):
+    x = normal(1, (130, 300), BF16)
+    x[3, 140] = bad
+    x[3, 141] = -0.0
+    q, s = zs.fp8_empty(130, 300, E4M3, tile)
+    qt, st = zs.fp8_empty(300, 130, E4M3, tile)
+    zs.zero_fp8_quantize(x, q, s, qt, st, tile=tile)
+    for got, got_s, want in ((q, s, divided(x, E4M3, tile)), (qt, st, divided(x.t(), E4M3, tile))):
+        same_bits(got_s, want[1])
+        same_bits(got, want[0])
+
+
+@pytest.mark.parametrize("wdtype,f8", [(BF16, E4M3), (F16, E5M2), (F32, E4M3)])
+@pytest.mark.parametrize("cols", [256, 1024, 2048, 4096, 8192, 16384, 32768])
+def test_rmsnorm_rounds_the_quotient(cols, wdtype, f8):
+    """Rows whose squares have the mean 4 exactly: rstd is 1/2 and y one product."""
+    eight = torch.tensor([[5, 2, 1, 1, 1, 0, 0, 0], [4, 3, 2, 1, 1, 1, 0, 0], [3, 3, 3, 2, 1, 0, 0, 0.]], device="cuda")
+    g, rows = gen(3), 6
+    pick = torch.randint(0, 3, (rows, cols // 8), device="cuda", generator=g)
+    sign = torch.randint(0, 2, (rows, cols), device="cuda", generator=g) * 2.0 - 1.0
+    x = (eight[pick].view(rows, cols) * sign).to(BF16)
+    w = (1 + normal(2, (cols,), F32, 0.2)).to(wdtype)
+    q, s = zs.fp8_empty(rows, cols, f8)
+    rstd = torch.empty(rows, device="cuda")
+    zs.zero_rmsnorm_fp8(x, w, 0.0, rstd, q=q, s=s)
+    assert (rstd == 0.5).all()
+    want, want_s = divided(x.float() * 0.5 * w.float(), f8, False)
+    assert torch.equal(s, want_s)
+    same_bits(q, want)

@@ -280,6 +280,54 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d)
     return lo | hi << 16;
 }
 
+// 1 / s of a block's scale s in two parts, hi rounded down and so lo >= 0.
+struct Inverse {
+    float hi, lo;
+};
+__device__ __forceinline__ Inverse inverse(float s)
+{
+    Inverse r;
+    r.hi = __frcp_rd(s);
+    r.lo = s == __int_as_float(0x7F800000) ? 0.0f : __fmul_rn(__fmaf_rn(-s, r.hi, 1.0f), r.hi);
+    return r;
+}
+
+// Two fp32 values at a time.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 r;
+    asm("{ .reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};"
+        " fma.rn.f32x2 w, x, y, z; mov.b64 {%0, %1}, w; }"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+// Eight quotients x / s, rounded to fp32 and then to 8 bits.  The fp32 quotient
+// is x * hi + round(x * lo), rounded: the correctly rounded one for every pair
+// of an fp16 or bf16 x below 2^117 and its block's s, above it and for fp32
+// in all but a few of 1e8 pairs (x * round(1 / s) is off by an ulp for a quarter
+// of all).  So an element whose quotient is the middle between two 8-bit values,
+// which is common where x and the block's largest element have few bits, goes to
+// the even one.  As lo is not negative, -0 stays.
+template <int F8>
+__device__ __forceinline__ uint2 quotients8(const float x[8], Inverse d)
+{
+    float2 q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 y = make_float2(x[2 * i], x[2 * i + 1]);
+        q[i] = fma2(y, make_float2(d.hi, d.hi), mul2(y, make_float2(d.lo, d.lo)));
+    }
+    return make_uint2(pack4<F8>(q[0].x, q[0].y, q[1].x, q[1].y), pack4<F8>(q[2].x, q[2].y, q[3].x, q[3].y));
+}
+
 // ------------------------------------------------------------------ reductions
 
 template <int N>

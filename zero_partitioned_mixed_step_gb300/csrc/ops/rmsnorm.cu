@@ -79,13 +79,10 @@ __device__ __forceinline__ void put_y(const NormParams &p, int64_t row, int64_t 
         a = max(a, magnitude(y[i]));
     a = max_over<16>(a);
     const float s = block_scale<F8>(a);
-    const float inv = __fdiv_rn(1.0f, s);
     if (n > 0) {
         if ((threadIdx.x & 15) == 0)
             p.s[(c / kBlock) * p.lds + row] = s;
-        const uint2 o = make_uint2(pack4<F8>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                                   pack4<F8>(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
-        store8b(p.q + row * p.ldq + c, n, p.wide_q, o);
+        store8b(p.q + row * p.ldq + c, n, p.wide_q, quotients8<F8>(y, inverse(s)));
     }
 }
 
