@@ -1008,8 +1008,10 @@ struct Plan {
 static Plan plan_of(int64_t m, int64_t n, int64_t k)
 {
     Plan r{};
-    const int64_t kb = ceil_div(k, kBlock);
     r.splits = 1;
+    if (m == 0 || n == 0)  // nothing to cut
+        return r;
+    const int64_t kb = ceil_div(k, kBlock);
     const int64_t pair_waves = ceil_div(ceil_div(m, 256) * ceil_div(n, 256), kPlanSms / 2);
     const int64_t single_waves = ceil_div(ceil_div(m, 128) * ceil_div(n, 128), kPlanSms);
     if (m > 64 && 3 * pair_waves < 2 * single_waves) {
