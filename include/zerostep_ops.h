@@ -64,7 +64,7 @@ typedef enum {
  * tensors add their sumsq and OR their found_inf before the clip. */
 typedef struct {
     double sumsq;      /* sum of the squares of all elements, times inv_scale^2 */
-    float norm;        /* its square root */
+    float norm;        /* its square root (infinite from 2^128 on; the clip goes by sumsq) */
     int32_t found_inf; /* 1 if an element times inv_scale is NaN or infinite */
 } zero_tensors_stat;
 
@@ -96,7 +96,8 @@ ZERO_API int zero_tensors_norm(int n, const void *const *x, const int64_t *numel
  * out = x * (inv_scale * c), rounded once to out's type, with
  * c = min(1, max_norm / (sqrt(stat->sumsq) + 1e-6)) as the step's own clip;
  * c = 1 when stat->found_inf, so that what is not finite stays so and reaches
- * the step, which skips, and c = 1 when max_norm is 0 (no clipping).
+ * the step, which skips, and c = 1 when max_norm is 0 (no clipping) or sumsq is not
+ * finite.
  *  out: NULL = in place (out_type is not read), or n pointers with the types
  *    out_type[n]; out[t] may equal x[t] when the types are the same.
  *    Pointers into the flat half buffer at the layout's tensor offsets make it

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import zero_partitioned_mixed_step_gb300 as zs
-from ops_reference import QMAX, TINY, blocks
+from ops_reference import QMAX, TINY, U, blocks, clip_factor, half_ulp
 from test_gpu_ops import BF16, E4M3, E5M2, F16, F32, gen, normal
 
 pytestmark = pytest.mark.gpu
@@ -96,3 +96,62 @@ def test_rmsnorm_rounds_the_quotient(cols, wdtype, f8):
     want, want_s = divided(x.float() * 0.5 * w.float(), f8, False)
     assert torch.equal(s, want_s)
     same_bits(q, want)
+
+
+# ----------------------------------------------------------------- clip
+
+def clipped(xs, outs, inv, max_norm, stat):
+    """zero_tensors_clip against the formula in 64 bits: the factor's rounding, the product's, out's."""
+    sumsq = zs.read_tensors_stat(stat).sumsq
+    before = [x.double() for x in xs]
+    zs.zero_tensors_clip(xs, outs, inv, max_norm, stat)
+    for x, o in zip(before, xs if outs is None else outs):
+        want = x * clip_factor(sumsq, inv, max_norm)
+        assert ((o.double() - want).abs() <= want.abs() * 6 * U + half_ulp(want, o.dtype) * (1 + 1e-6)).all()
+
+
+def norm_of(xs, inv):
+    ws = torch.zeros(zs.zero_tensors_workspace_bytes(xs), dtype=torch.uint8, device="cuda")
+    stat = zs.new_tensors_stat()
+    zs.zero_tensors_norm(xs, inv, stat, ws)
+    return stat
+
+
+@pytest.mark.parametrize("out", [None, F32, BF16])
+@pytest.mark.parametrize("max_norm", [1.0, 1e-3, 1e30])
+@pytest.mark.parametrize("inv", [1.0, 2.0 ** -4])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_clip_where_the_norm_leaves_fp32(dtype, inv, max_norm, out):
+    """Finite gradients whose norm is 2^128 or more: clipped, not zeroed."""
+    xs = [normal(1, (20_011,), F32).clamp(-3, 3).mul_(1e38).to(dtype), normal(2, (333,), F32).mul_(1e37).to(dtype),
+          normal(3, (5,), BF16)]
+    stat = norm_of(xs, inv)
+    got = zs.read_tensors_stat(stat)
+    assert got.found_inf == 0 and got.sumsq > 2.0 ** 256
+    clipped(xs, None if out is None else [torch.empty(x.shape, dtype=out, device="cuda") for x in xs], inv, max_norm, stat)
+
+
+def test_clip_of_two_elements_near_the_largest():
+    x = torch.tensor([3e38, -3e38], device="cuda")
+    stat = norm_of([x], 1.0)
+    clipped([x], None, 1.0, 1.0, stat)
+    assert torch.allclose(x, torch.tensor([0.5 ** 0.5, -0.5 ** 0.5], device="cuda"), rtol=1e-6)
+
+
+@pytest.mark.parametrize("inv", [2.0 ** -110, 2.0 ** -30, 1.0])
+@pytest.mark.parametrize("sumsq", [1e-60, 1e-30, 1e60, 1e90])
+def test_clip_with_a_sum_from_elsewhere(sumsq, inv):
+    """The sum over ranks is the caller's, anywhere in binary64's range."""
+    x = normal(4, (5000,), F32, 1e35 if inv < 1e-30 or sumsq > 1e59 else 1.0)
+    stat = zs.new_tensors_stat()
+    stat[:8].view(torch.float64).fill_(sumsq)
+    clipped([x], [torch.empty_like(x)], inv, 1.0, stat)
+
+
+@pytest.mark.parametrize("sumsq", [float("inf"), float("nan")])
+def test_clip_leaves_what_has_no_finite_sum(sumsq):
+    x = normal(4, (5000,), F32)
+    before, stat = x.clone(), zs.new_tensors_stat()
+    stat[:8].view(torch.float64).fill_(sumsq)
+    zs.zero_tensors_clip([x], None, 1.0, 1.0, stat)
+    assert torch.equal(x, before)

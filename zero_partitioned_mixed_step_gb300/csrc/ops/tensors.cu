@@ -333,26 +333,55 @@ __global__ void __launch_bounds__(kEndThreads)
 
 // ------------------------------------------------------------------ clip
 
+// What an element is multiplied by: f, then twice g, a power of two that is 1
+// wherever f alone has fp32's full precision.
+struct Factor {
+    float f, g;
+    __device__ __forceinline__ float of(float x) const { return __fmul_rn(__fmul_rn(__fmul_rn(x, f), g), g); }
+};
+
+// inv * c, c = min(1, max_norm / (sqrt(sumsq) + 1e-6)).  In fp32 where everything
+// is well inside its range: GB300's binary64 is slow.  Outside (a norm from
+// 2^128 on, say) in binary64, rounded once; of a factor that fp32 would hold with
+// few bits or none f keeps the bits and g half the exponent.  (Where x * f * g
+// is below fp32's normal numbers, with g <= 2^-49, the end is 0.)
+__device__ __forceinline__ Factor clip_factor(double sumsq, float inv, float max_norm)
+{
+    if (sumsq >= 0x1p-120 && sumsq <= 0x1p120) {
+        const float f = __fmul_rn(inv, fminf(1.0f, __fdiv_rn(max_norm, __fadd_rn(__fsqrt_rn((float)sumsq), 1e-6f))));
+        if (f >= 0x1p-100f)
+            return {f, 1.0f};
+    }
+    if (!(sumsq <= 1.7976931348623157e308))  // no finite sum: as with found_inf
+        return {inv, 1.0f};
+    const double f = inv * fmin(1.0, max_norm / (sqrt(sumsq) + 1e-6));
+    if (f >= 0x1p-100 || f == 0.0)
+        return {(float)f, 1.0f};
+    // f below 1/2, so that no product overflows; 2^-298 times the largest fp32 is 0
+    const int half = min((-ilogb(f) - 2) / 2, 149);
+    return {(float)scalbn(f, 2 * half), scalbnf(1.0f, -half)};
+}
+
 // Eight scaled elements to a 16-byte aligned p; nothing reads them here again.
 template <class U, class T>
-__device__ __forceinline__ void put(U *p, const Raw8<T> &x, float f)
+__device__ __forceinline__ void put(U *p, const Raw8<T> &x, Factor f)
 {
     uint32_t w[Raw8<U>::kWords];
     if constexpr (sizeof(U) == 4)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            w[i] = __float_as_uint(__fmul_rn(x.at(i), f));
+            w[i] = __float_as_uint(f.of(x.at(i)));
     else
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            w[i] = word_of<U>(__fmul_rn(x.at(2 * i), f), __fmul_rn(x.at(2 * i + 1), f));
+            w[i] = word_of<U>(f.of(x.at(2 * i)), f.of(x.at(2 * i + 1)));
 #pragma unroll
     for (int i = 0; i < Raw8<U>::kWords / 4; ++i)
         __stcs(reinterpret_cast<uint4 *>(p) + i, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
 }
 
 template <class T, class U>
-__device__ __forceinline__ void scale_chunk(const T *p, U *o, int64_t n, float f)
+__device__ __forceinline__ void scale_chunk(const T *p, U *o, int64_t n, Factor f)
 {
     const bool wide = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
     const bool wide_out = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
@@ -374,7 +403,7 @@ __device__ __forceinline__ void scale_chunk(const T *p, U *o, int64_t n, float f
         load8(p + u * kUnit, m, wide, x);
 #pragma unroll
         for (int i = 0; i < kUnit; ++i)
-            x[i] = __fmul_rn(x[i], f);
+            x[i] = f.of(x[i]);
         store8(o + u * kUnit, m, wide_out, x);
     }
 }
@@ -385,19 +414,13 @@ __global__ void __launch_bounds__(kThreads)
                 const zero_tensors_stat *stat)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the norm is there, the tensors are final
-    float c = 1.0f;
-    if (max_norm > 0.0f && stat->found_inf == 0) {
-        // the norm from sumsq (which the caller may have added over ranks),
-        // in fp32 where it is in range: GB300's binary64 is slow
-        const double s = stat->sumsq;
-        const float norm = s >= 0x1p-120 && s <= 0x1p120 ? __fsqrt_rn((float)s) : (float)sqrt(s);
-        c = fminf(1.0f, __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f)));
-    }
-    const float f = __fmul_rn(inv, c);
+    Factor f{inv, 1.0f};
+    if (max_norm > 0.0f && stat->found_inf == 0)
+        f = clip_factor(stat->sumsq, inv, max_norm);  // (the caller may have added sumsq over ranks)
     // from the list's end backwards: what the norm read last is still in L2
     const uint32_t chunk = gridDim.x - 1 - blockIdx.x;
     const int t = find_tensor(l, chunk);
-    if (f == 1.0f && l.out[t] == l.x[t])
+    if (f.f == 1.0f && f.g == 1.0f && l.out[t] == l.x[t])
         return;  // in place and unchanged
     const int64_t at = (int64_t)(chunk - l.first[t]) * l.chunk;
     const int64_t left = l.numel[t] - at;
