@@ -155,3 +155,13 @@ def test_clip_leaves_what_has_no_finite_sum(sumsq):
     stat[:8].view(torch.float64).fill_(sumsq)
     zs.zero_tensors_clip([x], None, 1.0, 1.0, stat)
     assert torch.equal(x, before)
+
+
+@pytest.mark.parametrize("max_norm", [1e-300, 1e-46, 1e-40, 1e-37, 1e37, 1e39, 1e300, float("inf")])
+@pytest.mark.parametrize("size", [1e-2, 1e30])
+def test_clip_to_limits_outside_fp32(size, max_norm):
+    """A positive limit clips, however small; no limit is too large."""
+    x = normal(4, (5000,), F32, size)
+    before, stat = x.clone(), norm_of([x], 1.0)
+    clipped([x], None, 1.0, max_norm, stat)
+    assert torch.equal(x, before) == (max_norm > 1e34)

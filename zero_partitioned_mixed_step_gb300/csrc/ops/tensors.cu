@@ -345,10 +345,10 @@ struct Factor {
 // 2^128 on, say) in binary64, rounded once; of a factor that fp32 would hold with
 // few bits or none f keeps the bits and g half the exponent.  (Where x * f * g
 // is below fp32's normal numbers, with g <= 2^-49, the end is 0.)
-__device__ __forceinline__ Factor clip_factor(double sumsq, float inv, float max_norm)
+__device__ __forceinline__ Factor clip_factor(double sumsq, float inv, double max_norm)
 {
     if (sumsq >= 0x1p-120 && sumsq <= 0x1p120) {
-        const float f = __fmul_rn(inv, fminf(1.0f, __fdiv_rn(max_norm, __fadd_rn(__fsqrt_rn((float)sumsq), 1e-6f))));
+        const float f = __fmul_rn(inv, fminf(1.0f, __fdiv_rn((float)max_norm, __fadd_rn(__fsqrt_rn((float)sumsq), 1e-6f))));
         if (f >= 0x1p-100f)
             return {f, 1.0f};
     }
@@ -410,12 +410,12 @@ __device__ __forceinline__ void scale_chunk(const T *p, U *o, int64_t n, Factor 
 
 template <int CAP>
 __global__ void __launch_bounds__(kThreads)
-    clip_kernel(const __grid_constant__ List<CAP, true> l, float inv, float max_norm,
+    clip_kernel(const __grid_constant__ List<CAP, true> l, float inv, double max_norm,
                 const zero_tensors_stat *stat)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the norm is there, the tensors are final
     Factor f{inv, 1.0f};
-    if (max_norm > 0.0f && stat->found_inf == 0)
+    if (max_norm > 0.0 && stat->found_inf == 0)
         f = clip_factor(stat->sumsq, inv, max_norm);  // (the caller may have added sumsq over ranks)
     // from the list's end backwards: what the norm read last is still in L2
     const uint32_t chunk = gridDim.x - 1 - blockIdx.x;
@@ -630,7 +630,7 @@ int zero_tensors_clip(int n, const void *const *x, const int64_t *numel, const i
     return for_each_list<true>(n, x, numel, type, out, out_type, total,
                                [&](auto &l, bool, bool) {
                                    return launch_after(clip_kernel<l.kCap>, l.first[l.n], kThreads, stream, l,
-                                                       inv_scale, (float)max_norm, stat);
+                                                       inv_scale, max_norm, stat);
                                });
 }
 
