@@ -10,8 +10,8 @@
  *                           128, and its transpose
  *   zero_fp8_matmul         the product of two such matrices
  *   zero_tensors_norm       the global L2 norm over many gradient tensors
- *   zero_tensors_clip       the unscaled, clipped gradients, in place or into
- *                           the flat half buffer that zero_step_fused reads
+ *   zero_tensors_clip       the clipped gradients, in place or into the flat
+ *                           half buffer that zero_step_fused reads
  *
  * Conventions: as zerostep.h (the caller owns every buffer, device work is
  * enqueued on `stream` and nothing synchronises the host, arguments are
@@ -102,6 +102,11 @@ ZERO_API int zero_tensors_norm(int n, const void *const *x, const int64_t *numel
  *    out_type[n]; out[t] may equal x[t] when the types are the same.
  *    Pointers into the flat half buffer at the layout's tensor offsets make it
  *    the gradient that the step reads.
+ *  inv_scale: under a loss scale S, 1 / S in zero_tensors_norm (max_norm is about
+ *    the unscaled gradients) and, into the step's buffer, 1 here: the step
+ *    divides what it reads by S itself, and the half type holds the small
+ *    gradients only while they are scaled.  1 / S here gives unscaled
+ *    gradients, for a reader that expects those.
  * In place with a factor of exactly 1 nothing is written.
  */
 ZERO_API int zero_tensors_clip(int n, const void *const *x, const int64_t *numel,

@@ -165,3 +165,34 @@ def test_clip_to_limits_outside_fp32(size, max_norm):
     before, stat = x.clone(), norm_of([x], 1.0)
     clipped([x], None, 1.0, max_norm, stat)
     assert torch.equal(x, before) == (max_norm > 1e34)
+
+
+@pytest.mark.parametrize("scale", [1.0, 1024.0, 2.0 ** 16])
+def test_norm_clip_and_step_under_a_loss_scale(scale):
+    """Gradients of a loss times `scale`: the norm's inv_scale is 1 / scale, the
+    clip's is 1, for the step divides what it reads by its state's own scale.
+    Elements that fp16 does not hold without the scale reach the moments."""
+    sizes, max_norm = [(300, F16), (4097, F16), (64, F32), (1001, F16)], 1e-6
+    z = zs.ZeroStep([n for n, _ in sizes], 1, zs.F16, zs.adam_cfg(), loss_scale=scale)
+    flat = torch.zeros(z.grad_numel(), dtype=F16, device="cuda")
+    outs = [flat[o:o + n] for o, (n, _) in zip(z.offsets, sizes)]
+    small = 1e-3 if scale == 1.0 else 1e-8
+    xs = [normal(i, (n,), F32, small * scale).to(t) for i, (n, t) in enumerate(sizes)]
+    stat = norm_of(xs, 1.0 / scale)
+    zs.zero_tensors_clip(xs, outs, 1.0, max_norm, stat)
+    z.step([flat])
+    st = z.read_state()
+    assert (st.t, st.skipped) == (1, 0)
+    # (1e-6 beside the norm is part of the factor)
+    c = clip_factor(sum(float((x.double() / scale).square().sum()) for x in xs), 1.0, max_norm)
+    assert c < 0.9
+    for x, o, n in zip(xs, z.offsets, (n for n, _ in sizes)):
+        m, kept = z.m[st.cur][o:o + n].double(), x.double() * c
+        want = kept / scale * 0.1
+        assert ((m - want).abs() <= want.abs() * 16 * U + half_ulp(kept, F16) * (1 + 1e-6) * 0.1 / scale).all()
+        assert scale == 1.0 or (m != 0).double().mean() > 0.95
+    xs[1][5] = float("inf")
+    stat = norm_of(xs, 1.0 / scale)
+    zs.zero_tensors_clip(xs, outs, 1.0, max_norm, stat)
+    z.step([flat])
+    assert (z.read_state().t, z.read_state().skipped) == (1, 1)

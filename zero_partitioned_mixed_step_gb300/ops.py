@@ -168,7 +168,9 @@ def zero_tensors_norm(tensors: Tensors, inv_scale: float, stat: torch.Tensor, ws
 def zero_tensors_clip(tensors: Tensors, out: Optional[Tensors], inv_scale: float, max_norm: float,
                       stat: torch.Tensor, stream=None) -> None:
     """out = tensors * inv_scale * min(1, max_norm / (norm + 1e-6)), in place
-    with ``out`` None; max_norm 0 does not clip."""
+    with ``out`` None; max_norm 0 does not clip.  Under a loss scale S the norm's
+    inv_scale is 1 / S; into the step's flat buffer it is 1 here, for the step
+    divides by S itself."""
     l, dev = tensor_list(tensors), _current()
     o = tensor_list(out) if out is not None else None
     if l.device != dev or o is not None and o.device != dev:
