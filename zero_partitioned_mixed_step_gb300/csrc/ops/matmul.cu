@@ -937,6 +937,7 @@ __global__ void __launch_bounds__(Few<TN>::kThreads, 2)
                     sum += x[s];
                 put_one(p, (int64_t)i * p.ldo + row, sum);
             }
+        __syncwarp();    // the lanes without a column come together with the others
         cluster_sync();  // nobody ends while its sums are being read
     }
     __syncwarp();
