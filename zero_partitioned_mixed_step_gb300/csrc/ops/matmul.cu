@@ -400,7 +400,15 @@ __global__ void __launch_bounds__(Shape<CG, NH, TILE_B>::kThreads, 1)
                     }
                 }
             }
-            if (!ok && rank == 0)  // copies in flight land before the CTA ends
+            // Copies in flight land before the CTA ends.  Those of a pair's second
+            // CTA are counted in the first, which may not have asked for them all,
+            // so it polls a barrier that nothing arrives at, a millisecond or more
+            // where a copy takes microseconds.
+            if (!ok && rank != 0)
+                for (int k = 0; k < kWaitLimit >> 6; ++k)
+                    if (bar_try(smem_u32(&full_bar[0]), 0))
+                        break;
+            if (!ok && rank == 0)
                 for (int i = 0; i < issued; ++i) {
                     if (--st < 0) {
                         st = kStages - 1;
