@@ -402,10 +402,9 @@ __global__ void __launch_bounds__(Shape<CG, NH, TILE_B>::kThreads, 1)
             }
             // Copies in flight land before the CTA ends.  Those of a pair's second
             // CTA are counted in the first, which may not have asked for them all,
-            // so it polls a barrier that nothing arrives at, a millisecond or more
-            // where a copy takes microseconds.
+            // so it polls a barrier that nothing arrives at.
             if (!ok && rank != 0)
-                for (int k = 0; k < kWaitLimit >> 6; ++k)
+                for (int k = 0; k < kDrainLimit; ++k)
                     if (bar_try(smem_u32(&full_bar[0]), 0))
                         break;
             if (!ok && rank == 0)
@@ -414,7 +413,7 @@ __global__ void __launch_bounds__(Shape<CG, NH, TILE_B>::kThreads, 1)
                         st = kStages - 1;
                         phase ^= 1;
                     }
-                    for (int k = 0; k < kWaitLimit; ++k)
+                    for (int k = 0; k < kDrainLimit; ++k)
                         if (bar_try(smem_u32(&full_bar[st]), phase ^ 1))
                             break;
                 }
@@ -458,7 +457,7 @@ __global__ void __launch_bounds__(Shape<CG, NH, TILE_B>::kThreads, 1)
             }
             if (!ok) {  // products in flight end before tensor memory is freed
                 mma_commit<CG>(smem_u32(&drain_bar[h]));
-                for (int k = 0; k < kWaitLimit; ++k)
+                for (int k = 0; k < kDrainLimit; ++k)
                     if (bar_try(smem_u32(&drain_bar[h]), 0))
                         break;
             }
@@ -774,7 +773,7 @@ __global__ void __launch_bounds__(Few<TN>::kThreads, 2)
                         st = kStages - 1;
                         phase ^= 1;
                     }
-                    for (int q = 0; q < kWaitLimit; ++q)
+                    for (int q = 0; q < kDrainLimit; ++q)
                         if (bar_try(smem_u32(&full_bar[st]), phase ^ 1))
                             break;
                 }
@@ -811,7 +810,7 @@ __global__ void __launch_bounds__(Few<TN>::kThreads, 2)
             }
             if (!ok) {  // products in flight end before tensor memory is freed
                 mma_commit<1>(smem_u32(&drain_bar));
-                for (int q = 0; q < kWaitLimit; ++q)
+                for (int q = 0; q < kDrainLimit; ++q)
                     if (bar_try(smem_u32(&drain_bar), 0))
                         break;
             }
