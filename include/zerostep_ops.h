@@ -131,7 +131,8 @@ ZERO_API int zero_fp8_quantize(const void *x, int type, int64_t rows, int64_t co
  * ones).  ZERO-FILL IT ONCE before its first use; a call leaves it ready for
  * the next one of any sizes that it is large enough for.  Its first 4 bytes
  * are an error word: nonzero if a kernel gave up waiting for its own copies
- * or products (never expected; the output is then undefined). */
+ * or products (never expected; that call's output is then undefined, and the
+ * word stays until the caller clears it). */
 ZERO_API size_t zero_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
 
 /*

@@ -1,5 +1,10 @@
 """The operators around the step where rounding, range, lengths and sharing of
 buffers are at their edges."""
+import json
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -196,3 +201,17 @@ def test_norm_clip_and_step_under_a_loss_scale(scale):
     zs.zero_tensors_clip(xs, outs, 1.0, max_norm, stat)
     z.step([flat])
     assert (z.read_state().t, z.read_state().skipped) == (1, 1)
+
+
+# ----------------------------------------------------------------- product
+
+def test_matmul_whose_waits_run_out_reports_and_leaves_the_workspace_ready():
+    """With ZERO_TEST_MATMUL_GIVE_UP=1 (read once per process: a child) every
+    second CTA takes a wait that its first poll does not end as run out: the
+    error word is set and every tile's counter is back at zero."""
+    env = dict(os.environ, ZERO_TEST_MATMUL_GIVE_UP="1")
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, os.path.join(here, "gpu_ops_children.py"), "give_up"], capture_output=True,
+                       text=True, env=env, timeout=600)
+    assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-4000:]
+    assert json.loads(r.stdout.strip().splitlines()[-1]) == {"ok": True}

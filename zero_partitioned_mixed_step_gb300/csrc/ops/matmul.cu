@@ -17,8 +17,9 @@
 //   a warp that brings the scales.
 // The CTAs are persistent and walk the tiles.  All waits are bounded: the
 // role that gives up marks the workspace's error word, the others follow, the
-// copies and products in flight are waited for (again bounded) and tensor
-// memory is freed.
+// copies and products in flight are waited for (again bounded), tensor memory is
+// freed and the parts of k that were left out are counted, so that the
+// workspace's counters are zero again.
 //
 // What bounds it: a block of 256x256x128 is 512 cycles of products, and takes
 // about 930, since tensor memory has no room for a third block: the product
@@ -32,6 +33,7 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <cstdlib>
 #include <type_traits>
 
 #include "ops.cuh"
@@ -58,6 +60,7 @@ struct MatmulParams {
     int32_t m, n, kb;           // rows, columns, blocks of k
     int32_t tiles_m, tiles_n, splits, units;
     int32_t out_type, add, tma_out;
+    int32_t give_up;            // test setting: every second CTA starts as if a wait of its had run out
     uint32_t instr;
 };
 
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(Shape<CG, NH, TILE_B>::kThreads, 1)
     const uint32_t rank = CG == 1 ? 0 : cluster_rank();
 
     if (threadIdx.x == 0) {
-        gave_up_sh = 0;
+        gave_up_sh = p.give_up & (int)blockIdx.x & 1;
         for (int i = 0; i < kStages; ++i) {
             bar_init(smem_u32(&full_bar[i]), 1);
             bar_init(smem_u32(&empty_bar[i]), P);
@@ -516,7 +519,8 @@ __global__ void __launch_bounds__(Shape<CG, NH, TILE_B>::kThreads, 1)
         int buf = 0, slot = 0, in_group = 0;
         uint32_t phase = 0, scale_phase = 0;
         bool ok = true;
-        for (int u = first; u < units; u += step) {
+        int u = first;
+        for (; u < units; u += step) {
             const Unit w = unit_of(p, u);
             const int m0 = w.m * S::kTileM + (int)rank * 128, n0 = w.n * S::kTileN + h * 128;
             const bool has_row = m0 + t < p.m;
@@ -650,8 +654,16 @@ __global__ void __launch_bounds__(Shape<CG, NH, TILE_B>::kThreads, 1)
             else
                 write_tile<float>(p, &map_out, acc, stage, id, t, m0, n0);
         }
-        if (t == 0)
+        if (t == 0) {
             bulk_wait_all();
+            // parts left out count all the same: the tiles' counters come back to zero
+            if (NH == 1 && !ok && p.splits > 1)  // (pairs do not split k)
+                for (; u < units; u += step) {
+                    uint32_t *count = p.counters + u / p.splits;
+                    if (atomicAdd(count, 1u) == (uint32_t)p.splits - 1)
+                        *count = 0;
+                }
+        }
     }
     __syncwarp();
     fence_before();
@@ -724,7 +736,7 @@ __global__ void __launch_bounds__(Few<TN>::kThreads, 2)
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        gave_up_sh = 0;
+        gave_up_sh = p.give_up & (int)blockIdx.x & 1;
         for (int i = 0; i < kStages; ++i) {
             bar_init(smem_u32(&full_bar[i]), 1);
             bar_init(smem_u32(&empty_bar[i]), 1);
@@ -1050,6 +1062,18 @@ struct Operands {
     int a_type, b_type;
 };
 
+// ZERO_TEST_MATMUL_GIVE_UP=1 in the environment (read once per process): in every
+// second CTA a wait that is not over at its first poll ends as if its polls had
+// run out.
+static int test_give_up()
+{
+    static const int on = [] {
+        const char *t = std::getenv("ZERO_TEST_MATMUL_GIVE_UP");
+        return t && std::atoi(t) > 0 ? 1 : 0;
+    }();
+    return on;
+}
+
 // Lets a kernel use that much shared memory, once for each device (bits of `ready`).
 static cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &ready)
 {
@@ -1215,6 +1239,7 @@ int zero_fp8_matmul(const void *a, int a_type, int64_t lda, const float *sa, int
     p.units = (int32_t)units;
     p.out_type = out_type;
     p.add = add ? 1 : 0;
+    p.give_up = test_give_up();
     // a TMA store (or reduction) of whole boxes; half types are added in fp32 and rounded once
     p.tma_out = rows_aligned(out, ldo, ob, 16) && (!add || out_type == ZERO_T_F32);
     const Operands o{a, b, lda, ldb, k, a_type, b_type};
