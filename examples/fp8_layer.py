@@ -112,6 +112,8 @@ def train(layer: Layer, x, residual, target, steps: int):
         loss = err.square().mean()
         layer.backward((err * (2.0 / err.numel())).to(torch.bfloat16), slot)
         layer.update()
+        if zs.read_matmul_error(layer.mm_ws):
+            raise RuntimeError("a product gave up waiting: its output is undefined")
         seen.append((float(loss), zs.read_tensors_stat(layer.stat).norm))
     return seen
 

@@ -30,7 +30,7 @@ def give_up():
             ws = torch.zeros(zs.zero_fp8_matmul_workspace_bytes(m, n, k) + 64, dtype=torch.uint8, device="cuda")
             zs.zero_fp8_matmul(a, sa, b, sb, out[:, :n], ws[:-64])
             torch.cuda.synchronize()
-            assert int(ws[:4].view(torch.int32)) == 1, (m, n, k)
+            assert zs.read_matmul_error(ws) and int(ws[:4].view(torch.int32)) == 1, (m, n, k)
             assert int(ws[4:4096].sum()) == 0, (m, n, k, "counters")
             assert int(ws[-64:].sum()) == 0 and bool((out[:, n:] == 5).all()), (m, n, k)
     x = torch.arange(1 << 20, device="cuda", dtype=torch.int64)

@@ -215,3 +215,14 @@ def test_matmul_whose_waits_run_out_reports_and_leaves_the_workspace_ready():
                        text=True, env=env, timeout=600)
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-4000:]
     assert json.loads(r.stdout.strip().splitlines()[-1]) == {"ok": True}
+
+
+def test_example_stops_on_a_product_that_gave_up():
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    from fp8_layer import Layer, train
+    layer = Layer(128, 128, 256)
+    x, residual, target = (normal(i, (128, 128), BF16) for i in range(3))
+    train(layer, x, residual, target, 1)
+    layer.mm_ws[0] = 1
+    with pytest.raises(RuntimeError):
+        train(layer, x, residual, target, 1)

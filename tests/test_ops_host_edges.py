@@ -24,3 +24,20 @@ def test_matmul_workspace_of_empty_sizes(lib):
             assert need == 4096
             assert lib.zero_fp8_matmul(P, E4M3, 784, P, max(m, 1), P, E4M3, 784, P, max(n, 1), 0, P, F32, max(n, 1),
                                        m, n, k, 0, P, need, None) == 0
+
+
+def test_matmul_error_is_read():
+    import torch
+    import zero_partitioned_mixed_step_gb300 as zs
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    ws[256:] = 1  # what follows the word is not read
+    assert zs.read_matmul_error(ws) is False
+    ws[:4].view(torch.int32).fill_(1)
+    assert zs.read_matmul_error(ws) is True
+    assert zs.read_matmul_error(ws.view(torch.float32)) is True
+    ws[:4].zero_()
+    assert zs.read_matmul_error(ws) is False
+    with pytest.raises(ValueError):
+        zs.read_matmul_error(ws[:2])
+    with pytest.raises(ValueError):
+        zs.read_matmul_error(ws[::2])

@@ -23,7 +23,7 @@ from ._ops_abi import (BLOCK, T_BF16, T_E4M3, T_E5M2, T_F16, T_F32, TensorsStat,
 __all__ = [
     "BLOCK", "TensorList", "TensorsStat", "tensor_list", "new_tensors_stat", "read_tensors_stat",
     "zero_tensors_workspace_bytes", "zero_tensors_norm", "zero_tensors_clip", "fp8_empty",
-    "zero_fp8_quantize", "zero_fp8_matmul_workspace_bytes", "zero_fp8_matmul",
+    "zero_fp8_quantize", "zero_fp8_matmul_workspace_bytes", "zero_fp8_matmul", "read_matmul_error",
     "zero_rmsnorm_fp8", "zero_rmsnorm_workspace_bytes", "zero_rmsnorm_backward",
 ]
 
@@ -247,6 +247,15 @@ def zero_fp8_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torc
           lib().zero_fp8_matmul(pa, _TYPE[a.dtype], lda, psa, ldsa, pb, _TYPE[b.dtype], ldb, psb, ldsb,
                                 tile, po, _TYPE[out.dtype], ldo, m, n, k, add, _flat(ws, dev),
                                 ws.nbytes, _stream(stream, dev)))
+
+
+def read_matmul_error(ws: torch.Tensor) -> bool:
+    """Whether a product with this workspace gave up waiting (synchronises with
+    its stream; never expected).  Its output is then undefined, and the
+    answer stays until the caller clears the word: ``ws[:4].zero_()``."""
+    if not ws.is_contiguous() or ws.nbytes < 4:
+        raise ValueError("ws: the product's workspace expected")
+    return bool(ws.reshape(-1).view(torch.uint8)[:4].any())
 
 
 # ----------------------------------------------------------------- root-mean-square norm
