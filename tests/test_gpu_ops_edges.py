@@ -1,6 +1,7 @@
 """The operators around the step where rounding, range, lengths and sharing of
 buffers are at their edges."""
 import json
+import math
 import os
 import subprocess
 import sys
@@ -9,8 +10,9 @@ import pytest
 import torch
 
 import zero_partitioned_mixed_step_gb300 as zs
-from ops_reference import QMAX, TINY, U, blocks, clip_factor, half_ulp
-from test_gpu_ops import BF16, E4M3, E5M2, F16, F32, gen, normal
+from ops_reference import QMAX, TINY, U, blocks, clip_factor, half_ulp, rmsnorm_backward
+from test_gpu_ops import (BF16, E4M3, E5M2, F16, F32, backward_case, chain, check_product, gen, normal, operand,
+                          workspace)
 
 pytestmark = pytest.mark.gpu
 
@@ -226,3 +228,107 @@ def test_example_stops_on_a_product_that_gave_up():
     layer.mm_ws[0] = 1
     with pytest.raises(RuntimeError):
         train(layer, x, residual, target, 1)
+
+
+@pytest.mark.parametrize("tile,add", [(True, False), (False, True), (False, False)])
+@pytest.mark.parametrize("n,k", [(40_000, 129), (50_257, 769), (39_000, 1100)])
+@pytest.mark.parametrize("m", [1, 17, 64])
+def test_matmul_of_few_rows_walks_many_columns(m, n, k, tile, add):
+    """More tiles than two to an SM: a CTA takes several, its rings of stages, sums and scales in the middle of a turn."""
+    a, sa = operand(m, m, k, E4M3, False)
+    b, sb = operand(n, n, k, E5M2 if add else E4M3, tile)
+    out = normal(3, (m, n), F32 if add else BF16, 5.0)
+    before, ws = out.double(), workspace(m, n, k)
+    zs.zero_fp8_matmul(a, sa, b, sb, out, ws, add=add)
+    check_product(out, a, sa, b, sb, before if add else None)
+    assert not zs.read_matmul_error(ws)
+
+
+# ----------------------------------------------------------------- norm and clip over lists
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("sizes,at", [([9000] * 1100, 0), ([9000] * 1100, 1099), ([3_000_001] * 5, 4), ([50_000] * 2300, 3)])
+def test_norm_of_a_long_list_finds_what_is_not_finite(sizes, at, bad):
+    """Lists whose norm ends in a kernel of its own, and several launches to a list."""
+    dtype = (BF16, F32)[at % 2]
+    xs = [normal(i, (n,), dtype) for i, n in enumerate(sizes)]
+    ws = torch.zeros(zs.zero_tensors_workspace_bytes(xs), dtype=torch.uint8, device="cuda")
+    each = torch.empty(len(xs), dtype=torch.float64, device="cuda")
+    xs[at][-1] = bad
+    stat = zs.new_tensors_stat()
+    zs.zero_tensors_norm(xs, 1.0, stat, ws, each)
+    got = zs.read_tensors_stat(stat)
+    assert got.found_inf == 1 and not math.isfinite(got.sumsq) and not math.isfinite(got.norm)
+    ok = torch.ones(len(xs), dtype=torch.bool)
+    ok[at] = False
+    assert each[ok.cuda()].isfinite().all() and not math.isfinite(float(each[at]))
+    zs.zero_tensors_clip(xs, None, 1.0, 1e-3, stat)  # nothing is clipped
+    assert torch.equal(xs[0][:100], normal(0, (sizes[0],), dtype)[:100])
+    xs[at][-1] = 0.0
+    zs.zero_tensors_norm(xs, 1.0, stat, ws)  # and the workspace carries nothing over
+    assert zs.read_tensors_stat(stat).found_inf == 0
+    assert int(ws[:8].sum()) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_clip_with_a_factor_of_one_keeps_every_bit(dtype):
+    """Every half value (fp32: 2^21 patterns over the whole range) but NaNs, in place and copied."""
+    if dtype == F32:
+        x = torch.arange(0, 1 << 32, 2047, device="cuda").to(torch.int32).view(F32)
+    else:
+        x = torch.arange(1 << 16, device="cuda", dtype=torch.int32).to(torch.int16).view(dtype)
+    x = x[torch.isfinite(x)].contiguous()
+    word = torch.int32 if dtype == F32 else torch.int16
+    before, y, stat = x.clone(), torch.empty_like(x), zs.new_tensors_stat()
+    for max_norm in (0.0, 1e30):  # no limit, and one above the stat's norm of 0
+        zs.zero_tensors_clip([x], [y], 1.0, max_norm, stat)
+        zs.zero_tensors_clip([x], None, 1.0, max_norm, stat)
+        assert torch.equal(x.view(word), before.view(word)) and torch.equal(y.view(word), before.view(word))
+
+
+# ----------------------------------------------------------------- root-mean-square norm
+
+@pytest.mark.parametrize("cols", [257, 1001, 4096, 9001, 17000, 17008])
+def test_rmsnorm_sum_over_the_residual(cols):
+    x, r, w = normal(1, (9, cols), BF16), normal(2, (9, cols), BF16), normal(3, (cols,), F32)
+    h, y, y2 = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+    (q, s), (q2, s2) = zs.fp8_empty(9, cols), zs.fp8_empty(9, cols)
+    zs.zero_rmsnorm_fp8(x, w, 1e-5, residual=r, h=h, y=y, q=q, s=s)
+    zs.zero_rmsnorm_fp8(x, w, 1e-5, residual=r, h=r, y=y2, q=q2, s=s2)
+    assert torch.equal(r, h) and torch.equal(y2, y) and torch.equal(s2, s)
+    same_bits(q2, q)
+
+
+@pytest.mark.parametrize("dtype,dwt", [(BF16, F32), (F16, F16)])
+@pytest.mark.parametrize("rows,cols", [(10_001, 200), (2500, 1000), (1300, 2048), (1000, 4096), (611, 4095), (400, 8192),
+                                       (400, 9001), (333, 12_288), (200, 16_384)])
+def test_rmsnorm_backward_of_many_rows(rows, cols, dtype, dwt):
+    """More rows than CTAs: the next row on its way while this one is reduced,
+    sums of dw over a CTA's rows, outputs over inputs that later rows still read."""
+    h, dy, w, dr, rstd = backward_case(rows, cols, dtype, True, seed=rows)
+    dx, dw = torch.empty_like(h), torch.empty(cols, dtype=dwt, device="cuda")
+    nbytes = zs.zero_rmsnorm_workspace_bytes(rows, cols)
+    parts = nbytes // (4 * cols)
+    assert parts < rows
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda").fill_(255)
+    zs.zero_rmsnorm_backward(dy, h, w, rstd, dx, dw, ws, dres=dr)
+    want, want_w, size, size_w = rmsnorm_backward(dy.double(), h.double(), w.double(), rstd.double(), dr.double())
+    tol = size * (chain(cols) + 4) * U
+    assert ((dx.double() - want).abs() <= tol + half_ulp(want, dtype) * (1 + 1e-6)).all()
+    # xhat's rounding, a CTA's rows, the CTAs' sums by 32 or 128 threads, two shuffles, 8 or 32 warps
+    steps = 1 + -(-rows // parts) + -(-parts // (128 if parts > 512 else 32)) + 2 + (32 if parts > 512 else 8)
+    tol_w = size_w * steps * U
+    assert ((dw.double() - want_w).abs() <= tol_w + half_ulp(want_w, dwt) * (1 + 1e-6)).all()
+    before = normal(9, (cols,), dwt)
+    added = before.clone()
+    zs.zero_rmsnorm_backward(dy, h, w, rstd, dx, added, ws, dres=dr, add_dw=True)
+    sum_w = want_w + before.double()
+    assert ((added.double() - sum_w).abs() <= tol_w + sum_w.abs() * U + half_ulp(sum_w, dwt) * (1 + 1e-6)).all()
+    for over in (dy.clone(), dr.clone()):
+        on_dy = torch.equal(over, dy)
+        again = torch.empty_like(dw)
+        zs.zero_rmsnorm_backward(over if on_dy else dy, h, w, rstd, over, again, ws, dres=dr if on_dy else over)
+        assert torch.equal(over, dx) and torch.equal(again, dw)
+    alone = torch.empty_like(dx)
+    zs.zero_rmsnorm_backward(dy, h, w, rstd, alone, None, None, dres=dr)  # without dw
+    assert torch.equal(alone, dx)
