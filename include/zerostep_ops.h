@@ -93,7 +93,7 @@ ZERO_API int zero_tensors_norm(int n, const void *const *x, const int64_t *numel
                                zero_stream_t stream);
 
 /*
- * out = x * (inv_scale * c), rounded once to out's type, with
+ * out = x * (inv_scale * c), formed in fp32 and rounded to out's type, with
  * c = min(1, max_norm / (sqrt(stat->sumsq) + 1e-6)) as the step's own clip;
  * c = 1 when stat->found_inf, so that what is not finite stays so and reaches
  * the step, which skips, and c = 1 when max_norm is 0 (no clipping) or sumsq is not
@@ -144,6 +144,8 @@ ZERO_API size_t zero_fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k)
  * in fp32 by the tensor cores, the blocks in fp32 in ascending order (in
  * groups, the groups in ascending order, where few outputs make the kernel
  * split k: a rule on the sizes alone); out (F16, BF16 or F32) is rounded once.
+ * sa * sb is formed first, in fp32: a product of scales below 2^-126 loses bits
+ * (below 2^-150 its block counts as zero), one of 2^128 or more is infinite.
  *   forward:              a = activations [tokens, in],   b = weights [out, in] in tiles
  *   input's gradient:     a = gradients [tokens, out],    b = transposed weights [in, out] in tiles
  *   weights' gradient:    a = transposed gradients [out, tokens],

@@ -21,13 +21,18 @@
 // freed and the parts of k that were left out are counted, so that the
 // workspace's counters are zero again.
 //
-// What bounds it: a block of 256x256x128 is 512 cycles of products, and takes
-// about 930, since tensor memory has no room for a third block: the product
-// warp sees a buffer free only a barrier's poll (150 cycles) and a commit (300)
-// after it is.  8192x14336x4096 into bf16, a scale for a tile of b: 395 us, 2.43
-// PFLOP/s.  With a scale for each column of b the scaling itself, 128 products
-// and 128 sums of a thread for each block, is the longer:
-// 14336x4096x8192 added in fp32, 555 us, 1.73 PFLOP/s.
+// What bounds it: latency, no unit (at 4096x4096x4096 the tensor pipe is 39 % busy,
+// issue slots 44, FMA 24).  A block of 256x256x128 is 512 cycles of products and
+// takes about 930: with two blocks in flight a block's sums pass through a commit
+// (300 cycles), polls (150 each), loads and a release one after the other, and
+// two epilogue warps to a scheduler do not cover that.  With a scale for each
+// column of b (tensor 29 %, issue 41, FMA 32) each group of 32 columns is loaded,
+// waited for and used in turn, four times a block.
+//   8192x14336x4096 into bf16, a scale for a tile of b: 395 us, 2.43 PFLOP/s, at
+//   2070 MHz; 422, 2.28, where varied operands bring the clock to the power
+//   limit's 1.93 GHz
+//   14336x4096x8192 added in fp32, a scale for each column: 551 us, 1.75
+//   PFLOP/s, at 2070 MHz, and 561
 // 1021x50257x769 into bf16, rows not on 16 bytes: 85 us; a tile has 7 blocks of
 // k, and its output's way out, which nothing hides, is half of its time.
 #include <cuda.h>

@@ -8,13 +8,15 @@
 // neighbouring rows, 8 neighbouring columns), so that a row's 16 bytes load at
 // once, a row's amax is a reduction over 16 lanes, a column's over 8 registers
 // and the 16 row groups, and 8 rows of a column pack into the 8 bytes that the
-// transposed form has side by side.  What keeps it from the copy rate is a
-// tile's way through loads, maxima and barriers, which the other CTAs of the SM
-// have to cover, and the ALU (half busy: two conversions and a rounding for
-// each element and form).
+// transposed form has side by side.  What keeps it from the copy rate is the
+// latency of a tile's way through loads, maxima and barriers, which only the
+// other three CTAs of the SM cover; no unit is the limit (8192x4096, both forms:
+// issue slots 55 % busy, ALU 48, DRAM 40).
 //   8192x4096 bf16, both forms:  29.2 us, 4.7 TB/s (0.69 of the copy rate)
 //   14336x4096 bf16, 128x128 tiles, both forms:  41.2 us, 5.7 TB/s (0.84)
 // The quotients' second product costs the first 1.5 us and the tiles nothing.
+//   8192x4096, 1x128 blocks, one form alone: bf16 20.6 us (0.72 of the copy rate), its
+//   transpose 25.4 (0.59); fp32 32.9 (0.75), 37.0 (0.67), both 44.7 (0.66)
 #include "ops.cuh"
 
 namespace zo {

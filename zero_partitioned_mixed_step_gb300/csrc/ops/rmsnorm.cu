@@ -7,7 +7,9 @@
 //
 // Both are bound by memory.  A row is held in registers between the sum of
 // its squares and its use, so each input is read once and each output written
-// once; the row's statistics, the gradients' sums and dw are fp32.
+// once; the row's statistics, the gradients' sums and dw are fp32.  The sizes of
+// CTAs are powers of two and a thread takes 8 columns at a time: widths below
+// one leave threads idle and fewer bytes in flight (each pass's figures).
 #include "ops.cuh"
 
 namespace zo {
@@ -115,7 +117,9 @@ __device__ __forceinline__ void load_h(const NormParams &p, int64_t row, int64_t
 // T threads to a row, V units of 8 elements to a thread; CTAs of max(T, 256).
 // h, which is of a half type, stays packed between its two uses.
 // 8192x4096 with a residual, h, y and 8 bits out: 50.9 us, 5.9 TB/s (0.88 of the
-// copy rate); with one unit to each of 512 threads 56.0.
+// copy rate); with one unit to each of 512 threads 56.0.  Without y, of the copy
+// rate: 32768x1024 0.69, 8192x4096 0.74, 4096x8192 0.65; between, 65536x320 0.21,
+// 32768x640 0.41, 8192x2304 0.45, 8192x5120 0.47, 4096x12288 0.48; 262144x64 0.15.
 template <class H, int F8, int T, int V>
 __global__ void __launch_bounds__(T > 256 ? T : 256, T > 512 ? 1 : T > 256 ? 2 : 5) rmsnorm_kernel(const NormParams p)
 {
@@ -239,6 +243,8 @@ struct BackParams {
 // TB/s (in column order and launched after the pass 54.0).  The next row's
 // loads took 18 us off; three rows ahead in registers cost 16, in a ring of
 // asynchronous copies 1; two rows to a barrier, 512 threads to an SM, 0.6.
+// Of the copy rate: 32768x1024 0.83, 4096x8192 0.80; between, 65536x320 0.30,
+// 32768x640 0.52, 8192x2304 0.56, 8192x5120 0.67; 262144x64 0.22.
 template <class H, int T>
 __global__ void __launch_bounds__(T, 1024 / T) rmsnorm_backward_kernel(const BackParams p)
 {
@@ -297,7 +303,8 @@ __global__ void __launch_bounds__(T, 1024 / T) rmsnorm_backward_kernel(const Bac
 }
 
 // Rows too long for the registers: dw's sums live in the workspace between
-// rows (each thread its own columns).
+// rows (each thread its own columns), and dy and h are read twice.  4096x12288
+// 167 us, 0.35 of the copy rate; 2048x16384 98, 0.40.
 template <class H>
 __global__ void __launch_bounds__(1024) rmsnorm_backward_long_kernel(const BackParams p)
 {
