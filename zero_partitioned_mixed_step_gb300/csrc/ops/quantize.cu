@@ -36,7 +36,7 @@ struct QuantParams {
 
 // A thread's 8x8 patch as it lies in memory.  Halves stay packed: half the
 // registers, so that four CTAs fit an SM (28.9 us for three's 31.2 at 8192x4096,
-// both forms), and their magnitudes are compared
+// both forms, with one product to a quotient), and their magnitudes are compared
 // two at a time.
 template <class T>
 struct Patch {
