@@ -1,5 +1,6 @@
-"""Build libzerostep.so (the step) and libzerostep_ops.so (the operators around
-it) in-tree with nvcc for sm_103a."""
+"""Build libzerostep.so (the step), libzerostep_ops.so (the operators around it)
+and libzerostep_layer.so (what lies between a layer's products) in-tree with nvcc
+for sm_103a."""
 from __future__ import annotations
 
 import concurrent.futures
@@ -17,6 +18,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libzerostep.so")
 OPS = os.path.join(CSRC, "ops")
 OPS_LIB = os.path.join(BUILD, "libzerostep_ops.so")
+LAYER = os.path.join(CSRC, "layer")
+LAYER_LIB = os.path.join(BUILD, "libzerostep_layer.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -58,6 +61,16 @@ def _ops_inputs():
         os.path.join(INCLUDE, "zerostep.h"), os.path.join(INCLUDE, "zerostep_ops.h"), __file__]
 
 
+def _layer_sources():
+    return sorted(glob.glob(os.path.join(LAYER, "*.cu")))
+
+
+def _layer_inputs():
+    return _layer_sources() + glob.glob(os.path.join(LAYER, "*.cuh")) + [
+        os.path.join(OPS, "ops.cuh"), os.path.join(INCLUDE, "zerostep.h"), os.path.join(INCLUDE, "zerostep_ops.h"),
+        os.path.join(INCLUDE, "zerostep_layer.h"), __file__]
+
+
 def _older(lib: str, inputs) -> bool:
     if not os.path.exists(lib):
         return True
@@ -66,15 +79,18 @@ def _older(lib: str, inputs) -> bool:
 
 
 def stale() -> bool:
-    return _older(LIB, _inputs()) or _older(OPS_LIB, _ops_inputs())
+    return (_older(LIB, _inputs()) or _older(OPS_LIB, _ops_inputs())
+            or _older(LAYER_LIB, _layer_inputs()))
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every translation unit of both libraries in parallel and link
+    """Compile every translation unit of the libraries in parallel and link
     them.  Returns the step library's path."""
     todo = [(lib, sources(), flags)
             for lib, sources, inputs, flags in ((LIB, _sources, _inputs, NVCC_FLAGS),
-                                                (OPS_LIB, _ops_sources, _ops_inputs, OPS_NVCC_FLAGS))
+                                                (OPS_LIB, _ops_sources, _ops_inputs, OPS_NVCC_FLAGS),
+                                                (LAYER_LIB, _layer_sources, _layer_inputs,
+                                                 OPS_NVCC_FLAGS))
             if force or _older(lib, inputs())]
     if not todo:
         return LIB
@@ -82,7 +98,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     def compile_one(job):
         lib, src, flags = job
-        obj = os.path.join(BUILD, ("ops_" if lib == OPS_LIB else "") + os.path.basename(src) + ".o")
+        obj = os.path.join(BUILD, {OPS_LIB: "ops_", LAYER_LIB: "layer_"}.get(lib, "") + os.path.basename(src) + ".o")
         cmd = [nvcc(), *flags, "-c", src, "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
@@ -92,7 +108,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return lib, obj, r.stderr
 
     objs = {}
-    with concurrent.futures.ThreadPoolExecutor(max_workers=8) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=12) as ex:
         for lib, obj, log in ex.map(compile_one, [(lib, src, flags) for lib, srcs, flags in todo
                                                   for src in srcs]):
             objs.setdefault(lib, []).append(obj)
