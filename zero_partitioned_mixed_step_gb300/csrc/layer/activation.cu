@@ -4,25 +4,37 @@
 //   silu: z = u;  gelu's tanh form: z = 2 sqrt(2 / pi) (u + 0.044715 u^3)
 //   du = da v (sig + u sig (1 - sig) z'),  dv = da u sig
 #include <initializer_list>
+#include <type_traits>
 
 #include "layer.cuh"
 
 namespace zo {
 
-// sig(z(u)) and z'(u).  exp and the quotient are approximate to a few fp32 units; a
-// quotient by 2^126 and more is 0.
+// sig(z(u)) and z'(u).  exp2 and the reciprocal are approximate to an fp32 unit or two; a
+// reciprocal of 2^126 and more is 0.
 template <bool GELU>
-__device__ __forceinline__ float sigmoid_of(float u, float &dz)
+__device__ __forceinline__ float2 sigmoid_of(float2 u, float2 &dz)
 {
-    float z = u;
-    dz = 1.0f;
+    constexpr float kLog2e = 1.4426950408889634f;
+    float2 z;
     if (GELU) {
         // beyond 16 the sigmoid is 0 or 1 in fp32; u^3 stays finite (a NaN reaches the result through u)
-        const float c = fminf(fmaxf(u, -16.0f), 16.0f), k = 1.5957691216057308f, c2 = c * c;
-        z = k * c * fmaf(0.044715f, c2, 1.0f);
-        dz = k * fmaf(3.0f * 0.044715f, c2, 1.0f);
+        const float2 c = make_float2(fminf(fmaxf(u.x, -16.0f), 16.0f), fminf(fmaxf(u.y, -16.0f), 16.0f));
+        constexpr float k = 1.5957691216057308f;
+        const float2 c2 = mul2(c, c);
+        dz = fma2(both(k * 3.0f * 0.044715f), c2, both(k));
+        z = mul2(mul2(both(-kLog2e), c), fma2(both(k * 0.044715f), c2, both(k)));
+    } else {
+        dz = both(1.0f);
+        z = mul2(both(-kLog2e), u);
     }
-    return __fdividef(1.0f, 1.0f + __expf(-z));
+    float2 e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(z.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(z.y));
+    e = add2(e, both(1.0f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+    return r;
 }
 
 // ------------------------------------------------------------------ forward
@@ -31,63 +43,84 @@ struct ActParams {
     const void *u, *v;
     void *a;
     Form a8, u8, v8;
-    int64_t ldu, ldv, lda, rows, cols;
-    int64_t row_tiles;
-    int32_t wide, e5m2;
+    int64_t ldu, ldv, lda;
+    int32_t rows, cols;
+    Tiles tiles;
+    int32_t e5m2;
 };
-
-template <class H>
-__device__ __forceinline__ void put_kept(const Form &f, int64_t row, int64_t c, int n, const Raw8<H> &r)
-{
-    Amax<H> a;
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        a.add(r.w[i]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        x[i] = r.at(i);
-    put_form(f, row, c, n, x, a.bits(), false);
-}
 
 constexpr int kActRows = 32;  // rows of a CTA: two to each 16 lanes
 
 // A CTA takes 128 columns of 32 neighbouring rows, whose scales lie side by side.
-template <class H, bool GELU>
+template <class H, bool GELU, int W>
 __global__ void __launch_bounds__(256) act_kernel(const ActParams p)
 {
-    const int64_t c = blockIdx.x / p.row_tiles * kBlock + (threadIdx.x & 15) * 8;
-    const int64_t r0 = blockIdx.x % p.row_tiles * kActRows + (threadIdx.x >> 4);
-    const int nc = in_row(p.cols, c);
+    const int lane = threadIdx.x & 15;
+    const TileAt at = tile_at(p.tiles);
+    const int64_t tc = at.c, row = (int64_t)at.r * kActRows + (threadIdx.x >> 4) * 2;
+    const int c = at.c * kBlock + lane * 8, nc = left_of(p.cols, c);
+    const int n[2] = {row < p.rows ? nc : 0, row + 1 < p.rows ? nc : 0};
     Raw8<H> u[2], v[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int64_t row = r0 + 16 * k;
-        const int n = row < p.rows ? nc : 0;
-        u[k] = load_raw(static_cast<const H *>(p.u) + row * p.ldu + c, n, p.wide);
+        u[k] = get_raw<W>(static_cast<const H *>(p.u) + (row + k) * p.ldu + c, n[k]);
         if (p.v)
-            v[k] = load_raw(static_cast<const H *>(p.v) + row * p.ldv + c, n, p.wide);
+            v[k] = get_raw<W>(static_cast<const H *>(p.v) + (row + k) * p.ldv + c, n[k]);
     }
+    // two rows into a form; lanes 8 .. 15 hold the second one's scale
+    auto put_scale = [&](const Form &f, float s) {
+        const int64_t r = row + (lane >> 3);
+        if ((lane & 7) == 0 && r < p.rows)
+            f.s[tc * f.lds + r] = s;
+    };
+    auto put_kept = [&](const Form &f, const Raw8<H> (&r)[2]) {
+        uint32_t most[2] = {amax8(r[0]), amax8(r[1])};
+        const float s = scale_of(max_shared(most), false);
+        const Inverse inv = inverse_of(quick_inverse(s), s);
+        put_scale(f, s);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const Inverse d = {shared_value<2>(inv.hi, k), shared_value<2>(inv.lo, k)};
+            float2 x[4];
+            pairs_of(r[k], x);
+            if (n[k] > 0)
+                put_bytes<W>(f.q + (row + k) * f.ld + c, n[k], bytes_of(x, d, false));
+        }
+    };
+    float2 a[2][4];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int64_t row = r0 + 16 * k;
-        const int n = row < p.rows ? nc : 0;
-        float a[8];
+        float2 x[4], dz;
+        pairs_of(u[k], x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float dz;
-            a[i] = u[k].at(i) * sigmoid_of<GELU>(u[k].at(i), dz);
-            if (p.v)
-                a[i] *= v[k].at(i);
+        for (int i = 0; i < 4; ++i)
+            a[k][i] = mul2(x[i], sigmoid_of<GELU>(x[i], dz));
+        if (p.v) {
+            pairs_of(v[k], x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                a[k][i] = mul2(a[k][i], x[i]);
         }
-        if (p.a && n > 0)
-            store8(static_cast<H *>(p.a) + row * p.lda + c, n, p.wide, a);
-        if (p.a8.q)
-            put_form(p.a8, row, c, n, a, amax8(a), p.e5m2);
-        if (p.u8.q)
-            put_kept(p.u8, row, c, n, u[k]);
-        if (p.v8.q)
-            put_kept(p.v8, row, c, n, v[k]);
+    }
+    if (p.u8.q)
+        put_kept(p.u8, u);
+    if (p.v8.q)
+        put_kept(p.v8, v);
+    if (p.a)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (n[k] > 0)
+                put_pairs<W>(static_cast<H *>(p.a) + (row + k) * p.lda + c, n[k], a[k]);
+    if (p.a8.q) {
+        uint32_t most[2] = {amax8(a[0]), amax8(a[1])};
+        const float s = scale_of(max_shared(most), p.e5m2), inv = quick_inverse(s);
+        put_scale(p.a8, s);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float d = shared_value<2>(inv, k);
+            if (n[k] > 0)
+                put_bytes<W>(p.a8.q + (row + k) * p.a8.ld + c, n[k], bytes_of(a[k], d, p.e5m2));
+        }
     }
 }
 
@@ -98,169 +131,220 @@ struct ActBackParams {
     const float *su, *sv;
     void *du, *dv;
     Form du8, dv8, du8t, dv8t, a8t;
-    int64_t ldda, ldu, ldv, ldsu, ldsv, lddu, lddv, rows, cols;
-    int64_t row_tiles;
-    int32_t wide, wide_kept, e5m2;
+    int64_t ldda, ldu, ldv, ldsu, ldsv, lddu, lddv;
+    int32_t rows, cols;
+    Tiles tiles;
+    int32_t e5m2;
 };
 
-constexpr int kBackThreads = 512;  // 32 groups of 16 lanes, 4 rows to a group
+constexpr int kBackThreads = 256;  // 16 groups of 16 lanes, 8 rows to a group
 
 // bf16 values of the 128x128 tile on their way to the transposed forms: a row's 128
-// values are 16 units of 8; unit j of row r lies at j ^ (r / 16), its halves
-// exchanged where r / 8 is odd.  So 4 neighbouring columns c = 4k .. of row r are the
-// 8 bytes at place k ^ (r / 8): the 16 lanes of a column (8 rows each) read
-// different banks, and so do the 16 lanes of a row as they write.
+// values are 16 units of 8; unit j of a row of group g (rows 8g ..) lies at j ^ (g / 2), its
+// halves exchanged where g is odd.  So 4 neighbouring columns 4k .. of that row are the
+// 8 bytes at place k ^ g: the 16 lanes of a column (8 rows each) read different banks,
+// and so do the 16 lanes of a row as they write.
 struct Staged {
     uint2 row[kBlock][32];
 };
-__device__ __forceinline__ void stage8(Staged &t, int r, int j, const float x[8])
+__device__ __forceinline__ void stage8(Staged &t, int group, int i, int j, const float2 x[4])
 {
-    const uint2 lo = make_uint2(word_of<bf16>(x[0], x[1]), word_of<bf16>(x[2], x[3]));
-    const uint2 hi = make_uint2(word_of<bf16>(x[4], x[5]), word_of<bf16>(x[6], x[7]));
-    const bool turned = r >> 3 & 1;
-    const uint2 a = turned ? hi : lo, b = turned ? lo : hi;
-    *reinterpret_cast<uint4 *>(&t.row[r][2 * (j ^ r >> 4)]) = make_uint4(a.x, a.y, b.x, b.y);
+    const uint2 lo = make_uint2(word_of<bf16>(x[0].x, x[0].y), word_of<bf16>(x[1].x, x[1].y));
+    const uint2 hi = make_uint2(word_of<bf16>(x[2].x, x[2].y), word_of<bf16>(x[3].x, x[3].y));
+    const uint2 a = group & 1 ? hi : lo, b = group & 1 ? lo : hi;
+    *reinterpret_cast<uint4 *>(&t.row[group * 8 + i][2 * (j ^ group >> 1)]) = make_uint4(a.x, a.y, b.x, b.y);
 }
 
 // Four columns (from 4k on) of a tile, 8 rows to each of 16 lanes, into a transposed
 // form.  amax: of the tile's columns, of the fp32 values.
+template <int W>
 __device__ __forceinline__ void put_columns(const Form &f, const Staged &t, const uint32_t *amax, int k, int64_t c0,
-                                            int64_t cols, int64_t r0, int64_t rows, bool e5m2)
+                                            int cols, int64_t r0, int rows, bool e5m2)
 {
     const int lane = threadIdx.x & 15;
     uint2 w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         w[i] = t.row[lane * 8 + i][k ^ lane];
-    // each lane forms one of the four scales
-    const float s = scale_of(amax[4 * k + (lane & 3)], e5m2);
-    const Inverse mine = inverse(s);
+    const float s = scale_of(amax[4 * k + (lane & 3)], e5m2);  // each lane forms one of the four scales
+    const float inv = quick_inverse(s);
     const int64_t c = c0 + 4 * k;
     if (lane < 4 && c + lane < cols)
         f.s[r0 / kBlock * f.lds + c + lane] = s;
     const int64_t row = r0 + lane * 8;
-    const int n = in_row(rows, row);
+    const int n = row < rows ? left_of(rows, (int)row) : 0;
+    uint8_t *to = f.q + c * f.ld + row;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const Inverse d = {__shfl_sync(0xFFFFFFFFu, mine.hi, j, 16), __shfl_sync(0xFFFFFFFFu, mine.lo, j, 16)};
-        float x[8];
+        const float d = __shfl_sync(0xFFFFFFFFu, inv, j, 16);
+        float2 x[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t two = j < 2 ? w[i].x : w[i].y;
-            x[i] = __uint_as_float(j & 1 ? two & 0xFFFF0000u : two << 16);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t p = j < 2 ? w[2 * i].x : w[2 * i].y, q = j < 2 ? w[2 * i + 1].x : w[2 * i + 1].y;
+            x[i] = j & 1 ? make_float2(__uint_as_float(p & 0xFFFF0000u), __uint_as_float(q & 0xFFFF0000u))
+                         : make_float2(__uint_as_float(p << 16), __uint_as_float(q << 16));
         }
-        const uint2 q = quotients_of(x, d, e5m2);
+        const uint2 q = bytes_of(x, d, e5m2);
         if (n > 0 && c + j < cols)
-            store8b(f.q + (c + j) * f.ld + row, n, f.wide, q);
+            put_bytes<W>(to + j * f.ld, n, q);
     }
 }
 
-// A CTA takes a 128x128 tile: rows first (gradients, their 8-bit forms along the row,
-// the columns' largest magnitudes), then, if a transposed form is wanted, columns.
-template <class H, bool S8, bool GATED, bool GELU>
-__global__ void __launch_bounds__(kBackThreads, 1) act_backward_kernel(const ActBackParams p)
+// A CTA takes a 128x128 tile: rows first, two at a time with the next two on their way
+// (gradients, their 8-bit forms along the row, the columns' largest magnitudes), then, if a
+// transposed form is wanted, columns.
+template <class H, bool S8, bool GATED, bool GELU, int W>
+__global__ void __launch_bounds__(kBackThreads, 2) act_backward_kernel(const ActBackParams p)
 {
     using K = Kept<H, S8>;
-    constexpr int kRows = kBlock * 16 / kBackThreads;
+    constexpr int kElem = K::kBytes / 8, kForms = GATED ? 3 : 2, kMaxima = GATED ? 4 : 2;
     extern __shared__ __align__(16) unsigned char dynamic[];
     Staged *tile = reinterpret_cast<Staged *>(dynamic);  // du, a and dv
-    __shared__ uint32_t amax[3][kBlock];
+    __shared__ uint32_t amax[kForms][kBlock];
     const bool trans = p.du8t.q || p.dv8t.q || p.a8t.q;
     const int j = threadIdx.x & 15, group = threadIdx.x >> 4;
-    const int64_t tr = blockIdx.x % p.row_tiles, tc = blockIdx.x / p.row_tiles;
-    const int64_t r0 = tr * kBlock, c0 = tc * kBlock, c = c0 + j * 8;
-    const int nc = in_row(p.cols, c);
+    const TileAt at = tile_at(p.tiles);
+    const int64_t tc = at.c, r0 = (int64_t)at.r * kBlock, c0 = tc * kBlock, first = r0 + group * 8;
+    const int c = at.c * kBlock + j * 8, nc = left_of(p.cols, c);
     if (trans) {
-        for (int i = threadIdx.x; i < 3 * kBlock; i += kBackThreads)
+        for (int i = threadIdx.x; i < kForms * kBlock; i += kBackThreads)
             (&amax[0][0])[i] = 0;
         __syncthreads();
     }
-    Raw8<H> da[kRows];
-    K u[kRows], v[kRows];
-    float su[kRows], sv[kRows];
+    Raw8<H> da[2];
+    K u[2], v[2];
+    float su[2], sv[2];
+    auto fetch = [&](int64_t row) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int64_t row = r0 + group * kRows + i;
-        const int n = row < p.rows ? nc : 0;
-        da[i] = load_raw(static_cast<const H *>(p.da) + row * p.ldda + c, n, p.wide);
-        u[i].load(p.u, row * p.ldu + c, n, p.wide_kept);
-        su[i] = S8 && n > 0 ? p.su[tc * p.ldsu + row] : 1.0f;
-        if (GATED) {
-            v[i].load(p.v, row * p.ldv + c, n, p.wide_kept);
-            sv[i] = S8 && n > 0 ? p.sv[tc * p.ldsv + row] : 1.0f;
-        }
-    }
-    uint32_t most[GATED ? 3 : 2][8] = {};
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int r = group * kRows + i;
-        const int64_t row = r0 + r;
-        const int n = row < p.rows ? nc : 0;
-        float uf[8], vf[8], du[8], dv[8], a[8];
-        u[i].get(uf, su[i]);
-        if (GATED)
-            v[i].get(vf, sv[i]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            float dz;
-            const float sig = sigmoid_of<GELU>(uf[k], dz), act = uf[k] * sig, g = da[i].at(k);
-            const float slope = fmaf(act * (1.0f - sig), dz, sig);
+        for (int i = 0; i < 2; ++i) {
+            const int n = row + i < p.rows ? nc : 0;
+            da[i] = get_raw<W>(static_cast<const H *>(p.da) + (row + i) * p.ldda + c, n);
+            u[i].template load<W>(static_cast<const unsigned char *>(p.u) + (row + i) * p.ldu * kElem, c, n);
+            su[i] = sv[i] = 1.0f;
+            if (S8 && n > 0)
+                su[i] = p.su[tc * p.ldsu + row + i];
             if (GATED) {
-                du[k] = g * vf[k] * slope;
-                dv[k] = g * act;
-                a[k] = act * vf[k];
-            } else {
-                du[k] = g * slope;
-                a[k] = act;
+                v[i].template load<W>(static_cast<const unsigned char *>(p.v) + (row + i) * p.ldv * kElem, c, n);
+                if (S8 && n > 0)
+                    sv[i] = p.sv[tc * p.ldsv + row + i];
             }
         }
-        if (p.du && n > 0)
-            store8(static_cast<H *>(p.du) + row * p.lddu + c, n, p.wide, du);
-        if (p.du8.q)
-            put_form(p.du8, row, c, n, du, amax8(du), p.e5m2);
-        if (GATED && p.dv && n > 0)
-            store8(static_cast<H *>(p.dv) + row * p.lddv + c, n, p.wide, dv);
-        if (GATED && p.dv8.q)
-            put_form(p.dv8, row, c, n, dv, amax8(dv), p.e5m2);
-        if (trans) {
-            stage8(tile[0], r, j, du);
-            stage8(tile[1], r, j, a);
-            if (GATED)
-                stage8(tile[2], r, j, dv);
+    };
+    fetch(first);
+    float most[kForms][8] = {};
+#pragma unroll 1
+    for (int step = 0; step < 8; step += 2) {
+        float2 g[2][4], uf[2][4], vf[2][4], du[2][4], dv[2][4], a[2][4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                most[0][k] = max(most[0][k], magnitude(du[k]));
-                most[1][k] = max(most[1][k], magnitude(a[k]));
+        for (int i = 0; i < 2; ++i) {
+            pairs_of(da[i], g[i]);
+            u[i].get(uf[i]);
+            if (GATED)
+                v[i].get(vf[i]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (S8)
+                    uf[i][k] = mul2(uf[i][k], both(su[i]));
+                if (S8 && GATED)
+                    vf[i][k] = mul2(vf[i][k], both(sv[i]));
+            }
+        }
+        const int64_t row = first + step;
+        const int n[2] = {row < p.rows ? nc : 0, row + 1 < p.rows ? nc : 0};
+        if (step < 6)
+            fetch(row + 2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float2 dz;
+                const float2 sig = sigmoid_of<GELU>(uf[i][k], dz), act = mul2(uf[i][k], sig);
+                const float2 rest = fma2(sig, both(-1.0f), both(1.0f));
+                const float2 slope = fma2(act, GELU ? mul2(rest, dz) : rest, sig);
+                if (GATED) {
+                    du[i][k] = mul2(mul2(g[i][k], vf[i][k]), slope);
+                    dv[i][k] = mul2(g[i][k], act);
+                    a[i][k] = mul2(act, vf[i][k]);
+                } else {
+                    du[i][k] = mul2(g[i][k], slope);
+                    a[i][k] = act;
+                }
+            }
+        if (trans) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                stage8(tile[0], group, step + i, j, du[i]);
+                stage8(tile[1], group, step + i, j, a[i]);
                 if (GATED)
-                    most[GATED ? 2 : 0][k] = max(most[GATED ? 2 : 0][k], magnitude(dv[k]));
+                    stage8(tile[2], group, step + i, j, dv[i]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                most[0][2 * k] = max3(most[0][2 * k], du[0][k].x, du[1][k].x);
+                most[0][2 * k + 1] = max3(most[0][2 * k + 1], du[0][k].y, du[1][k].y);
+                most[1][2 * k] = max3(most[1][2 * k], a[0][k].x, a[1][k].x);
+                most[1][2 * k + 1] = max3(most[1][2 * k + 1], a[0][k].y, a[1][k].y);
+                if (GATED) {
+                    most[kForms - 1][2 * k] = max3(most[kForms - 1][2 * k], dv[0][k].x, dv[1][k].x);
+                    most[kForms - 1][2 * k + 1] = max3(most[kForms - 1][2 * k + 1], dv[0][k].y, dv[1][k].y);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (p.du && n[i] > 0)
+                put_pairs<W>(static_cast<H *>(p.du) + (row + i) * p.lddu + c, n[i], du[i]);
+            if (GATED && p.dv && n[i] > 0)
+                put_pairs<W>(static_cast<H *>(p.dv) + (row + i) * p.lddv + c, n[i], dv[i]);
+        }
+        if (p.du8.q || (GATED && p.dv8.q)) {
+            uint32_t m[kMaxima];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m[i] = amax8(du[i]);
+                if (GATED)
+                    m[kMaxima - 2 + i] = amax8(dv[i]);
+            }
+            const float s = scale_of(max_shared(m), p.e5m2), inv = quick_inverse(s);
+            const int mine = shared_index<kMaxima>();
+            const Form &f = mine < 2 ? p.du8 : p.dv8;
+            if (j % (16 / kMaxima) == 0 && f.q && row + (mine & 1) < p.rows)
+                f.s[tc * f.lds + row + (mine & 1)] = s;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float d0 = shared_value<kMaxima>(inv, i), d1 = shared_value<kMaxima>(inv, kMaxima - 2 + i);
+                if (p.du8.q && n[i] > 0)
+                    put_bytes<W>(p.du8.q + (row + i) * p.du8.ld + c, n[i], bytes_of(du[i], d0, p.e5m2));
+                if (GATED && p.dv8.q && n[i] > 0)
+                    put_bytes<W>(p.dv8.q + (row + i) * p.dv8.ld + c, n[i], bytes_of(dv[i], d1, p.e5m2));
             }
         }
     }
     if (!trans)
         return;
 #pragma unroll
-    for (int f = 0; f < (GATED ? 3 : 2); ++f)
+    for (int f = 0; f < kForms; ++f)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t m = max(most[f][k], __shfl_xor_sync(0xFFFFFFFFu, most[f][k], 16));
-            if ((threadIdx.x & 16) == 0)
-                atomicMax(&amax[f][j * 8 + k], m);  // a maximum: in any order the same
-        }
+        for (int k = 0; k < 8; ++k)
+            atomicMax(&amax[f][j * 8 + k], __float_as_uint(most[f][k]));  // a maximum: in any order the same
     __syncthreads();
-    if (p.du8t.q)
-        put_columns(p.du8t, tile[0], amax[0], group, c0, p.cols, r0, p.rows, p.e5m2);
-    if (p.a8t.q)
-        put_columns(p.a8t, tile[1], amax[1], group, c0, p.cols, r0, p.rows, false);
-    if (GATED && p.dv8t.q)
-        put_columns(p.dv8t, tile[2], amax[2], group, c0, p.cols, r0, p.rows, p.e5m2);
+#pragma unroll 1
+    for (int k = group; k < 32; k += 16) {
+        if (p.du8t.q)
+            put_columns<W>(p.du8t, tile[0], amax[0], k, c0, p.cols, r0, p.rows, p.e5m2);
+        if (p.a8t.q)
+            put_columns<W>(p.a8t, tile[1], amax[1], k, c0, p.cols, r0, p.rows, false);
+        if (GATED && p.dv8t.q)
+            put_columns<W>(p.dv8t, tile[kForms - 1], amax[kForms - 1], k, c0, p.cols, r0, p.rows, p.e5m2);
+    }
 }
 
-template <class H, bool S8, bool GATED, bool GELU>
+template <class H, bool S8, bool GATED, bool GELU, int W>
 static int launch_act_backward(const ActBackParams &p, int64_t grid, cudaStream_t stream)
 {
     const bool trans = p.du8t.q || p.dv8t.q || p.a8t.q;
     const int bytes = trans ? (GATED ? 3 : 2) * (int)sizeof(Staged) : 0;
-    auto kernel = act_backward_kernel<H, S8, GATED, GELU>;
+    auto kernel = act_backward_kernel<H, S8, GATED, GELU, W>;
     if (bytes) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess)
@@ -270,14 +354,14 @@ static int launch_act_backward(const ActBackParams &p, int64_t grid, cudaStream_
     return launch_status();
 }
 
-template <class H, bool S8>
+template <class H, bool S8, int W>
 static int choose_act_backward(const ActBackParams &p, bool gelu, int64_t grid, cudaStream_t stream)
 {
     if (p.v)
-        return gelu ? launch_act_backward<H, S8, true, true>(p, grid, stream)
-                    : launch_act_backward<H, S8, true, false>(p, grid, stream);
-    return gelu ? launch_act_backward<H, S8, false, true>(p, grid, stream)
-                : launch_act_backward<H, S8, false, false>(p, grid, stream);
+        return gelu ? launch_act_backward<H, S8, true, true, W>(p, grid, stream)
+                    : launch_act_backward<H, S8, true, false, W>(p, grid, stream);
+    return gelu ? launch_act_backward<H, S8, false, true, W>(p, grid, stream)
+                : launch_act_backward<H, S8, false, false, W>(p, grid, stream);
 }
 
 }  // namespace zo
@@ -318,21 +402,30 @@ int zero_activation_fp8(const void *u, int64_t ldu, const void *v, int64_t ldv, 
     p.ldu = ldu;
     p.ldv = ldv;
     p.lda = lda;
-    p.rows = rows;
-    p.cols = cols;
-    p.row_tiles = ceil_div(rows, kActRows);
-    p.wide = rows_aligned(u, ldu, b, 16) && (!v || rows_aligned(v, ldv, b, 16)) && (!a || rows_aligned(a, lda, b, 16));
+    p.rows = (int32_t)rows;
+    p.cols = (int32_t)cols;
+    p.tiles = tiles_of(rows, cols, kActRows);
+    bool wide = rows_aligned(u, ldu, b, 16) && (!v || rows_aligned(v, ldv, b, 16)) && (!a || rows_aligned(a, lda, b, 16));
+    for (const Form *f : {&p.a8, &p.u8, &p.v8})
+        wide = wide && (!f->q || f->wide);
     p.e5m2 = a8 && fp8 == ZERO_T_E5M2;
-    const int64_t grid = p.row_tiles * ceil_div(cols, kBlock);
+    const int64_t grid = (int64_t)p.tiles.rows * p.tiles.cols;
     if (grid > kMaxDim)
         return ZERO_EINVAL;
     auto go = [&](auto kernel) {
         kernel<<<(unsigned)grid, 256, 0, stream>>>(p);
         return launch_status();
     };
-    if (type == ZERO_T_F16)
-        return act == ZERO_ACT_GELU ? go(act_kernel<f16, true>) : go(act_kernel<f16, false>);
-    return act == ZERO_ACT_GELU ? go(act_kernel<bf16, true>) : go(act_kernel<bf16, false>);
+    auto by_type = [&](auto half) {
+        using H = decltype(half);
+        auto by_act = [&](auto gelu) {
+            constexpr bool G = decltype(gelu)::value;
+            return !wide ? go(act_kernel<H, G, kApart>)
+                         : cols % 8 ? go(act_kernel<H, G, kWide>) : go(act_kernel<H, G, kWhole>);
+        };
+        return act == ZERO_ACT_GELU ? by_act(std::true_type{}) : by_act(std::false_type{});
+    };
+    return type == ZERO_T_F16 ? by_type(f16{}) : by_type(bf16{});
 }
 
 int zero_activation_backward_fp8(const void *da, int64_t ldda, const void *u, int64_t ldu, const float *su,
@@ -387,23 +480,30 @@ int zero_activation_backward_fp8(const void *da, int64_t ldda, const void *u, in
     p.ldsv = ldsv;
     p.lddu = lddu;
     p.lddv = lddv;
-    p.rows = rows;
-    p.cols = cols;
-    p.row_tiles = ceil_div(rows, kBlock);
-    p.wide = rows_aligned(da, ldda, b, 16) && (!du || rows_aligned(du, lddu, b, 16)) &&
-             (!dv || rows_aligned(dv, lddv, b, 16));
+    p.rows = (int32_t)rows;
+    p.cols = (int32_t)cols;
+    p.tiles = tiles_of(rows, cols, kBlock);
     const int kb = su ? 1 : b, to = su ? 8 : 16;
-    p.wide_kept = rows_aligned(u, ldu, kb, to) && (!v || rows_aligned(v, ldv, kb, to));
+    bool wide = rows_aligned(da, ldda, b, 16) && (!du || rows_aligned(du, lddu, b, 16)) &&
+                (!dv || rows_aligned(dv, lddv, b, 16)) && rows_aligned(u, ldu, kb, to) &&
+                (!v || rows_aligned(v, ldv, kb, to));
+    for (const Form *f : {&p.du8, &p.dv8, &p.du8t, &p.dv8t, &p.a8t})
+        wide = wide && (!f->q || f->wide);
     p.e5m2 = fp8 == ZERO_T_E5M2;
-    const int64_t grid = p.row_tiles * ceil_div(cols, kBlock);
+    const int64_t grid = (int64_t)p.tiles.rows * p.tiles.cols;
     if (grid > kMaxDim)
         return ZERO_EINVAL;
     const bool gelu = act == ZERO_ACT_GELU;
+    auto go = [&](auto half, auto kept) {
+        using H = decltype(half);
+        constexpr bool S8 = decltype(kept)::value;
+        return !wide ? choose_act_backward<H, S8, kApart>(p, gelu, grid, stream)
+                     : cols % 8 || rows % 8 ? choose_act_backward<H, S8, kWide>(p, gelu, grid, stream)
+                                            : choose_act_backward<H, S8, kWhole>(p, gelu, grid, stream);
+    };
     if (type == ZERO_T_F16)
-        return su ? choose_act_backward<f16, true>(p, gelu, grid, stream)
-                  : choose_act_backward<f16, false>(p, gelu, grid, stream);
-    return su ? choose_act_backward<bf16, true>(p, gelu, grid, stream)
-              : choose_act_backward<bf16, false>(p, gelu, grid, stream);
+        return su ? go(f16{}, std::true_type{}) : go(f16{}, std::false_type{});
+    return su ? go(bf16{}, std::true_type{}) : go(bf16{}, std::false_type{});
 }
 
 }  // extern "C"

@@ -1,0 +1,346 @@
+// The norms behind and ahead of a block, its gate and the residual stream in one
+// pass over the rows:
+//
+//   xo = o * ro, ro = 1 / sqrt(mean(o^2) + eps)   (xo = o without a norm behind the block)
+//   h = scale * x + gate * w_post * xo
+//   y = h * rh * w_pre, rh = 1 / sqrt(mean(h^2) + eps)
+//
+// Each input is read once and each output written once, but three 8-bit forms make it as
+// much a matter of instructions as of bytes: pairs, maxima that lanes share out and
+// scales formed once.
+#include <initializer_list>
+
+#include "norms.cuh"
+
+namespace zo {
+
+struct JoinParams {
+    const void *o, *x, *w_post, *w_pre;
+    Gate gate;
+    void *h, *y;
+    Form y8, o8, h8;
+    float *rstd_post, *rstd_pre;
+    int64_t ldo, ldx, ldh, ldy;
+    int64_t rows;
+    int32_t cols;
+    float scale, eps, inv_cols;
+    int32_t w_type, e5m2;
+};
+
+__device__ __forceinline__ float root(float sumsq, float inv_cols, float eps)
+{
+    return __fdiv_rn(1.0f, __fsqrt_rn(sumsq * inv_cols + eps));
+}
+
+// The gate's number where a row has one.
+__device__ __forceinline__ float row_gate(const Gate &g, int64_t row)
+{
+    return g.kind == ZERO_GATE_ONE ? load_one(g.p, g.type, 0) : g.kind == ZERO_GATE_ROWS ? load_one(g.p, g.type, row) : 1.0f;
+}
+
+template <class H>
+__device__ __forceinline__ float square_sum(const Raw8<H> &r, float2 s)
+{
+    float2 x[4];
+    pairs_of(r, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        s = fma2(x[i], x[i], s);
+    return s.x + s.y;
+}
+
+// h of 8 columns (`by`: the row's gate times ro).
+template <int W, class H>
+__device__ __forceinline__ void join8(const JoinParams &p, int c, int n, const Raw8<H> &o, const Raw8<H> &x, float by, float2 h[4])
+{
+    float2 f[4], xo[4], xs[4];
+    post_factors<W>(p.w_post, p.w_type, p.gate, c, n, f);
+    pairs_of(o, xo);
+    pairs_of(x, xs);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        h[i] = fma2(both(p.scale), xs[i], mul2(f[i], mul2(xo[i], both(by))));
+}
+
+// V units of a row, `step` columns apart, into two forms of fp32 values (either may be absent).
+template <int W, int V>
+__device__ __forceinline__ void put_two(const Form &f, const Form &g, int64_t row, int c, int step, int cols,
+                                        const float2 (&x)[V][4], const float2 (&y)[V][4], bool e5m2)
+{
+    uint32_t a[2 * V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        a[v] = amax8(x[v]);
+        a[V + v] = amax8(y[v]);
+    }
+    const uint32_t most = max_shared(a);
+    const int mine = shared_index<2 * V>(), unit = mine % V;
+    const bool second = mine >= V;
+    const float s = scale_of(most, second && e5m2), inv = quick_inverse(s);
+    const Form &w = second ? g : f;
+    const int at = c + unit * step;  // a column of this lane's block; its first decides
+    if (threadIdx.x % (16 / (2 * V)) == 0 && w.q && (at & ~(kBlock - 1)) < cols)
+        w.s[(at / kBlock) * w.lds + row] = s;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int at_v = c + v * step, n = left_of(cols, at_v);
+        const float i0 = shared_value<2 * V>(inv, v), i1 = shared_value<2 * V>(inv, V + v);
+        if (f.q && n > 0)
+            put_bytes<W>(f.q + row * f.ld + at_v, n, bytes_of(x[v], i0, false));
+        if (g.q && n > 0)
+            put_bytes<W>(g.q + row * g.ld + at_v, n, bytes_of(y[v], i1, e5m2));
+    }
+}
+
+// V units of halves into the form that zero_fp8_quantize gives them.
+template <int W, int V, class H>
+__device__ __forceinline__ void put_halves(const Form &f, int64_t row, int c, int step, int cols, const Raw8<H> (&r)[V])
+{
+    uint32_t a[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        a[v] = amax8(r[v]);
+    const uint32_t most = max_shared(a);
+    const float s = scale_of(most, false), quick = quick_inverse(s);
+    const Inverse inv = inverse_of(quick, s);
+    const int at = c + shared_index<V>() * step;
+    if (threadIdx.x % (16 / V) == 0 && (at & ~(kBlock - 1)) < cols)
+        f.s[(at / kBlock) * f.lds + row] = s;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int at_v = c + v * step, n = left_of(cols, at_v);
+        const Inverse d = {shared_value<V>(inv.hi, v), shared_value<V>(inv.lo, v)};
+        float2 x[4];
+        pairs_of(r[v], x);
+        if (n > 0)
+            put_bytes<W>(f.q + row * f.ld + at_v, n, bytes_of(x, d, false));
+    }
+}
+
+// What V units of a row leave once rh is known.
+template <int W, int V, class H>
+__device__ __forceinline__ void put_units(const JoinParams &p, int64_t row, int c, int step, int cols,
+                                          const float2 (&h)[V][4], float rh)
+{
+    float2 y[V][4];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int at = c + v * step, n = left_of(cols, at);
+        if (n > 0)
+            put_pairs<W>(static_cast<H *>(p.h) + row * p.ldh + at, n, h[v]);
+        get_vector<W>(p.w_pre, p.w_type, at, n, y[v]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            y[v][i] = mul2(mul2(h[v][i], both(rh)), y[v][i]);
+        if (W != kWhole && n < 8)  // behind the row's end 0 * rh may be a NaN
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                y[v][i] = make_float2(2 * i < n ? y[v][i].x : 0.0f, 2 * i + 1 < n ? y[v][i].y : 0.0f);
+        if (p.y && n > 0)
+            put_pairs<W>(static_cast<H *>(p.y) + row * p.ldy + at, n, y[v]);
+    }
+    if (p.h8.q || p.y8.q)
+        put_two<W>(p.h8, p.y8, row, c, step, cols, h, y, p.e5m2);
+}
+
+// A row to G lanes (16 or 32), or to the CTA (G = 0), V units of 8 to a thread.
+template <class H, int V, int G, int MAXT, int W>
+__global__ void __launch_bounds__(MAXT) join_kernel(const JoinParams p)
+{
+    constexpr int kWarps = MAXT / 32, kLanes = G ? G : 32;
+    __shared__ float slots[2][kWarps];
+    const int t = G ? threadIdx.x % kLanes : threadIdx.x;
+    const int step = (G ? G : blockDim.x) * 8, c = t * 8;
+    const int64_t at = G ? (int64_t)blockIdx.x * (MAXT / kLanes) + threadIdx.x / kLanes : blockIdx.x;
+    const bool live = at < p.rows;
+    const int64_t row = live ? at : 0;
+    const int cols = live ? p.cols : 0;
+    const H *po = static_cast<const H *>(p.o) + row * p.ldo, *px = static_cast<const H *>(p.x) + row * p.ldx;
+    Raw8<H> o[V], x[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int n = left_of(cols, c + v * step);
+        o[v] = get_raw<W>(po + c + v * step, n);
+        x[v] = get_raw<W>(px + c + v * step, n);
+    }
+    float ro = 1.0f;
+    if (p.w_post) {
+        float sq[1] = {0.0f};
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            sq[0] = square_sum(o[v], make_float2(sq[0], 0.0f));
+        row_sums<G, kWarps>(sq, slots[0]);
+        ro = root(sq[0], p.inv_cols, p.eps);
+        if (live && t == 0 && p.rstd_post)
+            p.rstd_post[row] = ro;
+    }
+    const float by = row_gate(p.gate, row) * ro;
+    float2 h[V][4], s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int n = left_of(cols, c + v * step);
+        join8<W>(p, c + v * step, n, o[v], x[v], by, h[v]);
+        if (W != kWhole && n < 8)  // behind the row's end 0 * ro may be a NaN
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                h[v][i] = make_float2(2 * i < n ? h[v][i].x : 0.0f, 2 * i + 1 < n ? h[v][i].y : 0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            s2 = fma2(h[v][i], h[v][i], s2);
+    }
+    if (p.o8.q)
+        put_halves<W>(p.o8, row, c, step, cols, o);
+    float sq[1] = {s2.x + s2.y};
+    row_sums<G, kWarps>(sq, slots[1]);
+    const float rh = root(sq[0], p.inv_cols, p.eps);
+    if (live && t == 0 && p.rstd_pre)
+        p.rstd_pre[row] = rh;
+    put_units<W, V, H>(p, row, c, step, cols, h, rh);
+}
+
+// Rows too long for the registers: o for its norm, o and x for h's, and both again
+// for what is written (h may be x or o, so nothing is written before that).
+template <class H, int W>
+__global__ void __launch_bounds__(1024) join_long_kernel(const JoinParams p)
+{
+    __shared__ float slots[2][32];
+    const int64_t row = blockIdx.x;
+    const H *po = static_cast<const H *>(p.o) + row * p.ldo;
+    const H *px = static_cast<const H *>(p.x) + row * p.ldx;
+    float ro = 1.0f;
+    if (p.w_post) {
+        float sq[1] = {0.0f};
+        for (int64_t c = threadIdx.x * 8; c < p.cols; c += 1024 * 8)
+            sq[0] = square_sum(get_raw<W>(po + c, left_of(p.cols, (int)c)), make_float2(sq[0], 0.0f));
+        row_sums<0, 32>(sq, slots[0]);
+        ro = root(sq[0], p.inv_cols, p.eps);
+        if (threadIdx.x == 0 && p.rstd_post)
+            p.rstd_post[row] = ro;
+    }
+    const float by = row_gate(p.gate, row) * ro;
+    Raw8<H> o[1];
+    float2 h[1][4], s2 = make_float2(0.0f, 0.0f);
+    auto join = [&](int c) {
+        const int n = left_of(p.cols, c);
+        o[0] = get_raw<W>(po + c, n);
+        join8<W>(p, c, n, o[0], get_raw<W>(px + c, n), by, h[0]);
+        if (W != kWhole && n < 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                h[0][i] = make_float2(2 * i < n ? h[0][i].x : 0.0f, 2 * i + 1 < n ? h[0][i].y : 0.0f);
+    };
+    for (int64_t c = threadIdx.x * 8; c < p.cols; c += 1024 * 8) {
+        join((int)c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            s2 = fma2(h[0][i], h[0][i], s2);
+    }
+    float sq[1] = {s2.x + s2.y};
+    row_sums<0, 32>(sq, slots[1]);
+    const float rh = root(sq[0], p.inv_cols, p.eps);
+    if (threadIdx.x == 0 && p.rstd_pre)
+        p.rstd_pre[row] = rh;
+    const int64_t end = ((int64_t)p.cols + 1024 * 8 - 1) / (1024 * 8) * (1024 * 8);
+    for (int64_t c = threadIdx.x * 8; c < end; c += 1024 * 8) {
+        join((int)c);
+        if (p.o8.q)
+            put_halves<W>(p.o8, row, (int)c, 0, p.cols, o);
+        put_units<W, 1, H>(p, row, (int)c, 0, p.cols, h, rh);
+    }
+}
+
+template <class H, int W>
+static int launch_join(const JoinParams &p, cudaStream_t stream)
+{
+    auto go = [&](auto kernel, int threads, int rows_per_cta) {
+        kernel<<<(unsigned)ceil_div(p.rows, rows_per_cta), threads, 0, stream>>>(p);
+        return launch_status();
+    };
+    auto threads = [&](int units) { return (int)(ceil_div(ceil_div(p.cols, 8 * units), 32) * 32); };
+    if (p.cols <= 128)
+        return go(join_kernel<H, 1, 16, 256, W>, 256, 16);
+    if (p.cols <= 256)
+        return go(join_kernel<H, 1, 32, 256, W>, 256, 8);
+    if (p.cols <= 512)
+        return go(join_kernel<H, 2, 32, 256, W>, 256, 8);
+    if (p.cols <= 8192)
+        return go(join_kernel<H, 2, 0, 512, W>, threads(2), 1);
+    if (p.cols <= 16384)
+        return go(join_kernel<H, 2, 0, 1024, W>, threads(2), 1);
+    return go(join_long_kernel<H, W>, 1024, 1);
+}
+
+}  // namespace zo
+
+using namespace zo;
+
+extern "C" {
+
+int zero_gated_norms_fp8(const void *o, int64_t ldo, const void *x, int64_t ldx, const void *w_post,
+                         const void *w_pre, int w_type, const void *gate, int gate_kind, int gate_type,
+                         float scale, int type, int64_t rows, int64_t cols, float eps, void *h, int64_t ldh,
+                         void *y, int64_t ldy, int fp8, const zero_fp8_form *y8, const zero_fp8_form *o8,
+                         const zero_fp8_form *h8, float *rstd_post, float *rstd_pre, zero_stream_t stream)
+{
+    if (!is_half(type) || !is_float(w_type) || bad_dim(rows) || bad_dim(cols) || cols < 1 || !(eps >= 0.0f) ||
+        !std::isfinite(eps) || !std::isfinite(scale) || bad_gate(gate, gate_kind, gate_type, rows) || (y8 && !is_fp8(fp8)))
+        return ZERO_EINVAL;
+    if (rows == 0)
+        return ZERO_OK;
+    if (!w_pre)
+        return ZERO_EINVAL;
+    const int b = type_bytes(type);
+    int rc = check_matrix(o, rows, cols, ldo, b);
+    if (!rc)
+        rc = check_matrix(x, rows, cols, ldx, b);
+    if (!rc)
+        rc = check_matrix(h, rows, cols, ldh, b);
+    if (!rc && y)
+        rc = check_matrix(y, rows, cols, ldy, b);
+    for (const zero_fp8_form *f : {y8, o8, h8})
+        if (!rc)
+            rc = check_form(f, rows, cols);
+    const uintptr_t wb = (uintptr_t)type_bytes(w_type);
+    if (!rc && (!aligned(w_pre, wb) || !aligned(w_post, wb) || !gate_aligned(gate, gate_kind, gate_type) ||
+                !aligned(rstd_post, 4) || !aligned(rstd_pre, 4)))
+        rc = ZERO_EALIGN;
+    if (rc)
+        return rc;
+    JoinParams p{};
+    p.o = o;
+    p.x = x;
+    p.w_post = w_post;
+    p.w_pre = w_pre;
+    p.gate = {gate, gate_kind, gate_type};
+    p.h = h;
+    p.y = y;
+    p.y8 = form_of(y8);
+    p.o8 = form_of(o8);
+    p.h8 = form_of(h8);
+    p.rstd_post = rstd_post;
+    p.rstd_pre = rstd_pre;
+    p.ldo = ldo;
+    p.ldx = ldx;
+    p.ldh = ldh;
+    p.ldy = ldy;
+    p.rows = rows;
+    p.cols = (int32_t)cols;
+    p.scale = scale;
+    p.eps = eps;
+    p.inv_cols = 1.0f / (float)cols;
+    p.w_type = w_type;
+    p.e5m2 = y8 && fp8 == ZERO_T_E5M2;
+    bool wide = rows_aligned(o, ldo, b, 16) && rows_aligned(x, ldx, b, 16) && rows_aligned(h, ldh, b, 16) &&
+                (!y || rows_aligned(y, ldy, b, 16)) && aligned(w_pre, 16) && aligned(w_post, 16) &&
+                (gate_kind != ZERO_GATE_COLS || aligned(gate, 16));
+    for (const Form *f : {&p.y8, &p.o8, &p.h8})
+        wide = wide && (!f->q || f->wide);
+    auto go = [&](auto half) {
+        using H = decltype(half);
+        return !wide ? launch_join<H, kApart>(p, stream)
+                     : cols % 8 ? launch_join<H, kWide>(p, stream) : launch_join<H, kWhole>(p, stream);
+    };
+    return type == ZERO_T_F16 ? go(f16{}) : go(bf16{});
+}
+
+}  // extern "C"

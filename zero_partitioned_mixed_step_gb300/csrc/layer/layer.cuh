@@ -44,37 +44,303 @@ inline int check_kept(const void *x, int64_t ld, const float *s, int64_t lds, in
     return rc || !s ? rc : check_matrix(s, ceil_div(cols, kBlock), rows, lds, 4);
 }
 
-// As a float, by a number that the whole launch shares.
+// A matrix in tiles of 128 columns: CTAs take one row of tiles after the other, so that those
+// which run together read whole rows of memory (8192x14336, an activation read back as halves:
+// 55.5 us, down the columns 59.6).
+struct Tiles {
+    int32_t rows, cols;  // tiles down and across
+};
+struct TileAt {
+    int32_t r, c;
+};
+__device__ __forceinline__ TileAt tile_at(const Tiles &t)
+{
+    return {(int32_t)(blockIdx.x / (uint32_t)t.cols), (int32_t)(blockIdx.x % (uint32_t)t.cols)};
+}
+inline Tiles tiles_of(int64_t rows, int64_t cols, int height)
+{
+    return {(int32_t)ceil_div(rows, height), (int32_t)ceil_div(cols, kBlock)};
+}
+
+// ------------------------------------------------------------------ eight elements
+
+// Eight neighbouring elements of a row are four pairs: Blackwell's fp32 pipes take a
+// pair at a time, and these kernels are bound by instructions before they are by memory.
+// How rows lie: not where wide accesses want them (16 bytes, 8-bit rows 8); there, with a
+// last unit of n < 8, which goes in at most three accesses of 4, 2 and 1 elements (a
+// vector's fp32 ones one by one); or there, and 8 divides their length.
+enum { kApart = 0, kWide = 1, kWhole = 2 };
+
+__device__ __forceinline__ int left_of(int cols, int c) { return min(8, max(0, cols - c)); }
+
+template <int W, class T>
+__device__ __forceinline__ Raw8<T> get_raw(const T *p, int n)
+{
+    if constexpr (W == kApart) {
+        return load_raw(p, n, false);
+    } else if constexpr (W == kWhole) {
+        Raw8<T> r{};
+        if (n > 0)
+            r = load_raw(p, 8, true);
+        return r;
+    } else if constexpr (sizeof(T) == 4) {
+        if (n >= 8)
+            return load_raw(p, 8, true);
+        Raw8<T> r{};
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (i < n)
+                r.w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+        return r;
+    } else {
+        if (n >= 8)
+            return load_raw(p, 8, true);
+        Raw8<T> r{};
+        const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+        uint2 four = make_uint2(0, 0);
+        uint32_t two = 0, one = 0;
+        if (n & 4)
+            four = *reinterpret_cast<const uint2 *>(q);
+        if (n & 2)
+            two = *reinterpret_cast<const uint32_t *>(q + (n & 4));
+        if (n & 1)
+            one = q[n & 6];
+        r.w[0] = n & 4 ? four.x : n & 2 ? two : one;
+        r.w[1] = n & 4 ? four.y : n & 2 ? one : 0u;
+        r.w[2] = n & 4 ? n & 2 ? two : one : 0u;
+        r.w[3] = (n & 6) == 6 ? one : 0u;
+        return r;
+    }
+}
+
+template <int W, class T>
+__device__ __forceinline__ void put_raw(T *p, int n, const Raw8<T> &r)
+{
+    if (W == kWhole) {
+        store_raw(p, 8, true, r);
+    } else if (W == kApart || n >= 8) {
+        store_raw(p, n, W, r);
+    } else {
+        uint16_t *q = reinterpret_cast<uint16_t *>(p);
+        if (n & 4)
+            *reinterpret_cast<uint2 *>(q) = make_uint2(r.w[0], r.w[1]);
+        if (n & 2)
+            *reinterpret_cast<uint32_t *>(q + (n & 4)) = n & 4 ? r.w[2] : r.w[0];
+        if (n & 1)
+            q[n & 6] = (uint16_t)((n & 4) ? (n & 2) ? r.w[3] : r.w[2] : (n & 2) ? r.w[1] : r.w[0]);
+    }
+}
+
+template <class H>
+__device__ __forceinline__ float2 pair_of(uint32_t w)
+{
+    if constexpr (Type<H>::code == ZERO_T_BF16)
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    else {
+        __half2 h;
+        memcpy(&h, &w, 4);
+        return __half22float2(h);
+    }
+}
+
+template <class H>
+__device__ __forceinline__ void pairs_of(const Raw8<H> &r, float2 x[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x[i] = pair_of<H>(r.w[i]);
+}
+
+// Rounded to H; n > 0.
+template <int W, class H>
+__device__ __forceinline__ void put_pairs(H *p, int n, const float2 x[4])
+{
+    if constexpr (sizeof(H) == 4) {
+        const float y[8] = {x[0].x, x[0].y, x[1].x, x[1].y, x[2].x, x[2].y, x[3].x, x[3].y};
+        store8(p, W == kWhole ? 8 : n, W, y);
+    } else {
+        Raw8<H> r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r.w[i] = word_of<H>(x[i].x, x[i].y);
+        put_raw<W>(p, n, r);
+    }
+}
+
+// Of a vector of any of the types.
+template <int W>
+__device__ __forceinline__ void get_vector(const void *w, int type, int at, int n, float2 x[4])
+{
+    if (type == ZERO_T_F16)
+        pairs_of(get_raw<W>(static_cast<const f16 *>(w) + at, n), x);
+    else if (type == ZERO_T_BF16)
+        pairs_of(get_raw<W>(static_cast<const bf16 *>(w) + at, n), x);
+    else {
+        const Raw8<float> r = get_raw<W>(static_cast<const float *>(w) + at, n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+    }
+}
+
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+// ------------------------------------------------------------------ 8-bit blocks
+
+__device__ __forceinline__ float max3(float a, float b, float c)  // of magnitudes; a NaN stays
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t amax8(const float2 x[4])
+{
+    float a = max3(x[0].x, x[0].y, x[1].x);
+    a = max3(a, x[1].y, x[2].x);
+    a = max3(a, x[2].y, x[3].x);
+    return __float_as_uint(max3(a, x[3].y, x[3].y));
+}
+template <class H>
+__device__ __forceinline__ uint32_t amax8(const Raw8<H> &r)
+{
+    Amax<H> a;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        a.add(r.w[i]);
+    return a.bits();
+}
+
+// The sums of P values (4 or 8) over L lanes (16 or 32), shared out in the same way: value i
+// ends with the lanes L / P * i and up.
+template <int P, int L>
+__device__ __forceinline__ float sum_shared(float (&x)[P])
+{
+    int bit = L / 2;
+#pragma unroll
+    for (int half = P / 2; half; half >>= 1, bit >>= 1)
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const bool up = threadIdx.x & bit;
+            const float keep = up ? x[i + half] : x[i], give = up ? x[i] : x[i + half];
+            x[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, bit);
+        }
+#pragma unroll
+    for (; bit; bit >>= 1)
+        x[0] += __shfl_xor_sync(0xFFFFFFFFu, x[0], bit);
+    return x[0];
+}
+
+// The largest of each of N values (1, 2 or 4) over 16 lanes.  The lanes share the
+// values out between them as they exchange: value i ends with the lanes
+// 16 / N * i and up, which then form its scale once.  log2 N + 4 - log2 N steps, but
+// N - 1 + 4 - log2 N shuffles where one value after the other takes 4 N.
+template <int N>
+__device__ __forceinline__ uint32_t max_shared(uint32_t (&a)[N])
+{
+    const int lane = threadIdx.x;
+    int bit = 8;
+#pragma unroll
+    for (int half = N / 2; half; half >>= 1, bit >>= 1)
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const bool up = lane & bit;
+            const uint32_t keep = up ? a[i + half] : a[i], give = up ? a[i] : a[i + half];
+            a[i] = max(keep, __shfl_xor_sync(0xFFFFFFFFu, give, bit));
+        }
+#pragma unroll
+    for (; bit; bit >>= 1)
+        a[0] = max(a[0], __shfl_xor_sync(0xFFFFFFFFu, a[0], bit));
+    return a[0];
+}
+template <int N>
+__device__ __forceinline__ int shared_index()
+{
+    return (threadIdx.x & 15) / (16 / N);
+}
+template <int N>
+__device__ __forceinline__ float shared_value(float mine, int i)
+{
+    return __shfl_sync(0xFFFFFFFFu, mine, 16 / N * i, 16);
+}
+
+// amax / qmax, correctly rounded, without a division: with y = 1 / qmax rounded to nearest,
+// q = a y and the remainder r = a - qmax q, which is exact, q + r y is the rounded
+// quotient (Markstein, IBM J. Res. Dev. 34, 1990).  Infinite and NaN maxima are their
+// own scales, and what is below the smallest scale becomes it.
+__device__ __forceinline__ float scale_from(uint32_t amax, float qmax, float inv_qmax)
+{
+    const float a = __uint_as_float(amax), q = a * inv_qmax;
+    float s = fmaf(fmaf(-qmax, q, a), inv_qmax, q);
+    s = a < __int_as_float(0x7F800000) ? s : a;
+    return s < kTinyScale ? kTinyScale : s;
+}
 __device__ __forceinline__ float scale_of(uint32_t amax, bool e5m2)
 {
-    const float s = __fdiv_rn(__uint_as_float(amax), e5m2 ? F8Type<ZERO_T_E5M2>::qmax : F8Type<ZERO_T_E4M3>::qmax);
-    return s < kTinyScale ? kTinyScale : s;  // NaN stays
+    return e5m2 ? scale_from(amax, 57344.0f, 1.0f / 57344.0f) : scale_from(amax, 448.0f, 1.0f / 448.0f);
 }
 
-__device__ __forceinline__ uint2 quotients_of(const float x[8], Inverse d, bool e5m2)
+// 1 / s to an fp32 unit.  For values that were computed in fp32 one product with it is a
+// quotient to 3 half units, next to the 2^19 of a step of the 8 bits.
+__device__ __forceinline__ float quick_inverse(float s)
 {
-    return e5m2 ? quotients8<ZERO_T_E5M2>(x, d) : quotients8<ZERO_T_E4M3>(x, d);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return r;
+}
+// In two parts, the first below 1 / s by up to 2^-21 of it: x * hi + x * lo rounds as x / s does,
+// which values of few bits need (their quotients are often the middle of two 8-bit
+// values), and as lo is positive -0 stays.
+__device__ __forceinline__ Inverse inverse_of(float quick, float s)
+{
+    Inverse r;
+    r.hi = quick * (1.0f - 0x1p-22f);
+    r.lo = fmaf(-s, r.hi, 1.0f) * r.hi;
+    return r;
 }
 
-__device__ __forceinline__ uint32_t amax8(const float x[8])
+__device__ __forceinline__ uint2 bytes_of(const float2 q[4], bool e5m2)
 {
-    uint32_t a = 0;
+    return e5m2 ? make_uint2(pack4<ZERO_T_E5M2>(q[0].x, q[0].y, q[1].x, q[1].y), pack4<ZERO_T_E5M2>(q[2].x, q[2].y, q[3].x, q[3].y))
+                : make_uint2(pack4<ZERO_T_E4M3>(q[0].x, q[0].y, q[1].x, q[1].y), pack4<ZERO_T_E4M3>(q[2].x, q[2].y, q[3].x, q[3].y));
+}
+__device__ __forceinline__ uint2 bytes_of(const float2 x[4], float inv, bool e5m2)
+{
+    float2 q[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        a = max(a, magnitude(x[i]));
-    return a;
+    for (int i = 0; i < 4; ++i)
+        q[i] = mul2(x[i], both(inv));
+    return bytes_of(q, e5m2);
 }
-
-// Eight neighbouring elements of a row into a form; the 16 lanes of a 1x128
-// block come here together, each with its own amax and zeros where the row has ended.
-__device__ __forceinline__ void put_form(const Form &f, int64_t row, int64_t c, int n, const float x[8],
-                                         uint32_t amax, bool e5m2)
+__device__ __forceinline__ uint2 bytes_of(const float2 x[4], Inverse d, bool e5m2)
 {
-    const float s = scale_of(max_over<16>(amax), e5m2);
-    if (n > 0) {
-        if ((threadIdx.x & 15) == 0)
-            f.s[(c / kBlock) * f.lds + row] = s;
-        store8b(f.q + row * f.ld + c, n, f.wide, quotients_of(x, inverse(s), e5m2));
+    float2 q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        q[i] = fma2(x[i], both(d.hi), mul2(x[i], both(d.lo)));
+    return bytes_of(q, e5m2);
+}
+template <int W>
+__device__ __forceinline__ void put_bytes(uint8_t *p, int n, uint2 v)
+{
+    if (W == kWhole) {
+        store8b(p, 8, true, v);
+    } else if (W == kApart || n >= 8) {
+        store8b(p, n, W, v);
+    } else {
+        if (n & 4)
+            *reinterpret_cast<uint32_t *>(p) = v.x;
+        const uint32_t rest = n & 4 ? v.y : v.x;
+        if (n & 2)
+            *reinterpret_cast<uint16_t *>(p + (n & 4)) = (uint16_t)rest;
+        if (n & 1)
+            p[n & 6] = (uint8_t)(n & 2 ? rest >> 16 : rest);
     }
 }
 
@@ -89,28 +355,34 @@ __device__ __forceinline__ float2 two_of(uint32_t pair)
 // Eight elements as they are kept: 8 bits each, or a half type's.
 struct Raw8b {
     uint32_t w[2];
-
-    template <int F8 = ZERO_T_E4M3>
-    __device__ __forceinline__ void get(float x[8]) const
-    {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 v = two_of<F8>(w[i >> 1] >> (16 * (i & 1)) & 0xFFFFu);
-            x[2 * i] = v.x;
-            x[2 * i + 1] = v.y;
-        }
-    }
 };
-
-__device__ __forceinline__ Raw8b load_raw8b(const uint8_t *p, int n, bool wide)
+template <int F8 = ZERO_T_E4M3>
+__device__ __forceinline__ void pairs_of(const Raw8b &r, float2 x[4])
 {
-    Raw8b r;
-    if (wide && n >= 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x[i] = two_of<F8>(i & 1 ? r.w[i >> 1] >> 16 : r.w[i >> 1] & 0xFFFFu);
+}
+
+template <int W>
+__device__ __forceinline__ Raw8b get_bytes(const uint8_t *p, int n)
+{
+    Raw8b r{};
+    if (W == kWhole ? n > 0 : W == kWide && n >= 8) {
         const uint2 x = *reinterpret_cast<const uint2 *>(p);
         r.w[0] = x.x;
         r.w[1] = x.y;
-    } else {
-        r.w[0] = r.w[1] = 0;
+    } else if (W == kWide) {
+        uint32_t four = 0, rest = 0;
+        if (n & 4)
+            four = *reinterpret_cast<const uint32_t *>(p);
+        if (n & 2)
+            rest = *reinterpret_cast<const uint16_t *>(p + (n & 4));
+        if (n & 1)
+            rest |= (uint32_t)p[n & 6] << (n & 2 ? 16 : 0);
+        r.w[0] = n & 4 ? four : rest;
+        r.w[1] = n & 4 ? rest : 0u;
+    } else if (W == kApart) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i < n)
@@ -119,39 +391,30 @@ __device__ __forceinline__ Raw8b load_raw8b(const uint8_t *p, int n, bool wide)
     return r;
 }
 
-// A kept matrix's unit: S8 = 8-bit (times the scale of its block), else halves.
+// A kept matrix's unit: S8 = 8-bit (its values times the scale of its block), else halves.
 template <class H, bool S8>
 struct Kept;
 template <class H>
 struct Kept<H, true> {
     static constexpr int kBytes = 8;
     Raw8b r;
-    __device__ __forceinline__ void load(const void *p, int64_t at, int n, bool wide)
+    template <int W>
+    __device__ __forceinline__ void load(const void *row, int c, int n)
     {
-        r = load_raw8b(static_cast<const uint8_t *>(p) + at, n, wide);
+        r = get_bytes<W>(static_cast<const uint8_t *>(row) + c, n);
     }
-    __device__ __forceinline__ void get(float x[8], float s) const
-    {
-        r.get(x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            x[i] *= s;
-    }
+    __device__ __forceinline__ void get(float2 x[4]) const { pairs_of(r, x); }
 };
 template <class H>
 struct Kept<H, false> {
     static constexpr int kBytes = 16;
     Raw8<H> r;
-    __device__ __forceinline__ void load(const void *p, int64_t at, int n, bool wide)
+    template <int W>
+    __device__ __forceinline__ void load(const void *row, int c, int n)
     {
-        r = load_raw(static_cast<const H *>(p) + at, n, wide);
+        r = get_raw<W>(static_cast<const H *>(row) + c, n);
     }
-    __device__ __forceinline__ void get(float x[8], float s) const
-    {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            x[i] = r.at(i) * s;
-    }
+    __device__ __forceinline__ void get(float2 x[4]) const { pairs_of(r, x); }
 };
 
 __device__ __forceinline__ float load_one(const void *p, int type, int64_t at)

@@ -15,29 +15,31 @@ struct RestoreParams {
     const void *col;
     void *x;
     Form t8;
-    int64_t ldq, lds, ldx, rows, cols;
-    int64_t row_tiles;
-    int32_t col_type, wide_q, wide_x, wide_col;
+    int64_t ldq, lds, ldx;
+    int32_t rows, cols;
+    Tiles tiles;
+    int32_t col_type;
 };
 
 constexpr int kRestoreThreads = 256;
 
-template <int F8, class X>
+template <int F8, class X, int W>
 __global__ void __launch_bounds__(kRestoreThreads) restore_kernel(const RestoreParams p)
 {
     // row r's 8 bytes of columns 8j .. lie at j ^ (r / 8), so that the 16 lanes of a column,
     // 8 rows each, read different banks
     __shared__ uint2 tile[kBlock][16];
-    __shared__ float factor[kBlock];
-    const int j = threadIdx.x & 15, group = threadIdx.x >> 4;
-    const int64_t tr = blockIdx.x % p.row_tiles, tc = blockIdx.x / p.row_tiles;
-    const int64_t r0 = tr * kBlock, c0 = tc * kBlock, c = c0 + j * 8;
-    const int nc = in_row(p.cols, c);
+    __shared__ __align__(16) float factor[kBlock];
+    const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
+    const TileAt tile_of = tile_at(p.tiles);
+    const int64_t tr = tile_of.r, tc = tile_of.c, r0 = tr * kBlock, c0 = tc * kBlock;
+    const int c = tile_of.c * kBlock + lane * 8, nc = left_of(p.cols, c);
+    const int nr = r0 + group * 8 < p.rows ? left_of(p.rows, (int)(r0 + group * 8)) : 0;
     Raw8b q[8];
     const uint8_t *from = p.q + (r0 + group * 8) * p.ldq + c;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        q[i] = load_raw8b(from + i * p.ldq, r0 + group * 8 + i < p.rows ? nc : 0, p.wide_q);
+        q[i] = get_bytes<W>(from + i * p.ldq, i < nr ? nc : 0);
     if (threadIdx.x < kBlock) {
         const int64_t row = r0 + threadIdx.x;
         float f = 0.0f;
@@ -51,81 +53,83 @@ __global__ void __launch_bounds__(kRestoreThreads) restore_kernel(const RestoreP
     if (p.t8.q)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            tile[group * 8 + i][j ^ group] = make_uint2(q[i].w[0], q[i].w[1]);
+            tile[group * 8 + i][lane ^ group] = make_uint2(q[i].w[0], q[i].w[1]);
     __syncthreads();
     if (p.x && nc > 0) {
-        float col[8];
+        float2 col[4];
         if (p.col)
-            load_w(p.col, p.col_type, c, nc, p.wide_col, col);
+            get_vector<W>(p.col, p.col_type, c, nc, col);
+        X *to = static_cast<X *>(p.x) + (r0 + group * 8) * p.ldx + c;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t row = r0 + group * 8 + i;
-            if (row >= p.rows)
-                break;
-            const float f = factor[group * 8 + i];
-            float x[8];
-            q[i].get<F8>(x);
+        for (int i = 0; i < 8; ++i)
+            if (i < nr) {
+                const float f = factor[group * 8 + i];
+                float2 x[4];
+                pairs_of<F8>(q[i], x);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                x[k] = p.col ? x[k] * f * col[k] : x[k] * f;
-            store8(static_cast<X *>(p.x) + row * p.ldx + c, nc, p.wide_x, x);
-        }
+                for (int k = 0; k < 4; ++k) {
+                    x[k] = mul2(x[k], both(f));
+                    if (p.col)
+                        x[k] = mul2(x[k], col[k]);
+                }
+                put_pairs<W>(to + i * p.ldx, nc, x);
+            }
     }
     if (!p.t8.q)
         return;
-    const int lane = j;
-    float f[8];
+    float2 f[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        f[i] = factor[lane * 8 + i];
+    for (int i = 0; i < 4; ++i)
+        f[i] = *reinterpret_cast<const float2 *>(&factor[lane * 8 + 2 * i]);
     const int64_t row = r0 + lane * 8;
-    const int n = in_row(p.rows, row);
+    const int n = row < p.rows ? left_of(p.rows, (int)row) : 0;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int k = group + 16 * half;  // columns 4k ..
-        float x[4][8];
-        uint32_t a[4] = {};
         const int64_t at = c0 + 4 * k;
-        float col[4];
+        float2 x[4][4];  // of a column, rows 2i and 2i + 1
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
-            col[m] = p.col && at + m < p.cols ? load_one(p.col, p.col_type, at + m) : 1.0f;
+        for (int i = 0; i < 4; ++i) {
+            const uint2 u = tile[lane * 8 + 2 * i][k >> 1 ^ lane], v = tile[lane * 8 + 2 * i + 1][k >> 1 ^ lane];
+            const uint32_t a = k & 1 ? u.y : u.x, b = k & 1 ? v.y : v.x;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint2 two = tile[lane * 8 + i][k >> 1 ^ lane];
-            const uint32_t w = k & 1 ? two.y : two.x;
-            const float2 lo = two_of<F8>(w & 0xFFFFu), hi = two_of<F8>(w >> 16);
-            x[0][i] = lo.x * f[i];
-            x[1][i] = lo.y * f[i];
-            x[2][i] = hi.x * f[i];
-            x[3][i] = hi.y * f[i];
+            for (int m = 0; m < 4; ++m)
+                x[m][i] = mul2(two_of<F8>(__byte_perm(a, b, m | (m + 4) << 4) & 0xFFFFu), f[i]);
+        }
+        if (p.col)
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                if (p.col)
-                    x[m][i] *= col[m];
-                a[m] = max(a[m], magnitude(x[m][i]));
+                const float col = at + m < p.cols ? load_one(p.col, p.col_type, at + m) : 1.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[m][i] = mul2(x[m][i], both(col));
             }
-        }
+        uint32_t a[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            a[m] = amax8(x[m]);
+        const float s = scale_of(max_shared(a), F8 == ZERO_T_E5M2);
+        const Inverse inv = inverse_of(quick_inverse(s), s);
+        const int mine = shared_index<4>();
+        if (lane % 4 == 0 && at + mine < p.cols)
+            p.t8.s[tr * p.t8.lds + at + mine] = s;
+        uint8_t *to = p.t8.q + at * p.t8.ld + row;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            const float s = block_scale<F8>(max_over<16>(a[m]));
-            if (at + m >= p.cols)
-                continue;
-            if (lane == 0)
-                p.t8.s[tr * p.t8.lds + at + m] = s;
-            if (n > 0)
-                store8b(p.t8.q + (at + m) * p.t8.ld + row, n, p.t8.wide, quotients8<F8>(x[m], inverse(s)));
+            const Inverse d = {shared_value<4>(inv.hi, m), shared_value<4>(inv.lo, m)};
+            if (n > 0 && at + m < p.cols)
+                put_bytes<W>(to + m * p.t8.ld, n, bytes_of(x[m], d, F8 == ZERO_T_E5M2));
         }
     }
 }
 
-template <class X>
+template <class X, int W>
 static int launch_restore(const RestoreParams &p, int fp8, int64_t grid, cudaStream_t stream)
 {
     if (fp8 == ZERO_T_E5M2)
-        restore_kernel<ZERO_T_E5M2, X><<<(unsigned)grid, kRestoreThreads, 0, stream>>>(p);
+        restore_kernel<ZERO_T_E5M2, X, W><<<(unsigned)grid, kRestoreThreads, 0, stream>>>(p);
     else
-        restore_kernel<ZERO_T_E4M3, X><<<(unsigned)grid, kRestoreThreads, 0, stream>>>(p);
+        restore_kernel<ZERO_T_E4M3, X, W><<<(unsigned)grid, kRestoreThreads, 0, stream>>>(p);
     return launch_status();
 }
 
@@ -164,19 +168,24 @@ extern "C" int zero_fp8_restore(const void *q, int fp8, int64_t ldq, const float
     p.ldq = ldq;
     p.lds = lds;
     p.ldx = ldx;
-    p.rows = rows;
-    p.cols = cols;
-    p.row_tiles = ceil_div(rows, kBlock);
+    p.rows = (int32_t)rows;
+    p.cols = (int32_t)cols;
+    p.tiles = tiles_of(rows, cols, kBlock);
     p.col_type = col_type;
-    p.wide_q = rows_aligned(q, ldq, 1, 8);
-    p.wide_x = x && rows_aligned(x, ldx, type_bytes(x_type), 16);
-    p.wide_col = aligned(col, 16);
-    const int64_t grid = p.row_tiles * ceil_div(cols, kBlock);
+    const bool wide = rows_aligned(q, ldq, 1, 8) && (!x || rows_aligned(x, ldx, type_bytes(x_type), 16)) &&
+                      aligned(col, 16) && (!t8 || p.t8.wide);
+    const int64_t grid = (int64_t)p.tiles.rows * p.tiles.cols;
     if (grid > kMaxDim)
         return ZERO_EINVAL;
+    auto go = [&](auto out) {
+        using X = decltype(out);
+        return !wide ? launch_restore<X, kApart>(p, fp8, grid, stream)
+                     : cols % 8 || rows % 8 ? launch_restore<X, kWide>(p, fp8, grid, stream)
+                                            : launch_restore<X, kWhole>(p, fp8, grid, stream);
+    };
     if (x && x_type == ZERO_T_F16)
-        return launch_restore<f16>(p, fp8, grid, stream);
+        return go(f16{});
     if (x && x_type == ZERO_T_F32)
-        return launch_restore<float>(p, fp8, grid, stream);
-    return launch_restore<bf16>(p, fp8, grid, stream);
+        return go(0.0f);
+    return go(bf16{});
 }
