@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(256) act_kernel(const ActParams p)
     };
     auto put_kept = [&](const Form &f, const Raw8<H> (&r)[2]) {
         uint32_t most[2] = {amax8(r[0]), amax8(r[1])};
-        const float s = scale_of(max_shared(most), false);
+        const float s = scale_of<false>(max_shared(most));
         const Inverse inv = inverse_of(quick_inverse(s), s);
         put_scale(f, s);
 #pragma unroll
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(256) act_kernel(const ActParams p)
             float2 x[4];
             pairs_of(r[k], x);
             if (n[k] > 0)
-                put_bytes<W>(f.q + (row + k) * f.ld + c, n[k], bytes_of(x, d, false));
+                put_bytes<W>(f.q + (row + k) * f.ld + c, n[k], bytes_of<false>(x, d));
         }
     };
     float2 a[2][4];
@@ -111,17 +111,22 @@ __global__ void __launch_bounds__(256) act_kernel(const ActParams p)
         for (int k = 0; k < 2; ++k)
             if (n[k] > 0)
                 put_pairs<W>(static_cast<H *>(p.a) + (row + k) * p.lda + c, n[k], a[k]);
-    if (p.a8.q) {
+    auto put_a8 = [&](auto e5m2) {
+        constexpr bool E = decltype(e5m2)::value;
         uint32_t most[2] = {amax8(a[0]), amax8(a[1])};
-        const float s = scale_of(max_shared(most), p.e5m2), inv = quick_inverse(s);
+        const float s = scale_of<E>(max_shared(most)), inv = quick_inverse(s);
         put_scale(p.a8, s);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const float d = shared_value<2>(inv, k);
             if (n[k] > 0)
-                put_bytes<W>(p.a8.q + (row + k) * p.a8.ld + c, n[k], bytes_of(a[k], d, p.e5m2));
+                put_bytes<W>(p.a8.q + (row + k) * p.a8.ld + c, n[k], bytes_of<E>(a[k], d));
         }
-    }
+    };
+    if (p.a8.q && p.e5m2)
+        put_a8(std::true_type{});
+    else if (p.a8.q)
+        put_a8(std::false_type{});
 }
 
 // ------------------------------------------------------------------ backward
@@ -140,53 +145,50 @@ struct ActBackParams {
 constexpr int kBackThreads = 256;  // 16 groups of 16 lanes, 8 rows to a group
 
 // bf16 values of the 128x128 tile on their way to the transposed forms: a row's 128
-// values are 16 units of 8; unit j of a row of group g (rows 8g ..) lies at j ^ (g / 2), its
-// halves exchanged where g is odd.  So 4 neighbouring columns 4k .. of that row are the
-// 8 bytes at place k ^ g: the 16 lanes of a column (8 rows each) read different banks,
-// and so do the 16 lanes of a row as they write.
+// values are 16 units of 8; unit j of a row of group g (rows 8g ..) lies at j ^ (g % 8), so that
+// 8 lanes that read one unit of 8 groups, and 8 that write a row's, meet different banks.
 struct Staged {
-    uint2 row[kBlock][32];
+    uint4 row[kBlock][16];
 };
 __device__ __forceinline__ void stage8(Staged &t, int group, int i, int j, const float2 x[4])
 {
-    const uint2 lo = make_uint2(word_of<bf16>(x[0].x, x[0].y), word_of<bf16>(x[1].x, x[1].y));
-    const uint2 hi = make_uint2(word_of<bf16>(x[2].x, x[2].y), word_of<bf16>(x[3].x, x[3].y));
-    const uint2 a = group & 1 ? hi : lo, b = group & 1 ? lo : hi;
-    *reinterpret_cast<uint4 *>(&t.row[group * 8 + i][2 * (j ^ group >> 1)]) = make_uint4(a.x, a.y, b.x, b.y);
+    t.row[group * 8 + i][j ^ (group & 7)] = make_uint4(word_of<bf16>(x[0].x, x[0].y), word_of<bf16>(x[1].x, x[1].y),
+                                                       word_of<bf16>(x[2].x, x[2].y), word_of<bf16>(x[3].x, x[3].y));
 }
 
-// Four columns (from 4k on) of a tile, 8 rows to each of 16 lanes, into a transposed
+// Eight columns (from 8k on) of a tile, 8 rows to each of 16 lanes, into a transposed
 // form.  amax: of the tile's columns, of the fp32 values.
-template <int W>
+template <int W, bool E5M2>
 __device__ __forceinline__ void put_columns(const Form &f, const Staged &t, const uint32_t *amax, int k, int64_t c0,
-                                            int cols, int64_t r0, int rows, bool e5m2)
+                                            int cols, int64_t r0, int rows)
 {
     const int lane = threadIdx.x & 15;
-    uint2 w[8];
+    uint4 w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        w[i] = t.row[lane * 8 + i][k ^ lane];
-    const float s = scale_of(amax[4 * k + (lane & 3)], e5m2);  // each lane forms one of the four scales
+        w[i] = t.row[lane * 8 + i][k ^ (lane & 7)];
+    const float s = scale_of<E5M2>(amax[8 * k + (lane & 7)]);  // each lane forms one of the eight scales
     const float inv = quick_inverse(s);
-    const int64_t c = c0 + 4 * k;
-    if (lane < 4 && c + lane < cols)
+    const int64_t c = c0 + 8 * k;
+    if (lane < 8 && c + lane < cols)
         f.s[r0 / kBlock * f.lds + c + lane] = s;
     const int64_t row = r0 + lane * 8;
     const int n = row < rows ? left_of(rows, (int)row) : 0;
     uint8_t *to = f.q + c * f.ld + row;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
         const float d = __shfl_sync(0xFFFFFFFFu, inv, j, 16);
         float2 x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t p = j < 2 ? w[2 * i].x : w[2 * i].y, q = j < 2 ? w[2 * i + 1].x : w[2 * i + 1].y;
+            const uint4 &a = w[2 * i], &b = w[2 * i + 1];
+            const uint32_t p = j < 2 ? a.x : j < 4 ? a.y : j < 6 ? a.z : a.w, q = j < 2 ? b.x : j < 4 ? b.y : j < 6 ? b.z : b.w;
             x[i] = j & 1 ? make_float2(__uint_as_float(p & 0xFFFF0000u), __uint_as_float(q & 0xFFFF0000u))
                          : make_float2(__uint_as_float(p << 16), __uint_as_float(q << 16));
         }
-        const uint2 q = bytes_of(x, d, e5m2);
         if (n > 0 && c + j < cols)
-            put_bytes<W>(to + j * f.ld, n, q);
+            put_bytes<W>(to, n, bytes_of<E5M2>(x, d));
+        to += f.ld;
     }
 }
 
@@ -214,23 +216,40 @@ __global__ void __launch_bounds__(kBackThreads, 2) act_backward_kernel(const Act
     Raw8<H> da[2];
     K u[2], v[2];
     float su[2], sv[2];
-    auto fetch = [&](int64_t row) {
+    // pointers move on by two rows at a time
+    const H *f_da = static_cast<const H *>(p.da) + first * p.ldda;
+    const unsigned char *f_u = static_cast<const unsigned char *>(p.u) + first * p.ldu * kElem;
+    const unsigned char *f_v = static_cast<const unsigned char *>(p.v) + first * p.ldv * kElem;
+    const float *f_su = p.su + tc * p.ldsu + first, *f_sv = p.sv + tc * p.ldsv + first;
+    const int left = (int)min((int64_t)8, max((int64_t)0, p.rows - first));  // of this group's 8 rows
+    auto fetch = [&](int step) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int n = row + i < p.rows ? nc : 0;
-            da[i] = get_raw<W>(static_cast<const H *>(p.da) + (row + i) * p.ldda + c, n);
-            u[i].template load<W>(static_cast<const unsigned char *>(p.u) + (row + i) * p.ldu * kElem, c, n);
+            const int n = step + i < left ? nc : 0;
+            da[i] = get_raw<W>(f_da + c, n);
+            u[i].template load<W>(f_u, c, n);
             su[i] = sv[i] = 1.0f;
             if (S8 && n > 0)
-                su[i] = p.su[tc * p.ldsu + row + i];
+                su[i] = f_su[step + i];
             if (GATED) {
-                v[i].template load<W>(static_cast<const unsigned char *>(p.v) + (row + i) * p.ldv * kElem, c, n);
+                v[i].template load<W>(f_v, c, n);
                 if (S8 && n > 0)
-                    sv[i] = p.sv[tc * p.ldsv + row + i];
+                    sv[i] = f_sv[step + i];
             }
+            f_da += p.ldda;
+            f_u += p.ldu * kElem;
+            f_v += p.ldv * kElem;
         }
     };
-    fetch(first);
+    H *to_du = static_cast<H *>(p.du) + first * p.lddu + c, *to_dv = static_cast<H *>(p.dv) + first * p.lddv + c;
+    uint8_t *to_du8 = p.du8.q + first * p.du8.ld + c, *to_dv8 = p.dv8.q + first * p.dv8.ld + c;
+    // a scale that this lane writes, of row (j / (16 / kMaxima)) % 2 of two
+    const int mine = shared_index<kMaxima>();
+    const bool second = mine >= 2;
+    const bool writes = j % (16 / kMaxima) == 0 && (second ? p.dv8.q : p.du8.q);
+    float *to_s = (second ? p.dv8.s + tc * p.dv8.lds : p.du8.s + tc * p.du8.lds) + first + (mine & 1);
+    fetch(0);
+    const Range range(p.e5m2);
     float most[kForms][8] = {};
 #pragma unroll 1
     for (int step = 0; step < 8; step += 2) {
@@ -249,10 +268,9 @@ __global__ void __launch_bounds__(kBackThreads, 2) act_backward_kernel(const Act
                     vf[i][k] = mul2(vf[i][k], both(sv[i]));
             }
         }
-        const int64_t row = first + step;
-        const int n[2] = {row < p.rows ? nc : 0, row + 1 < p.rows ? nc : 0};
+        const int n[2] = {step < left ? nc : 0, step + 1 < left ? nc : 0};
         if (step < 6)
-            fetch(row + 2);
+            fetch(step + 2);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -293,10 +311,12 @@ __global__ void __launch_bounds__(kBackThreads, 2) act_backward_kernel(const Act
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (p.du && n[i] > 0)
-                put_pairs<W>(static_cast<H *>(p.du) + (row + i) * p.lddu + c, n[i], du[i]);
+                put_pairs<W>(to_du + i * p.lddu, n[i], du[i]);
             if (GATED && p.dv && n[i] > 0)
-                put_pairs<W>(static_cast<H *>(p.dv) + (row + i) * p.lddv + c, n[i], dv[i]);
+                put_pairs<W>(to_dv + i * p.lddv, n[i], dv[i]);
         }
+        to_du += 2 * p.lddu;
+        to_dv += 2 * p.lddv;
         if (p.du8.q || (GATED && p.dv8.q)) {
             uint32_t m[kMaxima];
 #pragma unroll
@@ -305,19 +325,26 @@ __global__ void __launch_bounds__(kBackThreads, 2) act_backward_kernel(const Act
                 if (GATED)
                     m[kMaxima - 2 + i] = amax8(dv[i]);
             }
-            const float s = scale_of(max_shared(m), p.e5m2), inv = quick_inverse(s);
-            const int mine = shared_index<kMaxima>();
-            const Form &f = mine < 2 ? p.du8 : p.dv8;
-            if (j % (16 / kMaxima) == 0 && f.q && row + (mine & 1) < p.rows)
-                f.s[tc * f.lds + row + (mine & 1)] = s;
+            const float s = range.scale(max_shared(m)), inv = quick_inverse(s);
+            if (writes && step + (mine & 1) < left)
+                to_s[step] = s;
+            auto put = [&](auto e5m2) {
+                constexpr bool E = decltype(e5m2)::value;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float d0 = shared_value<kMaxima>(inv, i), d1 = shared_value<kMaxima>(inv, kMaxima - 2 + i);
-                if (p.du8.q && n[i] > 0)
-                    put_bytes<W>(p.du8.q + (row + i) * p.du8.ld + c, n[i], bytes_of(du[i], d0, p.e5m2));
-                if (GATED && p.dv8.q && n[i] > 0)
-                    put_bytes<W>(p.dv8.q + (row + i) * p.dv8.ld + c, n[i], bytes_of(dv[i], d1, p.e5m2));
-            }
+                for (int i = 0; i < 2; ++i) {
+                    const float d0 = shared_value<kMaxima>(inv, i), d1 = shared_value<kMaxima>(inv, kMaxima - 2 + i);
+                    if (p.du8.q && n[i] > 0)
+                        put_bytes<W>(to_du8 + i * p.du8.ld, n[i], bytes_of<E>(du[i], d0));
+                    if (GATED && p.dv8.q && n[i] > 0)
+                        put_bytes<W>(to_dv8 + i * p.dv8.ld, n[i], bytes_of<E>(dv[i], d1));
+                }
+            };
+            if (p.e5m2)
+                put(std::true_type{});
+            else
+                put(std::false_type{});
+            to_du8 += 2 * p.du8.ld;
+            to_dv8 += 2 * p.dv8.ld;
         }
     }
     if (!trans)
@@ -328,15 +355,19 @@ __global__ void __launch_bounds__(kBackThreads, 2) act_backward_kernel(const Act
         for (int k = 0; k < 8; ++k)
             atomicMax(&amax[f][j * 8 + k], __float_as_uint(most[f][k]));  // a maximum: in any order the same
     __syncthreads();
-#pragma unroll 1
-    for (int k = group; k < 32; k += 16) {
+    auto put = [&](auto e5m2) {
+        constexpr bool E = decltype(e5m2)::value;
         if (p.du8t.q)
-            put_columns<W>(p.du8t, tile[0], amax[0], k, c0, p.cols, r0, p.rows, p.e5m2);
-        if (p.a8t.q)
-            put_columns<W>(p.a8t, tile[1], amax[1], k, c0, p.cols, r0, p.rows, false);
+            put_columns<W, E>(p.du8t, tile[0], amax[0], group, c0, p.cols, r0, p.rows);
         if (GATED && p.dv8t.q)
-            put_columns<W>(p.dv8t, tile[kForms - 1], amax[kForms - 1], k, c0, p.cols, r0, p.rows, p.e5m2);
-    }
+            put_columns<W, E>(p.dv8t, tile[kForms - 1], amax[kForms - 1], group, c0, p.cols, r0, p.rows);
+    };
+    if (p.a8t.q)
+        put_columns<W, false>(p.a8t, tile[1], amax[1], group, c0, p.cols, r0, p.rows);
+    if (p.e5m2)
+        put(std::true_type{});
+    else
+        put(std::false_type{});
 }
 
 template <class H, bool S8, bool GATED, bool GELU, int W>

@@ -76,7 +76,7 @@ __device__ __forceinline__ void put_two(const Form &f, const Form &g, int64_t ro
     const uint32_t most = max_shared(a);
     const int mine = shared_index<2 * V>(), unit = mine % V;
     const bool second = mine >= V;
-    const float s = scale_of(most, second && e5m2), inv = quick_inverse(s);
+    const float s = Range(second && e5m2).scale(most), inv = quick_inverse(s);
     const Form &w = second ? g : f;
     const int at = c + unit * step;  // a column of this lane's block; its first decides
     if (threadIdx.x % (16 / (2 * V)) == 0 && w.q && (at & ~(kBlock - 1)) < cols)
@@ -86,9 +86,9 @@ __device__ __forceinline__ void put_two(const Form &f, const Form &g, int64_t ro
         const int at_v = c + v * step, n = left_of(cols, at_v);
         const float i0 = shared_value<2 * V>(inv, v), i1 = shared_value<2 * V>(inv, V + v);
         if (f.q && n > 0)
-            put_bytes<W>(f.q + row * f.ld + at_v, n, bytes_of(x[v], i0, false));
+            put_bytes<W>(f.q + row * f.ld + at_v, n, bytes_of<false>(x[v], i0));
         if (g.q && n > 0)
-            put_bytes<W>(g.q + row * g.ld + at_v, n, bytes_of(y[v], i1, e5m2));
+            put_bytes<W>(g.q + row * g.ld + at_v, n, e5m2 ? bytes_of<true>(y[v], i1) : bytes_of<false>(y[v], i1));
     }
 }
 
@@ -101,7 +101,7 @@ __device__ __forceinline__ void put_halves(const Form &f, int64_t row, int c, in
     for (int v = 0; v < V; ++v)
         a[v] = amax8(r[v]);
     const uint32_t most = max_shared(a);
-    const float s = scale_of(most, false), quick = quick_inverse(s);
+    const float s = scale_of<false>(most), quick = quick_inverse(s);
     const Inverse inv = inverse_of(quick, s);
     const int at = c + shared_index<V>() * step;
     if (threadIdx.x % (16 / V) == 0 && (at & ~(kBlock - 1)) < cols)
@@ -113,7 +113,7 @@ __device__ __forceinline__ void put_halves(const Form &f, int64_t row, int c, in
         float2 x[4];
         pairs_of(r[v], x);
         if (n > 0)
-            put_bytes<W>(f.q + row * f.ld + at_v, n, bytes_of(x, d, false));
+            put_bytes<W>(f.q + row * f.ld + at_v, n, bytes_of<false>(x, d));
     }
 }
 

@@ -281,10 +281,17 @@ __device__ __forceinline__ float scale_from(uint32_t amax, float qmax, float inv
     s = a < __int_as_float(0x7F800000) ? s : a;
     return s < kTinyScale ? kTinyScale : s;
 }
-__device__ __forceinline__ float scale_of(uint32_t amax, bool e5m2)
+template <bool E5M2>
+__device__ __forceinline__ float scale_of(uint32_t amax)
 {
-    return e5m2 ? scale_from(amax, 57344.0f, 1.0f / 57344.0f) : scale_from(amax, 448.0f, 1.0f / 448.0f);
+    return E5M2 ? scale_from(amax, 57344.0f, 1.0f / 57344.0f) : scale_from(amax, 448.0f, 1.0f / 448.0f);
 }
+// The same for a type that the launch knows: two numbers of it, formed once.
+struct Range {
+    float qmax, inv;
+    __device__ __forceinline__ explicit Range(bool e5m2) : qmax(e5m2 ? 57344.0f : 448.0f), inv(e5m2 ? 1.0f / 57344.0f : 1.0f / 448.0f) {}
+    __device__ __forceinline__ float scale(uint32_t amax) const { return scale_from(amax, qmax, inv); }
+};
 
 // 1 / s to an fp32 unit.  For values that were computed in fp32 one product with it is a
 // quotient to 3 half units, next to the 2^19 of a step of the 8 bits.
@@ -305,26 +312,31 @@ __device__ __forceinline__ Inverse inverse_of(float quick, float s)
     return r;
 }
 
-__device__ __forceinline__ uint2 bytes_of(const float2 q[4], bool e5m2)
+// Which type is a template's argument: where it is a number that the launch shares, the
+// compiler forms both and selects.
+template <bool E5M2>
+__device__ __forceinline__ uint2 bytes_of(const float2 q[4])
 {
-    return e5m2 ? make_uint2(pack4<ZERO_T_E5M2>(q[0].x, q[0].y, q[1].x, q[1].y), pack4<ZERO_T_E5M2>(q[2].x, q[2].y, q[3].x, q[3].y))
-                : make_uint2(pack4<ZERO_T_E4M3>(q[0].x, q[0].y, q[1].x, q[1].y), pack4<ZERO_T_E4M3>(q[2].x, q[2].y, q[3].x, q[3].y));
+    constexpr int F = E5M2 ? ZERO_T_E5M2 : ZERO_T_E4M3;
+    return make_uint2(pack4<F>(q[0].x, q[0].y, q[1].x, q[1].y), pack4<F>(q[2].x, q[2].y, q[3].x, q[3].y));
 }
-__device__ __forceinline__ uint2 bytes_of(const float2 x[4], float inv, bool e5m2)
+template <bool E5M2>
+__device__ __forceinline__ uint2 bytes_of(const float2 x[4], float inv)
 {
     float2 q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         q[i] = mul2(x[i], both(inv));
-    return bytes_of(q, e5m2);
+    return bytes_of<E5M2>(q);
 }
-__device__ __forceinline__ uint2 bytes_of(const float2 x[4], Inverse d, bool e5m2)
+template <bool E5M2>
+__device__ __forceinline__ uint2 bytes_of(const float2 x[4], Inverse d)
 {
     float2 q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         q[i] = fma2(x[i], both(d.hi), mul2(x[i], both(d.lo)));
-    return bytes_of(q, e5m2);
+    return bytes_of<E5M2>(q);
 }
 template <int W>
 __device__ __forceinline__ void put_bytes(uint8_t *p, int n, uint2 v)
