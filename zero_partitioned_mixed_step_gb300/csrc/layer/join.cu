@@ -9,6 +9,7 @@
 // much a matter of instructions as of bytes: pairs, maxima that lanes share out and
 // scales formed once.
 #include <initializer_list>
+#include <type_traits>
 
 #include "norms.cuh"
 
@@ -39,14 +40,25 @@ __device__ __forceinline__ float row_gate(const Gate &g, int64_t row)
 }
 
 template <class H>
-__device__ __forceinline__ float square_sum(const Raw8<H> &r, float2 s)
+__device__ __forceinline__ float square_sum(const Raw8<H> &r)
 {
-    float2 x[4];
+    float2 x[4], s = both(0.0f);
     pairs_of(r, x);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         s = fma2(x[i], x[i], s);
     return s.x + s.y;
+}
+
+// Zeros behind a row's end.  Where 8 divides its length, all 8 of a unit are there or none, and
+// what a unit without any holds is a NaN only where the row's own elements are.
+template <int W>
+__device__ __forceinline__ void clear_end(float2 x[4], int n)
+{
+    if (W != kWhole && n < 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = make_float2(2 * i < n ? x[i].x : 0.0f, 2 * i + 1 < n ? x[i].y : 0.0f);
 }
 
 // h of 8 columns (`by`: the row's gate times ro).
@@ -132,10 +144,7 @@ __device__ __forceinline__ void put_units(const JoinParams &p, int64_t row, int 
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             y[v][i] = mul2(mul2(h[v][i], both(rh)), y[v][i]);
-        if (W != kWhole && n < 8)  // behind the row's end 0 * rh may be a NaN
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                y[v][i] = make_float2(2 * i < n ? y[v][i].x : 0.0f, 2 * i + 1 < n ? y[v][i].y : 0.0f);
+        clear_end<W>(y[v], n);  // behind the row's end 0 * rh may be a NaN
         if (p.y && n > 0)
             put_pairs<W>(static_cast<H *>(p.y) + row * p.ldy + at, n, y[v]);
     }
@@ -143,18 +152,183 @@ __device__ __forceinline__ void put_units(const JoinParams &p, int64_t row, int 
         put_two<W>(p.h8, p.y8, row, c, step, cols, h, y, p.e5m2);
 }
 
-// A row to G lanes (16 or 32), or to the CTA (G = 0), V units of 8 to a thread.
-template <class H, int V, int G, int MAXT, int W>
-__global__ void __launch_bounds__(MAXT) join_kernel(const JoinParams p)
+// A CTA takes a run of neighbouring rows, two at a time, a thread the same 8 columns of each:
+// its factors stay in registers, and STAGES - 1 turns ahead are on their way through shared
+// memory (W other than kApart).  G: a row to 16 or 32 lanes, or (0) to the CTA.
+template <class H, int G, int MAXT, int STAGES, int W>
+__global__ void __launch_bounds__(MAXT, 512 / MAXT) join_kernel(const JoinParams p)
 {
-    constexpr int kWarps = MAXT / 32, kLanes = G ? G : 32;
+    constexpr bool kRing = W != kApart;
+    constexpr int kLanes = G ? G : 32;
+    __shared__ __align__(16) float slots[2][2][2 * 16];  // of the turn, of the sum
+    extern __shared__ __align__(16) unsigned char ring[];
+    const int t = G ? threadIdx.x % kLanes : threadIdx.x, c = t * 8;
+    const int groups = G ? MAXT / kLanes : 1, group = G ? threadIdx.x / kLanes : 0;
+    const int64_t all = (int64_t)gridDim.x * groups, me = (int64_t)blockIdx.x * groups + group;
+    const int64_t each = p.rows / all, more = p.rows % all;
+    const int64_t first = me * each + min(me, more);
+    const int mine = (int)each + (me < more ? 1 : 0), last = G == 16 ? (int)each + (more > 0 ? 1 : 0) : mine;
+    const int n = left_of(p.cols, c);
+    if (!G) {
+        for (int i = threadIdx.x; i < 128; i += blockDim.x)
+            (&slots[0][0][0])[i] = 0.0f;
+        __syncthreads();
+    }
+    float2 w[4], a[4];
+    get_vector<W>(p.w_pre, p.w_type, c, n, w);
+    post_factors<W>(p.w_post, p.w_type, p.gate, c, n, a);
+    const float fixed = p.gate.kind == ZERO_GATE_ONE ? load_one(p.gate.p, p.gate.type, 0) : 1.0f;
+
+    const uint32_t lanes = blockDim.x, turn_bytes = lanes * 64;  // o and x of two rows
+    const uint32_t place = (kRing ? (uint32_t)__cvta_generic_to_shared(ring) : 0u) + threadIdx.x * 16;
+    const H *f_o = static_cast<const H *>(p.o) + first * p.ldo + (n > 0 ? c : 0);
+    const H *f_x = static_cast<const H *>(p.x) + first * p.ldx + (n > 0 ? c : 0);
+    auto fetch = [&](int k, uint32_t stage) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int m = k + r < mine ? n : 0;  // where nothing is read the address is still one of the matrix
+            copy_async<16>(place + stage + r * lanes * 32, k + r < mine ? f_o : static_cast<const H *>(p.o), 2 * m);
+            copy_async<16>(place + stage + (r * 2 + 1) * lanes * 16, k + r < mine ? f_x : static_cast<const H *>(p.x), 2 * m);
+            f_o += p.ldo;
+            f_x += p.ldx;
+        }
+        commit_copies();
+    };
+    if (kRing)
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s)
+            fetch(s * 2, s * turn_bytes);
+    H *to_h = static_cast<H *>(p.h) + first * p.ldh + c, *to_y = static_cast<H *>(p.y) + first * p.ldy + c;
+    uint8_t *to_o8 = p.o8.q + first * p.o8.ld + c, *to_h8 = p.h8.q + first * p.h8.ld + c, *to_y8 = p.y8.q + first * p.y8.ld + c;
+    // the scale that a lane writes: of a row of o8, and of a row of h8 (the lower 8 of 16 lanes) or y8
+    const int block = c / kBlock, own2 = shared_index<2>(), own4 = shared_index<4>();
+    const bool inside = (c & ~(kBlock - 1)) < p.cols;
+    const Form &f4 = own4 < 2 ? p.h8 : p.y8;
+    float *to_so = (t & 7) == 0 && inside && p.o8.q ? p.o8.s + block * p.o8.lds + first + own2 : nullptr;
+    float *to_s4 = (t & 3) == 0 && inside && f4.q ? f4.s + block * f4.lds + first + (own4 & 1) : nullptr;
+    const Range range(own4 >= 2 && p.e5m2);
+
+    uint32_t stage = 0;
+    int turn = 0;
+    for (int k = 0; k < last; k += 2, turn ^= 1) {
+        Raw8<H> o[2], x[2];
+        const int m[2] = {k < mine ? n : 0, k + 1 < mine ? n : 0};
+        if (kRing) {
+            wait_copies<STAGES - 2>();
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                load_shared(o[r].w, place + stage + r * lanes * 32);
+                load_shared(x[r].w, place + stage + (r * 2 + 1) * lanes * 16);
+            }
+            // into the places of the turn before, whose values this thread has used
+            fetch(k + (STAGES - 1) * 2, stage == 0 ? (STAGES - 1) * turn_bytes : stage - turn_bytes);
+            stage = stage == (STAGES - 1) * turn_bytes ? 0 : stage + turn_bytes;
+        } else {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                o[r] = get_raw<W>(static_cast<const H *>(p.o) + (first + k + r) * p.ldo + c, m[r]);
+                x[r] = get_raw<W>(static_cast<const H *>(p.x) + (first + k + r) * p.ldx + c, m[r]);
+            }
+        }
+        float by[2];  // the row's gate times ro
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            by[r] = p.gate.kind != ZERO_GATE_ROWS ? fixed : k + r < mine ? load_one(p.gate.p, p.gate.type, first + k + r) : 0.0f;
+        if (p.w_post) {
+            float sq[2] = {square_sum(o[0]), square_sum(o[1])};
+            shared_sums<G>(sq, slots[turn][0]);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float ro = root(sq[r], p.inv_cols, p.eps);
+                by[r] *= ro;
+                if (t == 0 && k + r < mine && p.rstd_post)
+                    p.rstd_post[first + k + r] = ro;
+            }
+        }
+        if (p.o8.q) {
+            uint32_t most[2] = {amax8(o[0]), amax8(o[1])};
+            const float s = scale_of<false>(max_shared(most));
+            const Inverse inv = inverse_of(quick_inverse(s), s);
+            if (to_so && k + own2 < mine)
+                to_so[k] = s;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const Inverse d = {shared_value<2>(inv.hi, r), shared_value<2>(inv.lo, r)};
+                float2 v[4];
+                pairs_of(o[r], v);
+                if (m[r] > 0)
+                    put_bytes<W>(to_o8 + r * p.o8.ld, m[r], bytes_of<false>(v, d));
+            }
+            to_o8 += 2 * p.o8.ld;
+        }
+        float2 h[2][4];
+        float sq[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float2 xo[4], xs[4], s2 = both(0.0f);
+            pairs_of(o[r], xo);
+            pairs_of(x[r], xs);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                h[r][i] = fma2(both(p.scale), xs[i], mul2(a[i], mul2(xo[i], both(by[r]))));
+            clear_end<W>(h[r], m[r]);  // behind the row's end 0 * ro may be a NaN
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s2 = fma2(h[r][i], h[r][i], s2);
+            sq[r] = s2.x + s2.y;
+        }
+        shared_sums<G>(sq, slots[turn][1]);
+        float2 y[2][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float rh = root(sq[r], p.inv_cols, p.eps);
+            if (t == 0 && k + r < mine && p.rstd_pre)
+                p.rstd_pre[first + k + r] = rh;
+            if (m[r] > 0)
+                put_pairs<W>(to_h + r * p.ldh, m[r], h[r]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                y[r][i] = mul2(mul2(h[r][i], both(rh)), w[i]);
+            clear_end<W>(y[r], m[r]);
+            if (p.y && m[r] > 0)
+                put_pairs<W>(to_y + r * p.ldy, m[r], y[r]);
+        }
+        to_h += 2 * p.ldh;
+        to_y += 2 * p.ldy;
+        if (p.h8.q || p.y8.q) {
+            uint32_t most[4] = {amax8(h[0]), amax8(h[1]), amax8(y[0]), amax8(y[1])};
+            const float s = range.scale(max_shared(most)), inv = quick_inverse(s);
+            if (to_s4 && k + (own4 & 1) < mine)
+                to_s4[k] = s;
+            auto put = [&](auto e5m2) {
+                constexpr bool E = decltype(e5m2)::value;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float d = shared_value<4>(inv, r), e = shared_value<4>(inv, 2 + r);
+                    if (p.h8.q && m[r] > 0)
+                        put_bytes<W>(to_h8 + r * p.h8.ld, m[r], bytes_of<false>(h[r], d));
+                    if (p.y8.q && m[r] > 0)
+                        put_bytes<W>(to_y8 + r * p.y8.ld, m[r], bytes_of<E>(y[r], e));
+                }
+            };
+            if (p.e5m2)
+                put(std::true_type{});
+            else
+                put(std::false_type{});
+            to_h8 += 2 * p.h8.ld;
+            to_y8 += 2 * p.y8.ld;
+        }
+    }
+}
+
+// Rows of more columns than a CTA has threads for: one to a CTA, V units of 8 to a thread.
+template <class H, int V, int MAXT, int W>
+__global__ void __launch_bounds__(MAXT) join_wide_kernel(const JoinParams p)
+{
+    constexpr int kWarps = MAXT / 32;
     __shared__ float slots[2][kWarps];
-    const int t = G ? threadIdx.x % kLanes : threadIdx.x;
-    const int step = (G ? G : blockDim.x) * 8, c = t * 8;
-    const int64_t at = G ? (int64_t)blockIdx.x * (MAXT / kLanes) + threadIdx.x / kLanes : blockIdx.x;
-    const bool live = at < p.rows;
-    const int64_t row = live ? at : 0;
-    const int cols = live ? p.cols : 0;
+    const int t = threadIdx.x, step = blockDim.x * 8, c = t * 8, cols = p.cols;
+    const int64_t row = blockIdx.x;
     const H *po = static_cast<const H *>(p.o) + row * p.ldo, *px = static_cast<const H *>(p.x) + row * p.ldx;
     Raw8<H> o[V], x[V];
 #pragma unroll
@@ -168,10 +342,10 @@ __global__ void __launch_bounds__(MAXT) join_kernel(const JoinParams p)
         float sq[1] = {0.0f};
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            sq[0] = square_sum(o[v], make_float2(sq[0], 0.0f));
-        row_sums<G, kWarps>(sq, slots[0]);
+            sq[0] += square_sum(o[v]);
+        row_sums<0, kWarps>(sq, slots[0]);
         ro = root(sq[0], p.inv_cols, p.eps);
-        if (live && t == 0 && p.rstd_post)
+        if (t == 0 && p.rstd_post)
             p.rstd_post[row] = ro;
     }
     const float by = row_gate(p.gate, row) * ro;
@@ -180,10 +354,7 @@ __global__ void __launch_bounds__(MAXT) join_kernel(const JoinParams p)
     for (int v = 0; v < V; ++v) {
         const int n = left_of(cols, c + v * step);
         join8<W>(p, c + v * step, n, o[v], x[v], by, h[v]);
-        if (W != kWhole && n < 8)  // behind the row's end 0 * ro may be a NaN
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                h[v][i] = make_float2(2 * i < n ? h[v][i].x : 0.0f, 2 * i + 1 < n ? h[v][i].y : 0.0f);
+        clear_end<W>(h[v], n);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             s2 = fma2(h[v][i], h[v][i], s2);
@@ -191,9 +362,9 @@ __global__ void __launch_bounds__(MAXT) join_kernel(const JoinParams p)
     if (p.o8.q)
         put_halves<W>(p.o8, row, c, step, cols, o);
     float sq[1] = {s2.x + s2.y};
-    row_sums<G, kWarps>(sq, slots[1]);
+    row_sums<0, kWarps>(sq, slots[1]);
     const float rh = root(sq[0], p.inv_cols, p.eps);
-    if (live && t == 0 && p.rstd_pre)
+    if (t == 0 && p.rstd_pre)
         p.rstd_pre[row] = rh;
     put_units<W, V, H>(p, row, c, step, cols, h, rh);
 }
@@ -211,7 +382,7 @@ __global__ void __launch_bounds__(1024) join_long_kernel(const JoinParams p)
     if (p.w_post) {
         float sq[1] = {0.0f};
         for (int64_t c = threadIdx.x * 8; c < p.cols; c += 1024 * 8)
-            sq[0] = square_sum(get_raw<W>(po + c, left_of(p.cols, (int)c)), make_float2(sq[0], 0.0f));
+            sq[0] += square_sum(get_raw<W>(po + c, left_of(p.cols, (int)c)));
         row_sums<0, 32>(sq, slots[0]);
         ro = root(sq[0], p.inv_cols, p.eps);
         if (threadIdx.x == 0 && p.rstd_post)
@@ -224,10 +395,7 @@ __global__ void __launch_bounds__(1024) join_long_kernel(const JoinParams p)
         const int n = left_of(p.cols, c);
         o[0] = get_raw<W>(po + c, n);
         join8<W>(p, c, n, o[0], get_raw<W>(px + c, n), by, h[0]);
-        if (W != kWhole && n < 8)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                h[0][i] = make_float2(2 * i < n ? h[0][i].x : 0.0f, 2 * i + 1 < n ? h[0][i].y : 0.0f);
+        clear_end<W>(h[0], n);
     };
     for (int64_t c = threadIdx.x * 8; c < p.cols; c += 1024 * 8) {
         join((int)c);
@@ -252,22 +420,36 @@ __global__ void __launch_bounds__(1024) join_long_kernel(const JoinParams p)
 template <class H, int W>
 static int launch_join(const JoinParams &p, cudaStream_t stream)
 {
-    auto go = [&](auto kernel, int threads, int rows_per_cta) {
-        kernel<<<(unsigned)ceil_div(p.rows, rows_per_cta), threads, 0, stream>>>(p);
+    auto threads = [&](int units) { return (int)(ceil_div(ceil_div(p.cols, 8 * units), 32) * 32); };
+    auto go = [&](auto kernel, int threads) {
+        kernel<<<(unsigned)p.rows, threads, 0, stream>>>(p);
         return launch_status();
     };
-    auto threads = [&](int units) { return (int)(ceil_div(ceil_div(p.cols, 8 * units), 32) * 32); };
+    auto ring = [&](auto kernel, int threads, int groups, int stages) {
+        const size_t bytes = W != kApart ? (size_t)stages * threads * 64 : 0;
+        if (bytes > 32 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+            if (e != cudaSuccess)
+                return cuda_error(e);
+        }
+        const int64_t most = 152 * (512 / threads), turns = ceil_div(p.rows, 2 * groups);
+        kernel<<<(unsigned)(turns < most ? turns : most), threads, bytes, stream>>>(p);
+        return launch_status();
+    };
+    constexpr int kDepth = 4;
     if (p.cols <= 128)
-        return go(join_kernel<H, 1, 16, 256, W>, 256, 16);
+        return ring(join_kernel<H, 16, 256, kDepth, W>, 256, 16, kDepth);
     if (p.cols <= 256)
-        return go(join_kernel<H, 1, 32, 256, W>, 256, 8);
-    if (p.cols <= 512)
-        return go(join_kernel<H, 2, 32, 256, W>, 256, 8);
+        return ring(join_kernel<H, 32, 256, kDepth, W>, 256, 8, kDepth);
+    if (p.cols <= 2048)
+        return ring(join_kernel<H, 0, 256, kDepth, W>, threads(1), 1, kDepth);
+    if (p.cols <= 4096)
+        return ring(join_kernel<H, 0, 512, kDepth, W>, threads(1), 1, kDepth);
     if (p.cols <= 8192)
-        return go(join_kernel<H, 2, 0, 512, W>, threads(2), 1);
+        return go(join_wide_kernel<H, 2, 512, W>, threads(2));
     if (p.cols <= 16384)
-        return go(join_kernel<H, 2, 0, 1024, W>, threads(2), 1);
-    return go(join_long_kernel<H, W>, 1024, 1);
+        return go(join_wide_kernel<H, 2, 1024, W>, threads(2));
+    return go(join_long_kernel<H, W>, 1024);
 }
 
 }  // namespace zo

@@ -429,6 +429,25 @@ struct Kept<H, false> {
     __device__ __forceinline__ void get(float2 x[4]) const { pairs_of(r, x); }
 };
 
+// Copies of 4, 8 or 16 bytes into shared memory that run beside the thread; of them
+// `bytes` are read and the others become zeros.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void *from, int bytes)
+{
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+    else if constexpr (BYTES == 8)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>  // all but the last N groups have arrived
+__device__ __forceinline__ void wait_copies()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ float load_one(const void *p, int type, int64_t at)
 {
     if (type == ZERO_T_F16)

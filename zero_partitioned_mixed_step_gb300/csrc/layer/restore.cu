@@ -83,15 +83,15 @@ __global__ void __launch_bounds__(kRestoreThreads) restore_kernel(const RestoreP
         f[i] = *reinterpret_cast<const float2 *>(&factor[lane * 8 + 2 * i]);
     const int64_t row = r0 + lane * 8;
     const int n = row < p.rows ? left_of(p.rows, (int)row) : 0;
-#pragma unroll
+    const uint32_t *words = reinterpret_cast<const uint32_t *>(&tile[lane * 8][group ^ lane]);
+    uint8_t *to = p.t8.q + (c0 + group * 8) * p.t8.ld + row;
+#pragma unroll 1
     for (int half = 0; half < 2; ++half) {
-        const int k = group + 16 * half;  // columns 4k ..
-        const int64_t at = c0 + 4 * k;
+        const int64_t at = c0 + group * 8 + half * 4;  // four columns
         float2 x[4][4];  // of a column, rows 2i and 2i + 1
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint2 u = tile[lane * 8 + 2 * i][k >> 1 ^ lane], v = tile[lane * 8 + 2 * i + 1][k >> 1 ^ lane];
-            const uint32_t a = k & 1 ? u.y : u.x, b = k & 1 ? v.y : v.x;
+            const uint32_t a = words[2 * i * 32 + half], b = words[(2 * i + 1) * 32 + half];
 #pragma unroll
             for (int m = 0; m < 4; ++m)
                 x[m][i] = mul2(two_of<F8>(__byte_perm(a, b, m | (m + 4) << 4) & 0xFFFFu), f[i]);
@@ -113,12 +113,12 @@ __global__ void __launch_bounds__(kRestoreThreads) restore_kernel(const RestoreP
         const int mine = shared_index<4>();
         if (lane % 4 == 0 && at + mine < p.cols)
             p.t8.s[tr * p.t8.lds + at + mine] = s;
-        uint8_t *to = p.t8.q + at * p.t8.ld + row;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const Inverse d = {shared_value<4>(inv.hi, m), shared_value<4>(inv.lo, m)};
             if (n > 0 && at + m < p.cols)
-                put_bytes<W>(to + m * p.t8.ld, n, bytes_of<F8 == ZERO_T_E5M2>(x[m], d));
+                put_bytes<W>(to, n, bytes_of<F8 == ZERO_T_E5M2>(x[m], d));
+            to += p.t8.ld;
         }
     }
 }

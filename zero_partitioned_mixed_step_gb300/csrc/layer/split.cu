@@ -34,18 +34,6 @@ struct SplitParams {
     int32_t w_type;
 };
 
-// A thread's own copies into its own places of shared memory (nobody else reads
-// them, so waiting for them is all the order that is needed); bytes behind the row's
-// end become zeros.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t to, const void *from, int bytes)
-{
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
-}
-
 __device__ __forceinline__ void put_one(void *p, int type, int64_t at, float x)
 {
     if (type == ZERO_T_F16)
@@ -73,48 +61,6 @@ __device__ __forceinline__ void put_part(float *to, int n, bool whole, const flo
 
 constexpr int kSmallThreads = 256;  // of CTAs whose rows have 16 or 32 lanes
 
-// Sums of 3 R values over the threads of a row: G = 16 or 32 lanes, or (0) the CTA's warps,
-// at most 16.  The values are shared out between lanes as they are added, so that 6
-// take 9 shuffles in a warp and 8 behind the barrier.  `slot`: 16 floats for each of P
-// values, zeros where there is no warp, not used again before the next call's barrier.
-template <int G, int R>
-__device__ __forceinline__ void split_sums(float (&x)[3 * R], float *slot)
-{
-    constexpr int P = R == 2 ? 8 : 4, L = G ? G : 32;
-    float y[P];
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-        y[i] = i < 3 * R ? x[i] : 0.0f;
-    float s = sum_shared<P, L>(y);
-    if (!G) {
-        constexpr int kShare = 32 / P, kEach = 16 / kShare;  // lanes to a value, warps to a lane
-        const int lane = threadIdx.x & 31;
-        if (lane % kShare == 0)
-            slot[lane / kShare * 16 + (threadIdx.x >> 5)] = s;
-        __syncthreads();
-        const float *from = slot + lane / kShare * 16 + lane % kShare * kEach;
-        s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            s += from[i];
-#pragma unroll
-        for (int bit = kShare / 2; bit; bit >>= 1)
-            s += __shfl_xor_sync(0xFFFFFFFFu, s, bit);
-    }
-#pragma unroll
-    for (int i = 0; i < 3 * R; ++i)
-        x[i] = __shfl_sync(0xFFFFFFFFu, s, i * (L / P), L);
-}
-
-template <int WORDS>
-__device__ __forceinline__ void load_shared(uint32_t (&w)[WORDS], uint32_t from)
-{
-    if constexpr (WORDS == 4)
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from) : "memory");
-    else
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(from) : "memory");
-}
-
 // A CTA takes a run of neighbouring rows (of the blocks' scales, whose neighbours share
 // sectors, all are then read by one SM), R at a time, a thread the same V * 8 columns
 // of each, so that the sums over rows stay in registers.  W other than kApart: STAGES - 1
@@ -129,7 +75,7 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) split_kernel(const SplitPara
     constexpr int kLanes = G ? G : 32;
     constexpr int kUnit = 32 + 2 * K::kBytes;  // bytes of a row's unit: dy, dh, o, h
     constexpr int kElem = K::kBytes / 8;
-    __shared__ __align__(16) float slots[2][(R == 2 ? 8 : 4) * 16];
+    __shared__ __align__(16) float slots[2][kSumPlaces<3 * R> * 16];
     extern __shared__ __align__(16) unsigned char ring[];
     const int T = G ? G : blockDim.x;
     const int t = G ? threadIdx.x % kLanes : threadIdx.x;
@@ -189,7 +135,7 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) split_kernel(const SplitPara
             f_o += p.ldo * kElem;
             f_h += p.ldh * kElem;
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        commit_copies();
     };
     // the next turn's numbers of rows and of their blocks
     float so_next[R][V], sh_next[R][V], ro_next[R], rh_next[R], gate_next[R];
@@ -239,7 +185,7 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) split_kernel(const SplitPara
         Raw8<H> dy[R][V], dh[R][V];
         K o[R][V], h[R][V];
         if (kRing)
-            asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+            wait_copies<STAGES - 2>();
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -304,7 +250,7 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) split_kernel(const SplitPara
                 sum[3 * r + 2] = fmaf((s2.x + s2.y) * sh[r][v], so[r][v], sum[3 * r + 2]);
             }
         }
-        split_sums<G, R>(sum, slots[turn]);
+        shared_sums<G>(sum, slots[turn]);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const bool live = k + r < mine;
