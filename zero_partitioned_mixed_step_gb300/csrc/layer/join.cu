@@ -50,17 +50,8 @@ __device__ __forceinline__ float square_sum(const Raw8<H> &r)
     return s.x + s.y;
 }
 
-// Zeros behind a row's end.  Where 8 divides its length, all 8 of a unit are there or none, and
-// what a unit without any holds is a NaN only where the row's own elements are.
-template <int W>
-__device__ __forceinline__ void clear_end(float2 x[4], int n)
-{
-    if (W != kWhole && n < 8)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            x[i] = make_float2(2 * i < n ? x[i].x : 0.0f, 2 * i + 1 < n ? x[i].y : 0.0f);
-}
-
+// Behind a row's end o, x, w_post and w_pre are zeros, and so are h and y, but for a row whose by or
+// rh is not finite: there they are NaN, and so is the row's own sum or what is made of it.
 // h of 8 columns (`by`: the row's gate times ro).
 template <int W, class H>
 __device__ __forceinline__ void join8(const JoinParams &p, int c, int n, const Raw8<H> &o, const Raw8<H> &x, float by, float2 h[4])
@@ -144,7 +135,6 @@ __device__ __forceinline__ void put_units(const JoinParams &p, int64_t row, int 
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             y[v][i] = mul2(mul2(h[v][i], both(rh)), y[v][i]);
-        clear_end<W>(y[v], n);  // behind the row's end 0 * rh may be a NaN
         if (p.y && n > 0)
             put_pairs<W>(static_cast<H *>(p.y) + row * p.ldy + at, n, y[v]);
     }
@@ -156,7 +146,7 @@ __device__ __forceinline__ void put_units(const JoinParams &p, int64_t row, int 
 // its factors stay in registers, and STAGES - 1 turns ahead are on their way through shared
 // memory (W other than kApart).  G: a row to 16 or 32 lanes, or (0) to the CTA.
 template <class H, int G, int MAXT, int STAGES, int W>
-__global__ void __launch_bounds__(MAXT, 512 / MAXT) join_kernel(const JoinParams p)
+__global__ void __launch_bounds__(MAXT, MAXT == 320 ? 2 : 512 / MAXT) join_kernel(const JoinParams p)
 {
     constexpr bool kRing = W != kApart;
     constexpr int kLanes = G ? G : 32;
@@ -271,7 +261,6 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) join_kernel(const JoinParams
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 h[r][i] = fma2(both(p.scale), xs[i], mul2(a[i], mul2(xo[i], both(by[r]))));
-            clear_end<W>(h[r], m[r]);  // behind the row's end 0 * ro may be a NaN
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 s2 = fma2(h[r][i], h[r][i], s2);
@@ -289,7 +278,6 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) join_kernel(const JoinParams
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 y[r][i] = mul2(mul2(h[r][i], both(rh)), w[i]);
-            clear_end<W>(y[r], m[r]);
             if (p.y && m[r] > 0)
                 put_pairs<W>(to_y + r * p.ldy, m[r], y[r]);
         }
@@ -354,7 +342,6 @@ __global__ void __launch_bounds__(MAXT) join_wide_kernel(const JoinParams p)
     for (int v = 0; v < V; ++v) {
         const int n = left_of(cols, c + v * step);
         join8<W>(p, c + v * step, n, o[v], x[v], by, h[v]);
-        clear_end<W>(h[v], n);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             s2 = fma2(h[v][i], h[v][i], s2);
@@ -395,7 +382,6 @@ __global__ void __launch_bounds__(1024) join_long_kernel(const JoinParams p)
         const int n = left_of(p.cols, c);
         o[0] = get_raw<W>(po + c, n);
         join8<W>(p, c, n, o[0], get_raw<W>(px + c, n), by, h[0]);
-        clear_end<W>(h[0], n);
     };
     for (int64_t c = threadIdx.x * 8; c < p.cols; c += 1024 * 8) {
         join((int)c);
@@ -432,7 +418,7 @@ static int launch_join(const JoinParams &p, cudaStream_t stream)
             if (e != cudaSuccess)
                 return cuda_error(e);
         }
-        const int64_t most = 152 * (512 / threads), turns = ceil_div(p.rows, 2 * groups);
+        const int64_t most = 152 * ((threads > 256 && threads <= 320 ? 640 : 512) / threads), turns = ceil_div(p.rows, 2 * groups);
         kernel<<<(unsigned)(turns < most ? turns : most), threads, bytes, stream>>>(p);
         return launch_status();
     };
@@ -443,6 +429,8 @@ static int launch_join(const JoinParams &p, cudaStream_t stream)
         return ring(join_kernel<H, 32, 256, kDepth, W>, 256, 8, kDepth);
     if (p.cols <= 2048)
         return ring(join_kernel<H, 0, 256, kDepth, W>, threads(1), 1, kDepth);
+    if (p.cols <= 2560)  // two CTAs to an SM where registers are 96 (8192x4096 elements in 14563 rows: 66 us, 87 with one)
+        return ring(join_kernel<H, 0, 320, kDepth, W>, threads(1), 1, kDepth);
     if (p.cols <= 4096)
         return ring(join_kernel<H, 0, 512, kDepth, W>, threads(1), 1, kDepth);
     if (p.cols <= 8192)
