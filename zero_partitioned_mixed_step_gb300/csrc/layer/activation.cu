@@ -51,82 +51,100 @@ struct ActParams {
 
 constexpr int kActRows = 32;  // rows of a CTA: two to each 16 lanes
 
-// A CTA takes 128 columns of 32 neighbouring rows, whose scales lie side by side.
+// A tile is 128 columns of 32 neighbouring rows, whose scales lie side by side.  CTAs walk the
+// tiles with the next one on its way to the registers.
 template <class H, bool GELU, int W>
-__global__ void __launch_bounds__(256) act_kernel(const ActParams p)
+__global__ void __launch_bounds__(256, 3) act_kernel(const ActParams p)
 {
-    const int lane = threadIdx.x & 15;
-    const TileAt at = tile_at(p.tiles);
-    const int64_t tc = at.c, row = (int64_t)at.r * kActRows + (threadIdx.x >> 4) * 2;
-    const int c = at.c * kBlock + lane * 8, nc = left_of(p.cols, c);
-    const int n[2] = {row < p.rows ? nc : 0, row + 1 < p.rows ? nc : 0};
-    Raw8<H> u[2], v[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        u[k] = get_raw<W>(static_cast<const H *>(p.u) + (row + k) * p.ldu + c, n[k]);
-        if (p.v)
-            v[k] = get_raw<W>(static_cast<const H *>(p.v) + (row + k) * p.ldv + c, n[k]);
-    }
-    // two rows into a form; lanes 8 .. 15 hold the second one's scale
-    auto put_scale = [&](const Form &f, float s) {
-        const int64_t r = row + (lane >> 3);
-        if ((lane & 7) == 0 && r < p.rows)
-            f.s[tc * f.lds + r] = s;
-    };
-    auto put_kept = [&](const Form &f, const Raw8<H> (&r)[2]) {
-        uint32_t most[2] = {amax8(r[0]), amax8(r[1])};
-        const float s = scale_of<false>(max_shared(most));
-        const Inverse inv = inverse_of(quick_inverse(s), s);
-        put_scale(f, s);
+    const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
+    const uint32_t across = p.tiles.cols, tiles = p.tiles.rows * across;
+    Raw8<H> u_next[2], v_next[2];
+    auto fetch = [&](uint32_t tile) {
+        const int64_t row = (int64_t)(tile / across) * kActRows + group * 2;
+        const int c = (int)(tile % across) * kBlock + lane * 8, nc = tile < tiles ? left_of(p.cols, c) : 0;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const Inverse d = {shared_value<2>(inv.hi, k), shared_value<2>(inv.lo, k)};
-            float2 x[4];
-            pairs_of(r[k], x);
-            if (n[k] > 0)
-                put_bytes<W>(f.q + (row + k) * f.ld + c, n[k], bytes_of<false>(x, d));
+            const int n = row + k < p.rows ? nc : 0;
+            u_next[k] = get_raw<W>(static_cast<const H *>(p.u) + (row + k) * p.ldu + c, n);
+            if (p.v)
+                v_next[k] = get_raw<W>(static_cast<const H *>(p.v) + (row + k) * p.ldv + c, n);
         }
     };
-    float2 a[2][4];
+    fetch(blockIdx.x);
+    for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const Raw8<H> u[2] = {u_next[0], u_next[1]}, v[2] = {v_next[0], v_next[1]};
+        fetch(tile + gridDim.x);
+        const int64_t tc = tile % across, row = (int64_t)(tile / across) * kActRows + group * 2;
+        const int c = (int)tc * kBlock + lane * 8, nc = left_of(p.cols, c);
+        const int n[2] = {row < p.rows ? nc : 0, row + 1 < p.rows ? nc : 0};
+        // the scale that a lane writes of N values, two rows of each form
+        auto put_scale = [&](const Form &f, int mine, int every, float s) {
+            const int64_t r = row + (mine & 1);
+            if (lane % every == 0 && f.q && r < p.rows)
+                f.s[tc * f.lds + r] = s;
+        };
+        auto put_kept = [&](const Form &f, const Raw8<H> &r, int k, Inverse d) {
+            float2 x[4];
+            pairs_of(r, x);
+            if (f.q && n[k] > 0)
+                put_bytes<W>(f.q + (row + k) * f.ld + c, n[k], bytes_of<false>(x, d));
+        };
+        if (p.v && (p.u8.q || p.v8.q)) {
+            uint32_t most[4] = {amax8(u[0]), amax8(u[1]), amax8(v[0]), amax8(v[1])};
+            const float s = scale_of<false>(max_shared(most));
+            const Inverse inv = inverse_of(quick_inverse(s), s);
+            const int mine = shared_index<4>();
+            put_scale(mine < 2 ? p.u8 : p.v8, mine, 4, s);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        float2 x[4], dz;
-        pairs_of(u[k], x);
+            for (int k = 0; k < 4; ++k) {
+                const Inverse d = {shared_value<4>(inv.hi, k), shared_value<4>(inv.lo, k)};
+                put_kept(k < 2 ? p.u8 : p.v8, k < 2 ? u[k & 1] : v[k & 1], k & 1, d);
+            }
+        } else if (p.u8.q) {
+            uint32_t most[2] = {amax8(u[0]), amax8(u[1])};
+            const float s = scale_of<false>(max_shared(most));
+            const Inverse inv = inverse_of(quick_inverse(s), s);
+            put_scale(p.u8, shared_index<2>(), 8, s);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            a[k][i] = mul2(x[i], sigmoid_of<GELU>(x[i], dz));
-        if (p.v) {
-            pairs_of(v[k], x);
+            for (int k = 0; k < 2; ++k)
+                put_kept(p.u8, u[k], k, {shared_value<2>(inv.hi, k), shared_value<2>(inv.lo, k)});
+        }
+        float2 a[2][4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float2 x[4], dz;
+            pairs_of(u[k], x);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                a[k][i] = mul2(a[k][i], x[i]);
-        }
-    }
-    if (p.u8.q)
-        put_kept(p.u8, u);
-    if (p.v8.q)
-        put_kept(p.v8, v);
-    if (p.a)
+                a[k][i] = mul2(x[i], sigmoid_of<GELU>(x[i], dz));
+            if (p.v) {
+                pairs_of(v[k], x);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            if (n[k] > 0)
+                for (int i = 0; i < 4; ++i)
+                    a[k][i] = mul2(a[k][i], x[i]);
+            }
+            if (p.a && n[k] > 0)
                 put_pairs<W>(static_cast<H *>(p.a) + (row + k) * p.lda + c, n[k], a[k]);
-    auto put_a8 = [&](auto e5m2) {
-        constexpr bool E = decltype(e5m2)::value;
-        uint32_t most[2] = {amax8(a[0]), amax8(a[1])};
-        const float s = scale_of<E>(max_shared(most)), inv = quick_inverse(s);
-        put_scale(p.a8, s);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float d = shared_value<2>(inv, k);
-            if (n[k] > 0)
-                put_bytes<W>(p.a8.q + (row + k) * p.a8.ld + c, n[k], bytes_of<E>(a[k], d));
         }
-    };
-    if (p.a8.q && p.e5m2)
-        put_a8(std::true_type{});
-    else if (p.a8.q)
-        put_a8(std::false_type{});
+        if (!p.a8.q)
+            continue;
+        auto put_a8 = [&](auto e5m2) {
+            constexpr bool E = decltype(e5m2)::value;
+            uint32_t most[2] = {amax8(a[0]), amax8(a[1])};
+            const float s = scale_of<E>(max_shared(most)), inv = quick_inverse(s);
+            put_scale(p.a8, shared_index<2>(), 8, s);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float d = shared_value<2>(inv, k);
+                if (n[k] > 0)
+                    put_bytes<W>(p.a8.q + (row + k) * p.a8.ld + c, n[k], bytes_of<E>(a[k], d));
+            }
+        };
+        if (p.e5m2)
+            put_a8(std::true_type{});
+        else
+            put_a8(std::false_type{});
+    }
 }
 
 // ------------------------------------------------------------------ backward
@@ -440,11 +458,11 @@ int zero_activation_fp8(const void *u, int64_t ldu, const void *v, int64_t ldv, 
     for (const Form *f : {&p.a8, &p.u8, &p.v8})
         wide = wide && (!f->q || f->wide);
     p.e5m2 = a8 && fp8 == ZERO_T_E5M2;
-    const int64_t grid = (int64_t)p.tiles.rows * p.tiles.cols;
-    if (grid > kMaxDim)
+    const int64_t tiles = (int64_t)p.tiles.rows * p.tiles.cols, most = 152 * 3;  // three CTAs to an SM
+    if (tiles > kMaxDim)
         return ZERO_EINVAL;
     auto go = [&](auto kernel) {
-        kernel<<<(unsigned)grid, 256, 0, stream>>>(p);
+        kernel<<<(unsigned)(tiles < most ? tiles : most), 256, 0, stream>>>(p);
         return launch_status();
     };
     auto by_type = [&](auto half) {
