@@ -85,7 +85,8 @@ ZERO_API int zero_gated_norms_fp8(const void *o, int64_t ldo, const void *x, int
                                   zero_stream_t stream);
 
 /* Bytes of workspace that zero_gated_norms_backward needs (0 for invalid sizes;
- * contents undefined before and after). */
+ * contents undefined before and after, 32-byte aligned).  One workspace may serve
+ * one call after the other, of sizes that it is large enough for, not two at once. */
 ZERO_API size_t zero_gated_norms_workspace_bytes(int64_t rows, int64_t cols);
 
 /*

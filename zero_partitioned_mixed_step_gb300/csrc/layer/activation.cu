@@ -3,6 +3,14 @@
 //
 //   silu: z = u;  gelu's tanh form: z = 2 sqrt(2 / pi) (u + 0.044715 u^3)
 //   du = da v (sig + u sig (1 - sig) z'),  dv = da u sig
+//
+// Forward 8192x14336 bf16, gated, three 8-bit forms: 153 us, 5.4 TB/s (0.80 of the copy
+// rate; issue slots 66 % busy, ALU 51, DRAM 65).  Backward from checkpoints, du and dv
+// in 8 bits along the row and along the tokens, a along the tokens: 262 us, 4.1 TB/s (0.61; issue
+// 56 %, ALU 46, DRAM 50, 16 warps to an SM).  390 instructions for 8 elements of five 8-bit
+// forms, most of them conversions, leave the bytes behind; the registers (126) and the staged
+// tile (98 KB) allow no third CTA.  CTAs that walk the tiles with the next one's rows on their
+// way took 297.
 #include <initializer_list>
 #include <type_traits>
 

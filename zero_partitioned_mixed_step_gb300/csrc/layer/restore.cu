@@ -2,9 +2,14 @@
 // operand of a weight's gradient made from a checkpoint, without the tensor in a half
 // type in between.
 //
-// Bound by memory.  A CTA takes a 128x128 tile, 8 rows to 16 lanes of 8 columns.
-// The bytes go through shared memory as they are: within a tile a row has one scale
-// and one factor, so a transposed value is a byte times a row's and a column's number.
+// A CTA takes a 128x128 tile, 8 rows to 16 lanes of 8 columns.  The bytes go through
+// shared memory as they are: within a tile a row has one scale and one factor, so a
+// transposed value is a byte times a row's and a column's number.
+//
+// 8192x14336 as bf16: 55 us, 6.4 TB/s (0.95 of the copy rate).  8192x4096 transposed with both
+// factors: 21 us, 3.3 TB/s (0.48; issue slots 65 % busy, ALU 57): taking bytes apart and together
+// again is what it does.  CTAs that walk the tiles with two more on their way took 23, and the
+// first case 63.
 #include "layer.cuh"
 
 namespace zo {
