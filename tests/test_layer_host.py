@@ -26,7 +26,7 @@ def lib():
 
 def form(q=P, ld=130, s=P, lds=4):
     from zero_partitioned_mixed_step_gb300._layer_abi import Fp8Form
-    return Fp8Form(q, ld, s, lds)
+    return ctypes.byref(Fp8Form(q, ld, s, lds))
 
 
 def test_exports_what_the_header_declares(lib):

@@ -8,15 +8,14 @@ a pair in E4M3, or the half tensor itself.
 """
 from __future__ import annotations
 
-import ctypes
 from typing import Optional, Tuple
 
 import torch
 
 from ._abi import ZeroError
-from ._layer_abi import (ACT_GELU, ACT_SILU, GATE_COLS, GATE_NONE, GATE_ONE, GATE_ROWS, Fp8Form, lib)
-from ._ops_abi import T_E4M3, T_F32, check
-from .ops import (_F32, _F8, _FLOAT, _HALF, _NONE, _TYPE, _blocks, _current, _flat, _matrix, _stream, _type)
+from ._layer_abi import (ACT_GELU, ACT_SILU, GATE_COLS, GATE_NONE, GATE_ONE, GATE_ROWS, lib, pack_form)
+from ._ops_abi import BLOCK, T_E4M3, T_F32, check
+from .ops import (_F32, _F8, _FLOAT, _HALF, _NONE, _TYPE, _blocks, _current, _flat, _matrix, _stream, _type, _where)
 
 __all__ = [
     "zero_gated_norms_fp8", "zero_gated_norms_workspace_bytes", "zero_gated_norms_backward",
@@ -28,12 +27,13 @@ _E4M3 = (torch.float8_e4m3fn,)
 _ACT = {"silu": ACT_SILU, "gelu": ACT_GELU}
 
 
-def _form(pair: Optional[Pair], rows: int, cols: int, name: str, dtypes, dev: int) -> Optional[Fp8Form]:
+def _form(pair: Optional[Pair], rows: int, cols: int, name: str, dtypes, dev: int) -> Optional[bytes]:
     if pair is None:
         return None
     q, s = pair
-    return Fp8Form(*_matrix(q, rows, cols, name, dtypes, dev),
-                   *_matrix(s, _blocks(cols), rows, name + " scales", _F32, dev))
+    pq, ld = _matrix(q, rows, cols, name, dtypes, dev)
+    ps, lds = _matrix(s, (cols + BLOCK - 1) // BLOCK, rows, name, _F32, dev)
+    return pack_form(pq or 0, ld, ps or 0, lds)
 
 
 def _some(t: Optional[torch.Tensor], rows: int, cols: int, name: str, dtypes, dev: int) -> Tuple[Optional[int], int]:
@@ -42,16 +42,25 @@ def _some(t: Optional[torch.Tensor], rows: int, cols: int, name: str, dtypes, de
 
 def _one_type(*pairs: Optional[Pair]) -> int:
     """The 8-bit type of the pairs that are there (E4M3 without any)."""
-    types = {p[0].dtype for p in pairs if p is not None}
-    if len(types) > 1:
-        raise TypeError("8-bit outputs: one type expected")
-    return _TYPE.get(types.pop(), -1) if types else T_E4M3
+    dtype = None
+    for p in pairs:
+        if p is not None:
+            if dtype is not None and p[0].dtype != dtype:
+                raise TypeError("8-bit outputs: one type expected")
+            dtype = p[0].dtype
+    return T_E4M3 if dtype is None else _TYPE.get(dtype, -1)
 
 
-def _vector(t: torch.Tensor, n: int, name: str, dev: int, dtype=None) -> int:
+def _vector(t: Optional[torch.Tensor], n: int, name: str, dev: int, dtype=None) -> Optional[int]:
+    if t is None:
+        return None
     if t.numel() != n or dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name}: {n} elements{f' of {dtype}' if dtype else ''} expected")
-    return _flat(t, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous tensor expected")
+    if t.get_device() != dev or dev < 0:
+        _where(name)
+    return t.data_ptr()
 
 
 def _gate_kind(gate: Optional[torch.Tensor], rows: int, cols: int) -> int:
@@ -68,12 +77,9 @@ def _gate_kind(gate: Optional[torch.Tensor], rows: int, cols: int) -> int:
 
 def _norm_weights(w_pre, w_post, cols, dev):
     """(w_post, w_pre, their type)."""
-    post = None
-    if w_post is not None:
-        if w_post.dtype != w_pre.dtype:
-            raise TypeError("w_pre, w_post: one type expected")
-        post = _vector(w_post, cols, "w_post", dev)
-    return post, _vector(w_pre, cols, "w_pre", dev), _type(w_pre)
+    if w_post is not None and w_post.dtype != w_pre.dtype:
+        raise TypeError("w_pre, w_post: one type expected")
+    return _vector(w_post, cols, "w_post", dev), _vector(w_pre, cols, "w_pre", dev), _type(w_pre)
 
 
 # ----------------------------------------------------------------- norms around a block
@@ -102,8 +108,8 @@ def zero_gated_norms_fp8(o: torch.Tensor, x: torch.Tensor, w_pre: torch.Tensor, 
               _type(gate) if kind else T_F32, scale, _TYPE[o.dtype], rows, cols, eps, ph, ldh, py, ldy, _one_type(y8),
               _form(y8, rows, cols, "y8", _F8, dev), _form(o8, rows, cols, "o8", _E4M3, dev),
               _form(h8, rows, cols, "h8", _E4M3, dev),
-              None if rstd_post is None else _vector(rstd_post, rows, "rstd_post", dev, torch.float32),
-              None if rstd_pre is None else _vector(rstd_pre, rows, "rstd_pre", dev, torch.float32),
+              _vector(rstd_post, rows, "rstd_post", dev, torch.float32),
+              _vector(rstd_pre, rows, "rstd_pre", dev, torch.float32),
               _stream(stream, dev)))
 
 
@@ -145,23 +151,24 @@ def zero_gated_norms_backward(dy: torch.Tensor, o: torch.Tensor, h: torch.Tensor
     dt = dy.dtype
     pdy, lddy = _matrix(dy, rows, cols, "dy", _HALF, dev)
     kind = _gate_kind(gate, rows, cols)
-    grads = [g for g in (dw_pre, dw_post, dgate) if g is not None]
-    if any(g.dtype != grads[0].dtype for g in grads):
-        raise TypeError("dw_pre, dw_post, dgate: one type expected")
+    grad_type = T_F32
+    for g in (dw_pre, dw_post, dgate):
+        if g is not None:
+            grad_type = _type(g)
+            if g.dtype != (dw_pre if dw_pre is not None else dw_post if dw_post is not None else dgate).dtype:
+                raise TypeError("dw_pre, dw_post, dgate: one type expected")
     if ws is None and (dw_pre is not None or dw_post is not None or dgate is not None and kind != GATE_ROWS):
         raise ValueError("ws: a workspace expected (zero_gated_norms_workspace_bytes)")
     check("zero_gated_norms_backward",
           lib().zero_gated_norms_backward(
               pdy, lddy, *_some(dh, rows, cols, "dh", (dt,), dev), *_kept(o, so, rows, cols, "o", dt, dev),
               *_kept(h, sh, rows, cols, "h", dt, dev),
-              None if rstd_post is None else _vector(rstd_post, rows, "rstd_post", dev, torch.float32),
+              _vector(rstd_post, rows, "rstd_post", dev, torch.float32),
               _vector(rstd_pre, rows, "rstd_pre", dev, torch.float32), *_norm_weights(w_pre, w_post, cols, dev),
               _flat(gate, dev), kind, _type(gate) if kind else T_F32, scale, _TYPE[dt], rows, cols,
               *_matrix(d_o, rows, cols, "d_o", (dt,), dev), *_matrix(dx, rows, cols, "dx", (dt,), dev),
-              None if dw_post is None else _vector(dw_post, cols, "dw_post", dev),
-              None if dw_pre is None else _vector(dw_pre, cols, "dw_pre", dev),
-              None if dgate is None else _vector(dgate, gate.numel(), "dgate", dev),
-              _type(grads[0]) if grads else T_F32, add, _flat(ws, dev), 0 if ws is None else ws.nbytes,
+              _vector(dw_post, cols, "dw_post", dev), _vector(dw_pre, cols, "dw_pre", dev),
+              _vector(dgate, 0 if gate is None else gate.numel(), "dgate", dev), grad_type, add, _flat(ws, dev), 0 if ws is None else ws.nbytes,
               _stream(stream, dev)))
 
 
@@ -238,7 +245,7 @@ def zero_fp8_restore(q: torch.Tensor, s: torch.Tensor, row: Optional[torch.Tenso
     px, ldx = _some(x, rows, cols, "x", _FLOAT, dev)
     check("zero_fp8_restore",
           lib().zero_fp8_restore(
-              pq, _TYPE[q.dtype], ldq, ps, lds, None if row is None else _vector(row, rows, "row", dev, torch.float32),
-              None if col is None else _vector(col, cols, "col", dev), T_F32 if col is None else _type(col), rows, cols,
+              pq, _TYPE[q.dtype], ldq, ps, lds, _vector(row, rows, "row", dev, torch.float32),
+              _vector(col, cols, "col", dev), T_F32 if col is None else _type(col), rows, cols,
               px, T_F32 if x is None else _TYPE[x.dtype], ldx, _form(t8, cols, rows, "t8", (q.dtype,), dev),
               _stream(stream, dev)))
