@@ -313,6 +313,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 320 ? 2 : 512 / MAXT) join_kerne
             to_y8 += 2 * p.y8.ld;
         }
     }
+    if (kRing)
+        wait_copies<0>();  // nothing is on its way when the CTA leaves
 }
 
 // Rows of more than 4096 columns: one to a CTA, V units of 8 to a thread.  Clusters of 2 to 4

@@ -294,6 +294,8 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) split_kernel(const SplitPara
             do_row += p.lddo;
         }
     }
+    if (kRing)
+        wait_copies<0>();  // nothing is on its way when the CTA leaves
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the columns' launch may begin
     if (!p.part)
         return;
