@@ -217,7 +217,7 @@ __device__ __forceinline__ uint32_t amax8(const Raw8<H> &r)
     return a.bits();
 }
 
-// The sums of P values (4 or 8) over L lanes (16 or 32), shared out in the same way: value i
+// The sums of P values (2, 4 or 8) over L lanes (16 or 32), shared out in the same way: value i
 // ends with the lanes L / P * i and up.
 template <int P, int L>
 __device__ __forceinline__ float sum_shared(float (&x)[P])
@@ -429,17 +429,15 @@ struct Kept<H, false> {
     __device__ __forceinline__ void get(float2 x[4]) const { pairs_of(r, x); }
 };
 
-// Copies of 4, 8 or 16 bytes into shared memory that run beside the thread; of them
+// Copies of 8 or 16 bytes into shared memory that run beside the thread; of them
 // `bytes` are read and the others become zeros.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t to, const void *from, int bytes)
 {
     if constexpr (BYTES == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
-    else if constexpr (BYTES == 8)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>  // all but the last N groups have arrived

@@ -258,6 +258,15 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) split_kernel(const SplitPara
         }
         shared_sums<G>(sum, slots[turn]);
 #pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                renew(dy[r][v].w);
+                renew(dh[r][v].w);
+                renew(o[r][v].r.w);
+                renew(h[r][v].r.w);
+            }
+#pragma unroll
         for (int r = 0; r < R; ++r) {
             const bool live = k + r < mine;
             const float m = sum[3 * r] * p.inv_cols;
