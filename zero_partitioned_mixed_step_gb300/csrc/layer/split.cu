@@ -74,10 +74,13 @@ constexpr int kSmallThreads = 256;  // of CTAs whose rows have 16 or 32 lanes
 // factors and sums, have no room for.  A block's scale and its row's rstd are applied to sums
 // and factors, not to the kept values one by one.
 template <class H, bool S8, int V, int R, int G, int MAXT, int STAGES, int W>
-__global__ void __launch_bounds__(MAXT, 512 / MAXT) split_kernel(const SplitParams p)
+__global__ void __launch_bounds__(MAXT, MAXT == 320 ? 2 : 512 / MAXT) split_kernel(const SplitParams p)
 {
     using K = Kept<H, S8>;
     constexpr bool kRing = W != kApart;
+    // The next turn's scales in registers, where a thread has one unit; with two they would spill (4096x8192
+    // 105 us, 81 without), and kept halves have none.
+    constexpr bool kAhead = S8 && V == 1;
     constexpr int kLanes = G ? G : 32;
     constexpr int kUnit = 32 + 2 * K::kBytes;  // bytes of a row's unit: dy, dh, o, h
     constexpr int kElem = K::kBytes / 8;
@@ -180,7 +183,8 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) split_kernel(const SplitPara
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s)
             fetch(s * R, s * turn_bytes);
-    fetch_scales(0);
+    if (kAhead)
+        fetch_scales(0);
 
     // two groups of 16 lanes share a warp and its shuffles, so both take as many turns
     const int last = G == 16 ? (int)each + (more > 0 ? 1 : 0) : mine;
@@ -190,6 +194,8 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) split_kernel(const SplitPara
     for (int k = 0; k < last; k += R, turn ^= 1) {
         Raw8<H> dy[R][V], dh[R][V];
         K o[R][V], h[R][V];
+        if (!kAhead)
+            fetch_scales(k);
         if (kRing)
             wait_copies<STAGES - 2>();
 #pragma unroll
@@ -230,7 +236,8 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) split_kernel(const SplitPara
                 sh[r][v] = sh_next[r][v] * rh[r];
             }
         }
-        fetch_scales(k + R);
+        if (kAhead)
+            fetch_scales(k + R);
 
         float sum[3 * R];  // D, P, Q of each row
 #pragma unroll
@@ -529,7 +536,7 @@ struct Cut {
     int threads, groups;
     int64_t ctas;
 };
-static Cut cut_of(int64_t rows, int64_t cols)
+static Cut cut_of(int64_t rows, int64_t cols, bool s8)
 {
     Cut c{};
     int64_t most;
@@ -540,7 +547,7 @@ static Cut cut_of(int64_t rows, int64_t cols)
     } else if (cols <= 8192) {
         c.threads = (int)(ceil_div(ceil_div(cols, cols <= 4096 ? 8 : 16), 32) * 32);
         c.groups = 1;
-        most = 152 * (512 / c.threads);
+        most = 152 * ((!s8 && cols <= 2560 ? 682 : 512) / c.threads);  // by registers: 96 and 128
     } else {
         c.threads = 1024;
         c.groups = 1;
@@ -568,6 +575,9 @@ static int launch_split(const SplitParams &p, const Cut &cut, cudaStream_t strea
         return go(split_kernel<H, S8, 1, 1, 16, kSmallThreads, 4, W>, 1, 4);
     if (p.cols <= 256)
         return go(split_kernel<H, S8, 1, 1, 32, kSmallThreads, 4, W>, 1, 4);
+    if constexpr (!S8)
+        if (p.cols <= 2560)  // 96 registers (32768x1024 fp16 70 us, with 128 77; from checkpoints they spill)
+            return go(split_kernel<H, S8, 1, 2, 0, 320, 2, W>, 2, 2);
     if (p.cols <= 2048)
         return go(split_kernel<H, S8, 1, 2, 0, 256, 3, W>, 2, 3);
     if (p.cols <= 4096)
@@ -604,7 +614,8 @@ size_t zero_gated_norms_workspace_bytes(int64_t rows, int64_t cols)
 {
     if (bad_dim(rows) || bad_dim(cols) || cols < 1)
         return 0;
-    return (size_t)cut_of(rows, cols).ctas * (size_t)(2 * cols + 1) * sizeof(float);
+    // kept halves have the most CTAs
+    return (size_t)cut_of(rows, cols, false).ctas * (size_t)(2 * cols + 1) * sizeof(float);
 }
 
 int zero_gated_norms_backward(const void *dy, int64_t lddy, const void *dh, int64_t lddh, const void *o, int64_t ldo,
@@ -643,7 +654,7 @@ int zero_gated_norms_backward(const void *dy, int64_t lddy, const void *dh, int6
         rc = ZERO_ESPACE;
     if (rc)
         return rc;
-    const Cut cut = cut_of(rows, cols);
+    const Cut cut = cut_of(rows, cols, so != nullptr);
     const Gate g{gate, gate_kind, gate_type};
     if (rows > 0) {
         SplitParams p{};
