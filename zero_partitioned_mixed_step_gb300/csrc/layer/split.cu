@@ -11,11 +11,12 @@
 //
 // Each input is read once and each output written once.  8192x4096 bf16 from 8-bit
 // checkpoints: 65 us, 5.2 TB/s (0.77 of the copy rate), the pass over the rows 60 (issue slots 64 %
-// busy, FMA 41, DRAM 63), the columns' sums 5.  Two units of one row to a thread, and so a
-// barrier for each row, took 111, without the ring of copies 114.  Of the copy rate:
-// 32768x1024 0.76, 65536x512 0.74, 131072x256 0.75, 14563x2304 0.62 (288 of 512 threads; two CTAs
-// to an SM with 112 registers took 103 us for 80), 104857x320 0.53; above 4096 columns, where a thread has
-// two units, 4096x8192 0.44, and above 8192, where a row is read twice, 2048x16384 0.31.
+// busy, FMA 41, DRAM 63), the columns' sums 5; from kept halves 69 (0.85 of a longer floor).  Two
+// units of one row to a thread, and so a barrier for each row, took 111, without the ring of
+// copies 114.  Of the copy rate, from checkpoints: 262144x128 0.73, 65536x512 0.75, 32768x1024 and
+// 16384x2048 0.77, 14563x2304 0.62 (288 of 512 threads; 640 threads with 96 registers took 126 us for
+// 80), 14563x2309 0.58; above 4096 columns, where a thread has two units, 6553x5120 0.57, 4096x8192
+// 0.61, and above 8192, where a row is read twice, 2730x12288 0.29, 2048x16384 0.31.
 #include <type_traits>
 
 #include "norms.cuh"
@@ -396,7 +397,9 @@ __global__ void __launch_bounds__(1024) split_long_kernel(const SplitParams p)
         float2 w[4], a[4], xo[4], xh[4], d[4], e[4];
         auto read = [&](int c, int n) {
             get_vector<W>(p.w_pre, p.w_type, c, n, w);
-            post_factors<W>(p.w_post, p.w_type, p.gate, c, n, a);
+            // the short way for whole rows would hold more than 64 registers have room for (12288 columns:
+            // 196 us for 173)
+            post_factors<W == kWhole ? kWide : W>(p.w_post, p.w_type, p.gate, c, n, a);
             pairs_of(get_raw<W>(static_cast<const H *>(p.dy) + row * p.lddy + c, n), d);
             pairs_of(get_raw<W>(static_cast<const H *>(p.dh) + row * p.lddh + c, p.dh ? n : 0), e);
             K o, h;
