@@ -197,3 +197,74 @@ def test_calls_side_by_side():
         torch.cuda.synchronize()
         for g, w in zip(got, want):
             assert all(g[k] is None or torch.equal(g[k], w[k]) for k in g)
+
+
+# ----------------------------------------------------------------- checkpoints of every half
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_checkpoints_of_every_largest_value(dtype):
+    """Each finite value of the type as a block's largest, 127 smaller ones beside it: the scales are
+    zero_fp8_quantize's bit for bit, and so are the values (of bf16 below 2^117, from where on
+    either's quotients may be an fp32 unit off)."""
+    big = torch.arange(0x7F80 if dtype == BF16 else 0x7C00, device="cuda", dtype=torch.int32).to(torch.int16).view(dtype)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    part = torch.rand(big.numel(), 128, device="cuda", generator=g, dtype=torch.float64) * 2 - 1
+    u = (big.double()[:, None] * part).to(dtype)
+    u[:, 5] = -big
+    u8, want = pair(*u.shape), pair(*u.shape)
+    zs.zero_activation_fp8(u, None, "silu", u8=u8)
+    zs.zero_fp8_quantize(u, *want)
+    assert torch.equal(u8[1], want[1])
+    low = big.double() < 2.0 ** 117
+    assert torch.equal(u8[0][low].float(), want[0][low].float())
+    q, s = u8[0][~low].double(), u8[1][0][~low].double()[:, None]
+    assert ((q - u[~low].double() / s).abs() <= (u[~low].double() / s).abs() * (2.0 ** -4 + 2.0 ** -20) + 2.0 ** -10 + 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("cols", [4600, 9000])
+@pytest.mark.parametrize("over", ["x", "o"])
+def test_long_norms_in_place(cols, over):
+    o, x = normal(1, (9, cols), BF16), normal(2, (9, cols), BF16)
+    w = normal(3, (cols,), F32, 0.1, 1.0)
+    want = run_norms(o, x, w, w, None, 0.5)
+    y8, h = pair(9, cols), {"x": x, "o": o}[over]
+    zs.zero_gated_norms_fp8(o, x, w, EPS, h, w_post=w, scale=0.5, y8=y8)
+    assert torch.equal(h, want["h"]) and same(y8[0], want["y8"][0]) and torch.equal(y8[1], want["y8"][1])
+
+
+def test_forward_and_backward_in_one_graph():
+    """A block's end, forward and backward, and the activation's, captured once and replayed on new inputs."""
+    rows, cols = 300, 1000
+    w = normal(3, (cols,), F32, 0.1, 1.0)
+    o, x, u, v, dy = (normal(i, (rows, cols), BF16) for i in range(5))
+    ws = torch.empty(zs.zero_gated_norms_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    h, d_o, dx, du, dv = (torch.empty_like(o) for _ in range(5))
+    o8, h8, y8, u8, v8, a8, t8 = (*(pair(rows, cols) for _ in range(6)), pair(cols, rows))
+    ro, rh, dw = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda"), torch.empty(cols, device="cuda")
+
+    def chain():
+        zs.zero_gated_norms_fp8(o, x, w, EPS, h, w_post=w, y8=y8, o8=o8, h8=h8, rstd_post=ro, rstd_pre=rh)
+        zs.zero_activation_fp8(u, v, "silu", a8=a8, u8=u8, v8=v8)
+        zs.zero_activation_backward_fp8(dy, u8[0], v8[0], "silu", su=u8[1], sv=v8[1], du=du, dv=dv)
+        zs.zero_fp8_restore(*h8, row=rh, col=w, t8=t8)
+        zs.zero_gated_norms_backward(dy, o8[0], h8[0], w, rh, d_o, dx, ws, so=o8[1], sh=h8[1], dh=du, w_post=w,
+                                     rstd_post=ro, dw_pre=dw)
+
+    def outputs():
+        return [t.float().clone() for t in (h, d_o, dx, du, dv, dw, *y8, *a8, *t8)]
+
+    chain()
+    first = outputs()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for seed in (0, 40):
+        for i, t in enumerate((o, x, u, v, dy)):
+            t.copy_(normal(seed + i, (rows, cols), BF16))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = outputs()
+        chain()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, outputs()))
+        assert seed or all(torch.equal(a, b) for a, b in zip(got, first))
