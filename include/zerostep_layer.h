@@ -143,8 +143,7 @@ ZERO_API int zero_activation_fp8(const void *u, int64_t ldu, const void *v, int6
  *  du8t, dv8t (fp8), a8t (E4M3): the transposes' 8-bit forms, [cols, rows] with
  *    blocks along the rows of u: the operands of the weights' gradients.
  *  Without v: dv, dv8 and dv8t are NULL.
- * The scales are those of the fp32 values; on their way into a transposed form
- * the values are rounded to bf16 (relative 2^-8, beside 2^-4 and 2^-3 of the 8 bits).
+ * Every form is that of the fp32 values, which are rounded once.
  */
 ZERO_API int zero_activation_backward_fp8(const void *da, int64_t ldda, const void *u, int64_t ldu,
                                           const float *su, int64_t ldsu, const void *v, int64_t ldv,

@@ -1,0 +1,52 @@
+"""The 8-bit forms of what lies between a layer's products where their values are known exactly, and what
+is not finite in them."""
+import pytest
+import torch
+
+import zero_partitioned_mixed_step_gb300 as zs
+from layer_reference import check_form, value
+from test_gpu_layer import BF16, E4M3, E5M2, F16, gen, pair, strided
+
+pytestmark = pytest.mark.gpu
+
+
+def whole(seed, shape, low, high):
+    return torch.randint(low, high + 1, shape, device="cuda", generator=gen(seed)).double()
+
+
+def exact_act(rows, cols, dtype, s8, gated, seed=0):
+    """(da, u, v, su, sv) and the 64-bit (du, dv, a).  u >= 32, where exp(-u) < 2^-25: in fp32 the sigmoid
+    is 1, silu's and gelu's slopes are 1, and du = da v, dv = da u, a = u v are products of numbers of
+    at most 6 bits, which fp32 holds and 8 bits of fraction do not."""
+    da = (whole(seed + 1, (rows, cols), -63, 63) / 64).to(dtype)
+    if s8:  # 4 bits each, and a power of two for each block
+        u, v = (whole(seed + 2, (rows, cols), 8, 15) * 4).to(E4M3), whole(seed + 3, (rows, cols), -15, 15).to(E4M3)
+        u, v = (strided(q, 16 - cols % 16, 5.0) for q in (u, v))
+        su, sv = (2.0 ** whole(seed + i, ((cols + 127) // 128, rows), 0, 2).float() for i in (4, 5))
+    else:
+        u, v = whole(seed + 2, (rows, cols), 32, 63).to(dtype), (whole(seed + 3, (rows, cols), -63, 63) / 8).to(dtype)
+        su = sv = None
+    if not gated:
+        v = sv = None
+    u64, v64 = value(u, su), torch.ones_like(da, dtype=torch.float64) if v is None else value(v, sv)
+    return (da, u, v, su, sv), (da.double() * v64, da.double() * u64, u64 * v64)
+
+
+SHAPES = [(1, 1), (7, 131), (128, 128), (130, 255), (300, 264), (260, 1000)]
+
+
+@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("s8", [True, False])
+@pytest.mark.parametrize("gated", [True, False])
+def test_transposed_gradients_are_rounded_once(rows, cols, s8, gated):
+    """Off by half a step of the 8 bits and the quotient's units, and by nothing else."""
+    i = SHAPES.index((rows, cols))
+    dtype, f8, act = (BF16, F16)[i % 2], (E4M3, E5M2)[(i + s8) % 2], ("silu", "gelu")[(i + gated) % 2]
+    (da, u, v, su, sv), (du, dv, a) = exact_act(rows, cols, dtype, s8, gated)
+    out = dict(du8t=pair(cols, rows, f8), a8t=pair(cols, rows))
+    if gated:
+        out["dv8t"] = pair(cols, rows, f8)
+    zs.zero_activation_backward_fp8(da, u, v, act, su=su, sv=sv, **out)
+    for name, x in (("du8t", du), ("dv8t", dv), ("a8t", a)):
+        if name in out:
+            check_form(*out[name], x.t(), torch.zeros_like(x).t())

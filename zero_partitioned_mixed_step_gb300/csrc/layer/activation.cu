@@ -6,11 +6,10 @@
 //
 // Forward 8192x14336 bf16, gated, three 8-bit forms: 153 us, 5.4 TB/s (0.80 of the copy
 // rate; issue slots 66 % busy, ALU 51, DRAM 65).  Backward from checkpoints, du and dv
-// in 8 bits along the row and along the tokens, a along the tokens: 262 us, 4.1 TB/s (0.61; issue
-// 56 %, ALU 46, DRAM 50, 16 warps to an SM).  390 instructions for 8 elements of five 8-bit
-// forms, most of them conversions, leave the bytes behind; the registers (126) and the staged
-// tile (98 KB) allow no third CTA.  CTAs that walk the tiles with the next one's rows on their
-// way took 297.
+// in 8 bits along the row and along the tokens, a along the tokens: 298 us, 3.6 TB/s (0.54), 16 warps
+// to an SM by registers (128).  The transposed forms' values are computed twice, once for their
+// scales; most of the other instructions are conversions.  CTAs that walk the tiles with the next
+// one's rows on their way were slower.
 #include <initializer_list>
 #include <type_traits>
 
@@ -170,68 +169,88 @@ struct ActBackParams {
 
 constexpr int kBackThreads = 256;  // 16 groups of 16 lanes, 8 rows to a group
 
-// bf16 values of the 128x128 tile on their way to the transposed forms: a row's 128
-// values are 16 units of 8; unit j of a row of group g (rows 8g ..) lies at j ^ (g % 8), so that
-// 8 lanes that read one unit of 8 groups, and 8 that write a row's, meet different banks.
-struct Staged {
-    uint4 row[kBlock][16];
+// du, dv and a of two elements (dv without v: 0).
+struct Slopes {
+    float2 du, dv, a;
 };
-__device__ __forceinline__ void stage8(Staged &t, int group, int i, int j, const float2 x[4])
+template <bool GATED, bool GELU>
+__device__ __forceinline__ Slopes slopes_of(float2 da, float2 u, float2 v)
 {
-    t.row[group * 8 + i][j ^ (group & 7)] = make_uint4(word_of<bf16>(x[0].x, x[0].y), word_of<bf16>(x[1].x, x[1].y),
-                                                       word_of<bf16>(x[2].x, x[2].y), word_of<bf16>(x[3].x, x[3].y));
+    float2 dz;
+    const float2 sig = sigmoid_of<GELU>(u, dz), act = mul2(u, sig);
+    const float2 rest = fma2(sig, both(-1.0f), both(1.0f));
+    const float2 slope = fma2(act, GELU ? mul2(rest, dz) : rest, sig);
+    if (GATED)
+        return {mul2(mul2(da, v), slope), mul2(da, act), mul2(act, v)};
+    return {mul2(da, slope), both(0.0f), act};
 }
 
-// Eight columns (from 8k on) of a tile, 8 rows to each of 16 lanes, into a transposed
-// form.  amax: of the tile's columns, of the fp32 values.
-template <int W, bool E5M2>
-__device__ __forceinline__ void put_columns(const Form &f, const Staged &t, const uint32_t *amax, int k, int64_t c0,
-                                            int cols, int64_t r0, int rows)
+// The inputs of a 128x128 tile as they came.  The transposed forms' scales are known only when the whole
+// tile is, so its columns are computed again from these, by the same operations and so to the same
+// bits: held as values, three forms take 98 KB as bf16, which is a rounding that turns over one in a hundred
+// of their bytes, and 197 KB as fp32.  A row's 128 elements are 16 units of 8.  Unit j of a row of
+// group g (rows 8g ..) lies at j ^ g; units of halves at j ^ (g % 8), with their two parts of 4
+// elements exchanged from group 8 on.  So 16 lanes that read one part of 16 groups, and those
+// that write a row's units, meet different banks.
+template <class H, bool S8>
+struct Staged {
+    using Unit = std::conditional_t<S8, uint2, uint4>;
+    uint4 da[kBlock][16];
+    Unit u[kBlock][16], v[kBlock][16];  // v: not there without a gate
+    static constexpr int bytes(bool gated) { return (int)(sizeof(Staged) - (gated ? 0 : sizeof(Unit) * kBlock * 16)); }
+};
+__device__ __forceinline__ void stage8(uint4 (&t)[kBlock][16], int group, int i, int j, const uint32_t (&w)[4])
 {
-    const int lane = threadIdx.x & 15;
-    uint4 w[8];
+    t[group * 8 + i][j ^ (group & 7)] = group & 8 ? make_uint4(w[2], w[3], w[0], w[1]) : make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void stage8(uint2 (&t)[kBlock][16], int group, int i, int j, const uint32_t (&w)[2])
+{
+    t[group * 8 + i][j ^ group] = make_uint2(w[0], w[1]);
+}
+// Columns 8k + 4half .. + 3 of 8 rows: row i's 4 elements.
+__device__ __forceinline__ void staged4(const uint4 (&t)[kBlock][16], int lane, int k, int half, uint2 (&w)[8])
+{
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        w[i] = t.row[lane * 8 + i][k ^ (lane & 7)];
-    const float s = scale_of<E5M2>(amax[8 * k + (lane & 7)]);  // each lane forms one of the eight scales
-    const float inv = quick_inverse(s);
-    const int64_t c = c0 + 8 * k;
-    if (lane < 8 && c + lane < cols)
-        f.s[r0 / kBlock * f.lds + c + lane] = s;
-    const int64_t row = r0 + lane * 8;
-    const int n = row < rows ? left_of(rows, (int)row) : 0;
-    uint8_t *to = f.q + c * f.ld + row;
+        w[i] = reinterpret_cast<const uint2 *>(&t[lane * 8 + i][k ^ (lane & 7)])[half ^ (lane >> 3)];
+}
+__device__ __forceinline__ void staged4(const uint2 (&t)[kBlock][16], int lane, int k, int half, uint32_t (&w)[8])
+{
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float d = __shfl_sync(0xFFFFFFFFu, inv, j, 16);
-        float2 x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint4 &a = w[2 * i], &b = w[2 * i + 1];
-            const uint32_t p = j < 2 ? a.x : j < 4 ? a.y : j < 6 ? a.z : a.w, q = j < 2 ? b.x : j < 4 ? b.y : j < 6 ? b.z : b.w;
-            x[i] = j & 1 ? make_float2(__uint_as_float(p & 0xFFFF0000u), __uint_as_float(q & 0xFFFF0000u))
-                         : make_float2(__uint_as_float(p << 16), __uint_as_float(q << 16));
-        }
-        if (n > 0 && c + j < cols)
-            put_bytes<W>(to, n, bytes_of<E5M2>(x, d));
-        to += f.ld;
-    }
+    for (int i = 0; i < 8; ++i)
+        w[i] = reinterpret_cast<const uint32_t *>(&t[lane * 8 + i][k ^ lane])[half];
+}
+// Element m of two rows' 4.
+template <class H>
+__device__ __forceinline__ float2 down(uint2 a, uint2 b, int m)
+{
+    return pair_of<H>(__byte_perm(m & 2 ? a.y : a.x, m & 2 ? b.y : b.x, m & 1 ? 0x7632 : 0x5410));
+}
+template <class H>
+__device__ __forceinline__ float2 down(uint32_t a, uint32_t b, int m)
+{
+    return two_of<ZERO_T_E4M3>(__byte_perm(a, b, m | (m + 4) << 4) & 0xFFFFu);
 }
 
-// A CTA takes a 128x128 tile: rows first, two at a time with the next two on their way
-// (gradients, their 8-bit forms along the row, the columns' largest magnitudes), then, if a
-// transposed form is wanted, columns.
+// What a tile's columns need of its rows.
+struct TileNumbers {
+    uint32_t amax[3][kBlock];  // of the columns of du, a and dv
+    float2 inverse[3][kBlock];
+    float2 scale[2][kBlock / 2];  // of u's and v's rows, two at a time
+};
+
+// A 128x128 tile: rows first, two at a time with the next two on their way (gradients, their
+// 8-bit forms along the row, the columns' largest magnitudes), then, if a transposed form is wanted,
+// columns.
 template <class H, bool S8, bool GATED, bool GELU, int W>
-__global__ void __launch_bounds__(kBackThreads, 2) act_backward_kernel(const ActBackParams p)
+__device__ __forceinline__ void act_backward_tile(const ActBackParams &p, const TileAt at, Staged<H, S8> &tile, TileNumbers &numbers)
 {
     using K = Kept<H, S8>;
     constexpr int kElem = K::kBytes / 8, kForms = GATED ? 3 : 2, kMaxima = GATED ? 4 : 2;
-    extern __shared__ __align__(16) unsigned char dynamic[];
-    Staged *tile = reinterpret_cast<Staged *>(dynamic);  // du, a and dv
-    __shared__ uint32_t amax[kForms][kBlock];
+    auto &amax = numbers.amax;
+    auto &inverse = numbers.inverse;
     const bool trans = p.du8t.q || p.dv8t.q || p.a8t.q;
     const int j = threadIdx.x & 15, group = threadIdx.x >> 4;
-    const TileAt at = tile_at(p.tiles);
     const int64_t tc = at.c, r0 = (int64_t)at.r * kBlock, c0 = tc * kBlock, first = r0 + group * 8;
     const int c = at.c * kBlock + j * 8, nc = left_of(p.cols, c);
     if (trans) {
@@ -295,33 +314,30 @@ __global__ void __launch_bounds__(kBackThreads, 2) act_backward_kernel(const Act
             }
         }
         const int n[2] = {step < left ? nc : 0, step + 1 < left ? nc : 0};
+        if (trans)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                stage8(tile.da, group, step + i, j, da[i].w);
+                stage8(tile.u, group, step + i, j, u[i].r.w);
+                if (GATED)
+                    stage8(tile.v, group, step + i, j, v[i].r.w);
+                if (S8 && j == 0) {
+                    reinterpret_cast<float *>(numbers.scale[0])[group * 8 + step + i] = su[i];
+                    reinterpret_cast<float *>(numbers.scale[1])[group * 8 + step + i] = sv[i];
+                }
+            }
         if (step < 6)
             fetch(step + 2);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                float2 dz;
-                const float2 sig = sigmoid_of<GELU>(uf[i][k], dz), act = mul2(uf[i][k], sig);
-                const float2 rest = fma2(sig, both(-1.0f), both(1.0f));
-                const float2 slope = fma2(act, GELU ? mul2(rest, dz) : rest, sig);
-                if (GATED) {
-                    du[i][k] = mul2(mul2(g[i][k], vf[i][k]), slope);
-                    dv[i][k] = mul2(g[i][k], act);
-                    a[i][k] = mul2(act, vf[i][k]);
-                } else {
-                    du[i][k] = mul2(g[i][k], slope);
-                    a[i][k] = act;
-                }
+                const Slopes d = slopes_of<GATED, GELU>(g[i][k], uf[i][k], vf[i][k]);
+                du[i][k] = d.du;
+                dv[i][k] = d.dv;
+                a[i][k] = d.a;
             }
         if (trans) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                stage8(tile[0], group, step + i, j, du[i]);
-                stage8(tile[1], group, step + i, j, a[i]);
-                if (GATED)
-                    stage8(tile[2], group, step + i, j, dv[i]);
-            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 most[0][2 * k] = max3(most[0][2 * k], du[0][k].x, du[1][k].x);
@@ -381,27 +397,104 @@ __global__ void __launch_bounds__(kBackThreads, 2) act_backward_kernel(const Act
         for (int k = 0; k < 8; ++k)
             atomicMax(&amax[f][j * 8 + k], __float_as_uint(most[f][k]));  // a maximum: in any order the same
     __syncthreads();
-    auto put = [&](auto e5m2) {
+    // A group takes 8 columns from `group * 8` on, 8 rows to a lane; it forms their scales first.
+    const int k0 = group * 8;
+    for (int i = j; i < kForms * 8; i += 16) {
+        const int f = i >> 3, at_k = k0 + (i & 7);
+        const Form &to = f == 0 ? p.du8t : f == 1 ? p.a8t : p.dv8t;
+        const float s = (f == 1 ? Range(false) : range).scale(amax[f][at_k]);
+        const float inv = quick_inverse(s);
+        inverse[f][at_k] = make_float2(inv, 0.0f);
+        if (to.q && c0 + at_k < p.cols)
+            to.s[r0 / kBlock * to.lds + c0 + at_k] = s;
+    }
+    __syncwarp();
+    const int64_t row = r0 + j * 8;
+    const int nr = row < p.rows ? left_of(p.rows, (int)row) : 0;
+    float2 fu[4], fv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (S8) {
+            fu[i] = numbers.scale[0][j * 4 + i];
+            fv[i] = numbers.scale[1][j * 4 + i];
+        }
+    auto columns = [&](auto e5m2) {
         constexpr bool E = decltype(e5m2)::value;
-        if (p.du8t.q)
-            put_columns<W, E>(p.du8t, tile[0], amax[0], group, c0, p.cols, r0, p.rows);
-        if (GATED && p.dv8t.q)
-            put_columns<W, E>(p.dv8t, tile[kForms - 1], amax[kForms - 1], group, c0, p.cols, r0, p.rows);
+        using Part = std::conditional_t<S8, uint32_t, uint2>;
+        const int64_t first_k = c0 + k0;
+        uint8_t *to_du = p.du8t.q + first_k * p.du8t.ld + row, *to_a = p.a8t.q + first_k * p.a8t.ld + row;
+        uint8_t *to_dv = p.dv8t.q + first_k * p.dv8t.ld + row;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+            uint2 wd[8];
+            Part wu[8], wv[8];
+            staged4(tile.da, j, group, half, wd);
+            staged4(tile.u, j, group, half, wu);
+            if (GATED)
+                staged4(tile.v, j, group, half, wv);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                float2 du[4], dv[4], a[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float2 x = down<H>(wu[2 * i], wu[2 * i + 1], m), y = both(0.0f);
+                    if (GATED)
+                        y = down<H>(wv[2 * i], wv[2 * i + 1], m);
+                    if (S8) {
+                        x = mul2(x, fu[i]);
+                        if (GATED)
+                            y = mul2(y, fv[i]);
+                    }
+                    const Slopes d = slopes_of<GATED, GELU>(down<H>(wd[2 * i], wd[2 * i + 1], m), x, y);
+                    du[i] = d.du;
+                    dv[i] = d.dv;
+                    a[i] = d.a;
+                }
+                const int at_k = k0 + half * 4 + m;
+                if (nr > 0 && c0 + at_k < p.cols) {
+                    if (p.du8t.q)
+                        put_bytes<W>(to_du, nr, bytes_of<E>(du, inverse[0][at_k].x));
+                    if (p.a8t.q)
+                        put_bytes<W>(to_a, nr, bytes_of<false>(a, inverse[1][at_k].x));
+                    if (GATED && p.dv8t.q)
+                        put_bytes<W>(to_dv, nr, bytes_of<E>(dv, inverse[kForms - 1][at_k].x));
+                }
+                to_du += p.du8t.ld;
+                to_a += p.a8t.ld;
+                to_dv += p.dv8t.ld;
+            }
+        }
     };
-    if (p.a8t.q)
-        put_columns<W, false>(p.a8t, tile[1], amax[1], group, c0, p.cols, r0, p.rows);
     if (p.e5m2)
-        put(std::true_type{});
+        columns(std::true_type{});
     else
-        put(std::false_type{});
+        columns(std::false_type{});
 }
 
-template <class H, bool S8, bool GATED, bool GELU, int W>
+// Whether a short unit of 8 has to be reckoned with is asked of each tile, as only those at the ends
+// have one: 8191x14336 takes what 8192x14336 does, and a third more where the call decides.
+template <class H, bool S8, bool GATED, bool GELU, bool WIDE>
+__global__ void __launch_bounds__(kBackThreads, 2) act_backward_kernel(const ActBackParams p)
+{
+    extern __shared__ __align__(16) unsigned char dynamic[];
+    Staged<H, S8> &tile = *reinterpret_cast<Staged<H, S8> *>(dynamic);
+    __shared__ TileNumbers numbers;
+    const TileAt at = tile_at(p.tiles);
+    const bool whole = (p.cols % 8 == 0 || at.c < p.cols / kBlock) && (p.rows % 8 == 0 || at.r < p.rows / kBlock);
+    if constexpr (!WIDE)
+        act_backward_tile<H, S8, GATED, GELU, kApart>(p, at, tile, numbers);
+    else if (whole)
+        act_backward_tile<H, S8, GATED, GELU, kWhole>(p, at, tile, numbers);
+    else
+        act_backward_tile<H, S8, GATED, GELU, kWide>(p, at, tile, numbers);
+}
+
+template <class H, bool S8, bool GATED, bool GELU, bool WIDE>
 static int launch_act_backward(const ActBackParams &p, int64_t grid, cudaStream_t stream)
 {
     const bool trans = p.du8t.q || p.dv8t.q || p.a8t.q;
-    const int bytes = trans ? (GATED ? 3 : 2) * (int)sizeof(Staged) : 0;
-    auto kernel = act_backward_kernel<H, S8, GATED, GELU, W>;
+    const int bytes = trans ? Staged<H, S8>::bytes(GATED) : 0;
+    auto kernel = act_backward_kernel<H, S8, GATED, GELU, WIDE>;
     if (bytes) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess)
@@ -411,14 +504,14 @@ static int launch_act_backward(const ActBackParams &p, int64_t grid, cudaStream_
     return launch_status();
 }
 
-template <class H, bool S8, int W>
+template <class H, bool S8, bool WIDE>
 static int choose_act_backward(const ActBackParams &p, bool gelu, int64_t grid, cudaStream_t stream)
 {
     if (p.v)
-        return gelu ? launch_act_backward<H, S8, true, true, W>(p, grid, stream)
-                    : launch_act_backward<H, S8, true, false, W>(p, grid, stream);
-    return gelu ? launch_act_backward<H, S8, false, true, W>(p, grid, stream)
-                : launch_act_backward<H, S8, false, false, W>(p, grid, stream);
+        return gelu ? launch_act_backward<H, S8, true, true, WIDE>(p, grid, stream)
+                    : launch_act_backward<H, S8, true, false, WIDE>(p, grid, stream);
+    return gelu ? launch_act_backward<H, S8, false, true, WIDE>(p, grid, stream)
+                : launch_act_backward<H, S8, false, false, WIDE>(p, grid, stream);
 }
 
 }  // namespace zo
@@ -554,9 +647,8 @@ int zero_activation_backward_fp8(const void *da, int64_t ldda, const void *u, in
     auto go = [&](auto half, auto kept) {
         using H = decltype(half);
         constexpr bool S8 = decltype(kept)::value;
-        return !wide ? choose_act_backward<H, S8, kApart>(p, gelu, grid, stream)
-                     : cols % 8 || rows % 8 ? choose_act_backward<H, S8, kWide>(p, gelu, grid, stream)
-                                            : choose_act_backward<H, S8, kWhole>(p, gelu, grid, stream);
+        return wide ? choose_act_backward<H, S8, true>(p, gelu, grid, stream)
+                    : choose_act_backward<H, S8, false>(p, gelu, grid, stream);
     };
     if (type == ZERO_T_F16)
         return su ? go(f16{}, std::true_type{}) : go(f16{}, std::false_type{});
