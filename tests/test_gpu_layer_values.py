@@ -10,6 +10,15 @@ from test_gpu_layer import BF16, E4M3, E5M2, F16, gen, pair, strided
 pytestmark = pytest.mark.gpu
 
 
+def as_bytes(q):
+    return q.contiguous().view(torch.uint8)
+
+
+def same_form(a, b):
+    """The same bytes and scales, those of NaN too."""
+    return torch.equal(as_bytes(a[0]), as_bytes(b[0])) and torch.equal(a[1].view(torch.int32), b[1].view(torch.int32))
+
+
 def whole(seed, shape, low, high):
     return torch.randint(low, high + 1, shape, device="cuda", generator=gen(seed)).double()
 
@@ -50,3 +59,22 @@ def test_transposed_gradients_are_rounded_once(rows, cols, s8, gated):
     for name, x in (("du8t", du), ("dv8t", dv), ("a8t", a)):
         if name in out:
             check_form(*out[name], x.t(), torch.zeros_like(x).t())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("cols", [100, 128, 300, 1000, 5000, 16400])
+def test_checkpoints_of_what_is_not_finite(cols, dtype):
+    """o8, u8 and v8 are zero_fp8_quantize's form, byte for byte, in blocks that hold an infinity or a NaN."""
+    rows = 9
+    x = (torch.randn(rows, cols, device="cuda", generator=gen(1)) * 3).to(dtype)
+    x[1, 3], x[2, cols - 1], x[3, cols // 2] = float("inf"), float("-inf"), float("nan")
+    x[4, 0], x[4, cols - 1], x[5] = float("inf"), float("nan"), float("inf")
+    x[6, ::2], x[6, 1::2] = -0.0, float("inf")
+    want, o8, u8, v8 = (pair(rows, cols) for _ in range(4))
+    zs.zero_fp8_quantize(x, *want)
+    w = torch.ones(cols, device="cuda")
+    zs.zero_gated_norms_fp8(x, torch.zeros_like(x), w, 1e-5, torch.empty_like(x), o8=o8)
+    zs.zero_activation_fp8(x, x, "silu", u8=u8, v8=v8)
+    alone = pair(rows, cols)
+    zs.zero_activation_fp8(x, None, "gelu", u8=alone)
+    assert all(same_form(got, want) for got in (o8, u8, v8, alone))

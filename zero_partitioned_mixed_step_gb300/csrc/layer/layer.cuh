@@ -303,12 +303,13 @@ __device__ __forceinline__ float quick_inverse(float s)
 }
 // In two parts, the first below 1 / s by up to 2^-21 of it: x * hi + x * lo rounds as x / s does,
 // which values of few bits need (their quotients are often the middle of two 8-bit
-// values), and as lo is positive -0 stays.
+// values), and as lo is not negative -0 stays.  An infinite block has hi = lo = 0: its numbers
+// become 0, its infinities NaN.
 __device__ __forceinline__ Inverse inverse_of(float quick, float s)
 {
     Inverse r;
     r.hi = quick * (1.0f - 0x1p-22f);
-    r.lo = fmaf(-s, r.hi, 1.0f) * r.hi;
+    r.lo = s == __int_as_float(0x7F800000) ? 0.0f : fmaf(-s, r.hi, 1.0f) * r.hi;
     return r;
 }
 
