@@ -78,3 +78,54 @@ def test_checkpoints_of_what_is_not_finite(cols, dtype):
     alone = pair(rows, cols)
     zs.zero_activation_fp8(x, None, "gelu", u8=alone)
     assert all(same_form(got, want) for got in (o8, u8, v8, alone))
+
+
+def quantized(x64, dtype):
+    """zero_fp8_quantize's form of values that fp32 holds, and its transpose's."""
+    (rows, cols), x = x64.shape, x64.float().contiguous()
+    assert (x.double() == x64).all()
+    q, t = pair(rows, cols, dtype), pair(cols, rows, dtype)
+    zs.zero_fp8_quantize(x, *q, *t)
+    return q, t
+
+
+@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("s8", [True, False])
+@pytest.mark.parametrize("gated", [True, False])
+def test_forms_of_computed_values_are_the_quotients(rows, cols, s8, gated):
+    """What is computed in fp32 is divided as zero_fp8_quantize divides it: the same bytes, also where a quotient is
+    the middle of two 8-bit values, which numbers of few bits often have."""
+    i = SHAPES.index((rows, cols))
+    dtype, f8, act = (F16, BF16)[i % 2], (E5M2, E4M3)[(i + s8) % 2], ("gelu", "silu")[(i + gated) % 2]
+    args, values = exact_act(rows, cols, dtype, s8, gated, 10)
+    da, u, v, su, sv = args
+    out = dict(du8=pair(rows, cols, f8), du8t=pair(cols, rows, f8), a8t=pair(cols, rows))
+    if gated:
+        out.update(dv8=pair(rows, cols, f8), dv8t=pair(cols, rows, f8))
+    zs.zero_activation_backward_fp8(da, u, v, act, su=su, sv=sv, **out)
+    for name, x in zip(("du", "dv", "a"), values):
+        along, across = quantized(x, E4M3 if name == "a" else f8)
+        for got, want in ((name + "8", along), (name + "8t", across)):
+            assert got not in out or same_form(out[got], want), got
+    if not s8:
+        a8 = pair(rows, cols, f8)
+        zs.zero_activation_fp8(u, v, act, a8=a8)
+        assert same_form(a8, quantized(values[2], f8)[0])
+
+
+@pytest.mark.parametrize("f8", [E4M3, E5M2])
+@pytest.mark.parametrize("cols", [64, 256, 1024, 2048, 4096, 8192, 16384, 32768])
+def test_norms_forms_of_computed_values_are_the_quotients(cols, f8):
+    """Whole numbers make h exact.  A row whose elements are all +-2^k has a mean square of 4^k, exact as cols is a
+    power of two, and so with eps = 0 y = +-w."""
+    rows = 24
+    o, x = whole(1, (rows, cols), -31, 31).to(BF16), whole(2, (rows, cols), -31, 31).to(BF16)
+    w = (whole(3, (cols,), 1, 63) * whole(4, (cols,), 1, 63)).float()
+    h8, y8, h = pair(rows, cols), pair(rows, cols, f8), torch.empty_like(o)
+    gate = 2.0 ** whole(5, (rows, 1), -2, 2).float()
+    zs.zero_gated_norms_fp8(o, x, w, 0.0, h, gate=gate, scale=0.5, h8=h8)
+    assert same_form(h8, quantized(0.5 * x.double() + gate.double() * o.double(), E4M3)[0])
+    sign = whole(6, (rows, cols), 0, 1) * 2 - 1
+    x = (sign * 2.0 ** whole(7, (rows, 1), -3, 3)).to(BF16)
+    zs.zero_gated_norms_fp8(torch.zeros_like(x), x, w, 0.0, h, y8=y8)
+    assert same_form(y8, quantized(sign * w.double(), f8)[0])

@@ -4,9 +4,9 @@
 //   silu: z = u;  gelu's tanh form: z = 2 sqrt(2 / pi) (u + 0.044715 u^3)
 //   du = da v (sig + u sig (1 - sig) z'),  dv = da u sig
 //
-// Forward 8192x14336 bf16, gated, three 8-bit forms: 153 us, 5.4 TB/s (0.80 of the copy
+// Forward 8192x14336 bf16, gated, three 8-bit forms: 155 us, 5.4 TB/s (0.79 of the copy
 // rate; issue slots 66 % busy, ALU 51, DRAM 65).  Backward from checkpoints, du and dv
-// in 8 bits along the row and along the tokens, a along the tokens: 298 us, 3.6 TB/s (0.54), 16 warps
+// in 8 bits along the row and along the tokens, a along the tokens: 304 us, 3.6 TB/s (0.52), 16 warps
 // to an SM by registers (128).  The transposed forms' values are computed twice, once for their
 // scales; most of the other instructions are conversions.  CTAs that walk the tiles with the next
 // one's rows on their way were slower.
@@ -99,22 +99,22 @@ __global__ void __launch_bounds__(256, 3) act_kernel(const ActParams p)
         if (p.v && (p.u8.q || p.v8.q)) {
             uint32_t most[4] = {amax8(u[0]), amax8(u[1]), amax8(v[0]), amax8(v[1])};
             const float s = scale_of<false>(max_shared(most));
-            const Inverse inv = inverse_of(quick_inverse(s), s);
+            const Inverse inv = inverse_of(s);
             const int mine = shared_index<4>();
             put_scale(mine < 2 ? p.u8 : p.v8, mine, 4, s);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const Inverse d = {shared_value<4>(inv.hi, k), shared_value<4>(inv.lo, k)};
+                const Inverse d = shared_value<4>(inv, k);
                 put_kept(k < 2 ? p.u8 : p.v8, k < 2 ? u[k & 1] : v[k & 1], k & 1, d);
             }
         } else if (p.u8.q) {
             uint32_t most[2] = {amax8(u[0]), amax8(u[1])};
             const float s = scale_of<false>(max_shared(most));
-            const Inverse inv = inverse_of(quick_inverse(s), s);
+            const Inverse inv = inverse_of(s);
             put_scale(p.u8, shared_index<2>(), 8, s);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-                put_kept(p.u8, u[k], k, {shared_value<2>(inv.hi, k), shared_value<2>(inv.lo, k)});
+                put_kept(p.u8, u[k], k, shared_value<2>(inv, k));
         }
         float2 a[2][4];
 #pragma unroll
@@ -138,11 +138,12 @@ __global__ void __launch_bounds__(256, 3) act_kernel(const ActParams p)
         auto put_a8 = [&](auto e5m2) {
             constexpr bool E = decltype(e5m2)::value;
             uint32_t most[2] = {amax8(a[0]), amax8(a[1])};
-            const float s = scale_of<E>(max_shared(most)), inv = quick_inverse(s);
+            const float s = scale_of<E>(max_shared(most));
+            const Inverse inv = inverse_of(s);
             put_scale(p.a8, shared_index<2>(), 8, s);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float d = shared_value<2>(inv, k);
+                const Inverse d = shared_value<2>(inv, k);
                 if (n[k] > 0)
                     put_bytes<W>(p.a8.q + (row + k) * p.a8.ld + c, n[k], bytes_of<E>(a[k], d));
             }
@@ -189,9 +190,9 @@ __device__ __forceinline__ Slopes slopes_of(float2 da, float2 u, float2 v)
 // tile is, so its columns are computed again from these, by the same operations and so to the same
 // bits: held as values, three forms take 98 KB as bf16, which is a rounding that turns over one in a hundred
 // of their bytes, and 197 KB as fp32.  A row's 128 elements are 16 units of 8.  Unit j of a row of
-// group g (rows 8g ..) lies at j ^ g; units of halves at j ^ (g % 8), with their two parts of 4
-// elements exchanged from group 8 on.  So 16 lanes that read one part of 16 groups, and those
-// that write a row's units, meet different banks.
+// group g (rows 8g ..) lies at j ^ g, units of halves at j ^ (g % 8).  So 16 lanes that read one
+// part of 16 groups' units, lanes from 8 on the other part of halves, and those that write a row's units meet
+// different banks.
 template <class H, bool S8>
 struct Staged {
     using Unit = std::conditional_t<S8, uint2, uint4>;
@@ -201,24 +202,24 @@ struct Staged {
 };
 __device__ __forceinline__ void stage8(uint4 (&t)[kBlock][16], int group, int i, int j, const uint32_t (&w)[4])
 {
-    t[group * 8 + i][j ^ (group & 7)] = group & 8 ? make_uint4(w[2], w[3], w[0], w[1]) : make_uint4(w[0], w[1], w[2], w[3]);
+    t[group * 8 + i][j ^ (group & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ void stage8(uint2 (&t)[kBlock][16], int group, int i, int j, const uint32_t (&w)[2])
 {
     t[group * 8 + i][j ^ group] = make_uint2(w[0], w[1]);
 }
-// Columns 8k + 4half .. + 3 of 8 rows: row i's 4 elements.
-__device__ __forceinline__ void staged4(const uint4 (&t)[kBlock][16], int lane, int k, int half, uint2 (&w)[8])
+// Columns 8k + 4part .. + 3 of 8 rows: row i's 4 elements.
+__device__ __forceinline__ void staged4(const uint4 (&t)[kBlock][16], int lane, int k, int part, uint2 (&w)[8])
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        w[i] = reinterpret_cast<const uint2 *>(&t[lane * 8 + i][k ^ (lane & 7)])[half ^ (lane >> 3)];
+        w[i] = reinterpret_cast<const uint2 *>(&t[lane * 8 + i][k ^ (lane & 7)])[part];
 }
-__device__ __forceinline__ void staged4(const uint2 (&t)[kBlock][16], int lane, int k, int half, uint32_t (&w)[8])
+__device__ __forceinline__ void staged4(const uint2 (&t)[kBlock][16], int lane, int k, int part, uint32_t (&w)[8])
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        w[i] = reinterpret_cast<const uint32_t *>(&t[lane * 8 + i][k ^ lane])[half];
+        w[i] = reinterpret_cast<const uint32_t *>(&t[lane * 8 + i][k ^ lane])[part];
 }
 // Element m of two rows' 4.
 template <class H>
@@ -235,7 +236,7 @@ __device__ __forceinline__ float2 down(uint32_t a, uint32_t b, int m)
 // What a tile's columns need of its rows.
 struct TileNumbers {
     uint32_t amax[3][kBlock];  // of the columns of du, a and dv
-    float2 inverse[3][kBlock];
+    Inverse inverse[3][kBlock];
     float2 scale[2][kBlock / 2];  // of u's and v's rows, two at a time
 };
 
@@ -367,14 +368,15 @@ __device__ __forceinline__ void act_backward_tile(const ActBackParams &p, const 
                 if (GATED)
                     m[kMaxima - 2 + i] = amax8(dv[i]);
             }
-            const float s = range.scale(max_shared(m)), inv = quick_inverse(s);
+            const float s = range.scale(max_shared(m));
+            const Inverse inv = inverse_of(s);
             if (writes && step + (mine & 1) < left)
                 to_s[step] = s;
             auto put = [&](auto e5m2) {
                 constexpr bool E = decltype(e5m2)::value;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float d0 = shared_value<kMaxima>(inv, i), d1 = shared_value<kMaxima>(inv, kMaxima - 2 + i);
+                    const Inverse d0 = shared_value<kMaxima>(inv, i), d1 = shared_value<kMaxima>(inv, kMaxima - 2 + i);
                     if (p.du8.q && n[i] > 0)
                         put_bytes<W>(to_du8 + i * p.du8.ld, n[i], bytes_of<E>(du[i], d0));
                     if (GATED && p.dv8.q && n[i] > 0)
@@ -398,14 +400,13 @@ __device__ __forceinline__ void act_backward_tile(const ActBackParams &p, const 
             atomicMax(&amax[f][j * 8 + k], __float_as_uint(most[f][k]));  // a maximum: in any order the same
     __syncthreads();
     // A group takes 8 columns from `group * 8` on, 8 rows to a lane; it forms their scales first.
-    const int k0 = group * 8;
+    const int k0 = group * 8, wide_k = p.cols - (int)c0;
     for (int i = j; i < kForms * 8; i += 16) {
         const int f = i >> 3, at_k = k0 + (i & 7);
         const Form &to = f == 0 ? p.du8t : f == 1 ? p.a8t : p.dv8t;
         const float s = (f == 1 ? Range(false) : range).scale(amax[f][at_k]);
-        const float inv = quick_inverse(s);
-        inverse[f][at_k] = make_float2(inv, 0.0f);
-        if (to.q && c0 + at_k < p.cols)
+        inverse[f][at_k] = inverse_of(s);
+        if (to.q && at_k < wide_k)
             to.s[r0 / kBlock * to.lds + c0 + at_k] = s;
     }
     __syncwarp();
@@ -421,17 +422,17 @@ __device__ __forceinline__ void act_backward_tile(const ActBackParams &p, const 
     auto columns = [&](auto e5m2) {
         constexpr bool E = decltype(e5m2)::value;
         using Part = std::conditional_t<S8, uint32_t, uint2>;
-        const int64_t first_k = c0 + k0;
-        uint8_t *to_du = p.du8t.q + first_k * p.du8t.ld + row, *to_a = p.a8t.q + first_k * p.a8t.ld + row;
-        uint8_t *to_dv = p.dv8t.q + first_k * p.dv8t.ld + row;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
+            const int part = half ^ (j >> 3), first_k = k0 + part * 4;
+            uint8_t *to_du = p.du8t.q + (c0 + first_k) * p.du8t.ld + row, *to_a = p.a8t.q + (c0 + first_k) * p.a8t.ld + row;
+            uint8_t *to_dv = p.dv8t.q + (c0 + first_k) * p.dv8t.ld + row;
             uint2 wd[8];
             Part wu[8], wv[8];
-            staged4(tile.da, j, group, half, wd);
-            staged4(tile.u, j, group, half, wu);
+            staged4(tile.da, j, group, part, wd);
+            staged4(tile.u, j, group, part, wu);
             if (GATED)
-                staged4(tile.v, j, group, half, wv);
+                staged4(tile.v, j, group, part, wv);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 float2 du[4], dv[4], a[4];
@@ -450,14 +451,14 @@ __device__ __forceinline__ void act_backward_tile(const ActBackParams &p, const 
                     dv[i] = d.dv;
                     a[i] = d.a;
                 }
-                const int at_k = k0 + half * 4 + m;
-                if (nr > 0 && c0 + at_k < p.cols) {
+                const int at_k = first_k + m;
+                if (nr > 0 && at_k < wide_k) {
                     if (p.du8t.q)
-                        put_bytes<W>(to_du, nr, bytes_of<E>(du, inverse[0][at_k].x));
+                        put_bytes<W>(to_du, nr, bytes_of<E>(du, inverse[0][at_k]));
                     if (p.a8t.q)
-                        put_bytes<W>(to_a, nr, bytes_of<false>(a, inverse[1][at_k].x));
+                        put_bytes<W>(to_a, nr, bytes_of<false>(a, inverse[1][at_k]));
                     if (GATED && p.dv8t.q)
-                        put_bytes<W>(to_dv, nr, bytes_of<E>(dv, inverse[kForms - 1][at_k].x));
+                        put_bytes<W>(to_dv, nr, bytes_of<E>(dv, inverse[kForms - 1][at_k]));
                 }
                 to_du += p.du8t.ld;
                 to_a += p.a8t.ld;

@@ -7,8 +7,8 @@
 //
 // Each input is read once and each output written once, but three 8-bit forms make it as
 // much a matter of instructions as of bytes: fp32 values go in pairs, maxima are shared out
-// between lanes and each scale is formed once.  8192x4096 bf16, three forms: 62 us, 4.9 TB/s
-// (0.73 of the copy rate; issue slots 60 % busy, ALU 47, DRAM 52).  One row to a CTA of 256
+// between lanes and each scale is formed once.  8192x4096 bf16, three forms: 66 us, 4.6 TB/s
+// (0.69 of the copy rate; issue slots 59 % busy, ALU 45, DRAM 49).  One row to a CTA of 256
 // threads, two units to a thread, without the ring of copies and with the factors read for
 // every row took 70; the values one by one and a division for each scale 94.  16384x768 31 us
 // (0.66).  Of the copy rate: 65536x512 0.75, 32768x1024 0.75, 16384x2048 0.73, 14563x2304 0.68,
@@ -85,7 +85,8 @@ __device__ __forceinline__ void put_two(const Form &f, const Form &g, int64_t ro
     const uint32_t most = max_shared(a);
     const int mine = shared_index<2 * V>(), unit = mine % V;
     const bool second = mine >= V;
-    const float s = Range(second && e5m2).scale(most), inv = quick_inverse(s);
+    const float s = Range(second && e5m2).scale(most);
+    const Inverse inv = inverse_of(s);
     const Form &w = second ? g : f;
     const int at = c + unit * step;  // a column of this lane's block; its first decides
     if (threadIdx.x % (16 / (2 * V)) == 0 && w.q && (at & ~(kBlock - 1)) < cols)
@@ -93,7 +94,7 @@ __device__ __forceinline__ void put_two(const Form &f, const Form &g, int64_t ro
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int at_v = c + v * step, n = left_of(cols, at_v);
-        const float i0 = shared_value<2 * V>(inv, v), i1 = shared_value<2 * V>(inv, V + v);
+        const Inverse i0 = shared_value<2 * V>(inv, v), i1 = shared_value<2 * V>(inv, V + v);
         if (f.q && n > 0)
             put_bytes<W>(f.q + row * f.ld + at_v, n, bytes_of<false>(x[v], i0));
         if (g.q && n > 0)
@@ -110,15 +111,15 @@ __device__ __forceinline__ void put_halves(const Form &f, int64_t row, int c, in
     for (int v = 0; v < V; ++v)
         a[v] = amax8(r[v]);
     const uint32_t most = max_shared(a);
-    const float s = scale_of<false>(most), quick = quick_inverse(s);
-    const Inverse inv = inverse_of(quick, s);
+    const float s = scale_of<false>(most);
+    const Inverse inv = inverse_of(s);
     const int at = c + shared_index<V>() * step;
     if (threadIdx.x % (16 / V) == 0 && (at & ~(kBlock - 1)) < cols)
         f.s[(at / kBlock) * f.lds + row] = s;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int at_v = c + v * step, n = left_of(cols, at_v);
-        const Inverse d = {shared_value<V>(inv.hi, v), shared_value<V>(inv.lo, v)};
+        const Inverse d = shared_value<V>(inv, v);
         float2 x[4];
         pairs_of(r[v], x);
         if (n > 0)
@@ -244,12 +245,12 @@ __global__ void __launch_bounds__(MAXT, MAXT == 320 ? 2 : 512 / MAXT) join_kerne
         if (p.o8.q) {
             uint32_t most[2] = {amax8(o[0]), amax8(o[1])};
             const float s = scale_of<false>(max_shared(most));
-            const Inverse inv = inverse_of(quick_inverse(s), s);
+            const Inverse inv = inverse_of(s);
             if (to_so && k + own2 < mine)
                 to_so[k] = s;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const Inverse d = {shared_value<2>(inv.hi, r), shared_value<2>(inv.lo, r)};
+                const Inverse d = shared_value<2>(inv, r);
                 float2 v[4];
                 pairs_of(o[r], v);
                 if (m[r] > 0)
@@ -291,14 +292,15 @@ __global__ void __launch_bounds__(MAXT, MAXT == 320 ? 2 : 512 / MAXT) join_kerne
         to_y += 2 * p.ldy;
         if (p.h8.q || p.y8.q) {
             uint32_t most[4] = {amax8(h[0]), amax8(h[1]), amax8(y[0]), amax8(y[1])};
-            const float s = range.scale(max_shared(most)), inv = quick_inverse(s);
+            const float s = range.scale(max_shared(most));
+            const Inverse inv = inverse_of(s);
             if (to_s4 && k + (own4 & 1) < mine)
                 to_s4[k] = s;
             auto put = [&](auto e5m2) {
                 constexpr bool E = decltype(e5m2)::value;
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float d = shared_value<4>(inv, r), e = shared_value<4>(inv, 2 + r);
+                    const Inverse d = shared_value<4>(inv, r), e = shared_value<4>(inv, 2 + r);
                     if (p.h8.q && m[r] > 0)
                         put_bytes<W>(to_h8 + r * p.h8.ld, m[r], bytes_of<false>(h[r], d));
                     if (p.y8.q && m[r] > 0)

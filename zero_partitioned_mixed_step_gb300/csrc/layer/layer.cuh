@@ -293,24 +293,23 @@ struct Range {
     __device__ __forceinline__ float scale(uint32_t amax) const { return scale_from(amax, qmax, inv); }
 };
 
-// 1 / s to an fp32 unit.  For values that were computed in fp32 one product with it is a
-// quotient to 3 half units, next to the 2^19 of a step of the 8 bits.
-__device__ __forceinline__ float quick_inverse(float s)
+// 1 / s in two parts, the first below it by up to 2^-21 of it: x * hi + x * lo rounds as x / s does, in the
+// halves that are kept and in what is computed in fp32 alike.  Quotients are often the middle of two 8-bit
+// values, which one product with 1 / s turns over.  As lo is not negative -0 stays.  An infinite block has
+// hi = lo = 0: its numbers become 0, its infinities NaN.
+__device__ __forceinline__ Inverse inverse_of(float s)
 {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-    return r;
-}
-// In two parts, the first below 1 / s by up to 2^-21 of it: x * hi + x * lo rounds as x / s does,
-// which values of few bits need (their quotients are often the middle of two 8-bit
-// values), and as lo is not negative -0 stays.  An infinite block has hi = lo = 0: its numbers
-// become 0, its infinities NaN.
-__device__ __forceinline__ Inverse inverse_of(float quick, float s)
-{
+    float quick;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(quick) : "f"(s));
     Inverse r;
     r.hi = quick * (1.0f - 0x1p-22f);
     r.lo = s == __int_as_float(0x7F800000) ? 0.0f : fmaf(-s, r.hi, 1.0f) * r.hi;
     return r;
+}
+template <int N>
+__device__ __forceinline__ Inverse shared_value(Inverse mine, int i)
+{
+    return {shared_value<N>(mine.hi, i), shared_value<N>(mine.lo, i)};
 }
 
 // Which type is a template's argument: where it is a number that the launch shares, the
@@ -320,15 +319,6 @@ __device__ __forceinline__ uint2 bytes_of(const float2 q[4])
 {
     constexpr int F = E5M2 ? ZERO_T_E5M2 : ZERO_T_E4M3;
     return make_uint2(pack4<F>(q[0].x, q[0].y, q[1].x, q[1].y), pack4<F>(q[2].x, q[2].y, q[3].x, q[3].y));
-}
-template <bool E5M2>
-__device__ __forceinline__ uint2 bytes_of(const float2 x[4], float inv)
-{
-    float2 q[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        q[i] = mul2(x[i], both(inv));
-    return bytes_of<E5M2>(q);
 }
 template <bool E5M2>
 __device__ __forceinline__ uint2 bytes_of(const float2 x[4], Inverse d)

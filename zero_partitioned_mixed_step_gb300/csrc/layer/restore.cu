@@ -114,13 +114,13 @@ __global__ void __launch_bounds__(kRestoreThreads) restore_kernel(const RestoreP
         for (int m = 0; m < 4; ++m)
             a[m] = amax8(x[m]);
         const float s = scale_of<F8 == ZERO_T_E5M2>(max_shared(a));
-        const Inverse inv = inverse_of(quick_inverse(s), s);
+        const Inverse inv = inverse_of(s);
         const int mine = shared_index<4>();
         if (lane % 4 == 0 && at + mine < p.cols)
             p.t8.s[tr * p.t8.lds + at + mine] = s;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            const Inverse d = {shared_value<4>(inv.hi, m), shared_value<4>(inv.lo, m)};
+            const Inverse d = shared_value<4>(inv, m);
             if (n > 0 && at + m < p.cols)
                 put_bytes<W>(to, n, bytes_of<F8 == ZERO_T_E5M2>(x[m], d));
             to += p.t8.ld;
