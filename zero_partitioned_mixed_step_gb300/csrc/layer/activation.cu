@@ -495,12 +495,9 @@ static int launch_act_backward(const ActBackParams &p, int64_t grid, cudaStream_
 {
     const bool trans = p.du8t.q || p.dv8t.q || p.a8t.q;
     const int bytes = trans ? Staged<H, S8>::bytes(GATED) : 0;
-    auto kernel = act_backward_kernel<H, S8, GATED, GELU, WIDE>;
-    if (bytes) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess)
-            return cuda_error(e);
-    }
+    constexpr auto kernel = act_backward_kernel<H, S8, GATED, GELU, WIDE>;
+    if (const int rc = allow_smem<kernel>(Staged<H, S8>::bytes(GATED)))
+        return rc;
     kernel<<<(unsigned)grid, kBackThreads, bytes, stream>>>(p);
     return launch_status();
 }

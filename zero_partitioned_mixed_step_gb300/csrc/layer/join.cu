@@ -423,28 +423,27 @@ static int launch_join(const JoinParams &p, cudaStream_t stream)
         kernel<<<(unsigned)p.rows, threads, 0, stream>>>(p);
         return launch_status();
     };
-    auto ring = [&](auto kernel, int threads, int groups, int stages) {
+    // `most_threads`: of any launch of the kernel
+    auto ring = [&](auto kernel, int most_threads, int threads, int groups, int stages) {
         const size_t bytes = W != kApart ? (size_t)stages * threads * 64 : 0;
-        if (bytes > 32 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-            if (e != cudaSuccess)
-                return cuda_error(e);
-        }
+        if (W != kApart)
+            if (const int rc = allow_smem<kernel.value>(stages * most_threads * 64))
+                return rc;
         const int64_t most = 152 * ((threads > 256 && threads <= 320 ? 640 : 512) / threads), turns = ceil_div(p.rows, 2 * groups);
-        kernel<<<(unsigned)(turns < most ? turns : most), threads, bytes, stream>>>(p);
+        kernel.value<<<(unsigned)(turns < most ? turns : most), threads, bytes, stream>>>(p);
         return launch_status();
     };
     constexpr int kDepth = 4;
     if (p.cols <= 128)
-        return ring(join_kernel<H, 16, 256, kDepth, W>, 256, 16, kDepth);
+        return ring(Kernel<join_kernel<H, 16, 256, kDepth, W>>{}, 256, 256, 16, kDepth);
     if (p.cols <= 256)
-        return ring(join_kernel<H, 32, 256, kDepth, W>, 256, 8, kDepth);
+        return ring(Kernel<join_kernel<H, 32, 256, kDepth, W>>{}, 256, 256, 8, kDepth);
     if (p.cols <= 2048)
-        return ring(join_kernel<H, 0, 256, kDepth, W>, threads(1), 1, kDepth);
+        return ring(Kernel<join_kernel<H, 0, 256, kDepth, W>>{}, 256, threads(1), 1, kDepth);
     if (p.cols <= 2560)  // two CTAs to an SM where registers are 96 (8192x4096 elements in 14563 rows: 66 us, 87 with one)
-        return ring(join_kernel<H, 0, 320, kDepth, W>, threads(1), 1, kDepth);
+        return ring(Kernel<join_kernel<H, 0, 320, kDepth, W>>{}, 320, threads(1), 1, kDepth);
     if (p.cols <= 4096)
-        return ring(join_kernel<H, 0, 512, kDepth, W>, threads(1), 1, kDepth);
+        return ring(Kernel<join_kernel<H, 0, 512, kDepth, W>>{}, 512, threads(1), 1, kDepth);
     if (p.cols <= 8192)
         return go(join_wide_kernel<H, 2, 512, W>, threads(2));
     if (p.cols <= 16384)

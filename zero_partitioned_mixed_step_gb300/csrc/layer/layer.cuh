@@ -2,6 +2,8 @@
 // and read them, sums over a row's threads, and the checks of their arguments.
 #pragma once
 
+#include <atomic>
+
 #include "../ops/ops.cuh"
 #include "zerostep_layer.h"
 
@@ -42,6 +44,28 @@ inline int check_kept(const void *x, int64_t ld, const float *s, int64_t lds, in
 {
     const int rc = check_matrix(x, rows, cols, ld, s ? 1 : type_bytes(type));
     return rc || !s ? rc : check_matrix(s, ceil_div(cols, kBlock), rows, lds, 4);
+}
+
+// A kernel as a value that a launch's lambda can hand on as a template's argument.
+template <auto KERNEL>
+struct Kernel {
+    static constexpr auto value = KERNEL;
+};
+// Lets a kernel take that much dynamic shared memory, once for each device: the most that any launch of it
+// takes, not the call's own amount, as the limit is the process's, and another thread's may come between
+// a call's limit and its launch.
+template <auto KERNEL>
+inline int allow_smem(int bytes)
+{
+    static std::atomic<uint64_t> ready{0};  // bits of devices
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && !(dev < 64 && (ready.load(std::memory_order_acquire) >> dev & 1))) {
+        e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess && dev < 64)
+            ready.fetch_or(UINT64_C(1) << dev, std::memory_order_acq_rel);
+    }
+    return e == cudaSuccess ? ZERO_OK : cuda_error(e);
 }
 
 // A matrix in tiles of 128 columns: CTAs take one row of tiles after the other, so that those

@@ -564,29 +564,28 @@ static Cut cut_of(int64_t rows, int64_t cols, bool s8)
 template <class H, bool S8, int W>
 static int launch_split(const SplitParams &p, const Cut &cut, cudaStream_t stream)
 {
-    auto go = [&](auto kernel, int units, int stages) {
+    // `most_threads`: of any launch of the kernel
+    auto go = [&](auto kernel, int most_threads, int units, int stages) {
         const size_t bytes = W != kApart ? (size_t)stages * units * cut.threads * (S8 ? 48 : 64) : 0;
-        if (bytes > 32 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-            if (e != cudaSuccess)
-                return cuda_error(e);
-        }
-        kernel<<<(unsigned)cut.ctas, cut.threads, bytes, stream>>>(p);
+        if (W != kApart)
+            if (const int rc = allow_smem<kernel.value>(stages * units * most_threads * (S8 ? 48 : 64)))
+                return rc;
+        kernel.value<<<(unsigned)cut.ctas, cut.threads, bytes, stream>>>(p);
         return launch_status();
     };
     if (p.cols <= 128)
-        return go(split_kernel<H, S8, 1, 1, 16, kSmallThreads, 4, W>, 1, 4);
+        return go(Kernel<split_kernel<H, S8, 1, 1, 16, kSmallThreads, 4, W>>{}, kSmallThreads, 1, 4);
     if (p.cols <= 256)
-        return go(split_kernel<H, S8, 1, 1, 32, kSmallThreads, 4, W>, 1, 4);
+        return go(Kernel<split_kernel<H, S8, 1, 1, 32, kSmallThreads, 4, W>>{}, kSmallThreads, 1, 4);
     if constexpr (!S8)
         if (p.cols <= 2560)  // 96 registers (32768x1024 fp16 70 us, with 128 77; from checkpoints they spill)
-            return go(split_kernel<H, S8, 1, 2, 0, 320, 2, W>, 2, 2);
+            return go(Kernel<split_kernel<H, S8, 1, 2, 0, 320, 2, W>>{}, 320, 2, 2);
     if (p.cols <= 2048)
-        return go(split_kernel<H, S8, 1, 2, 0, 256, 3, W>, 2, 3);
+        return go(Kernel<split_kernel<H, S8, 1, 2, 0, 256, 3, W>>{}, 256, 2, 3);
     if (p.cols <= 4096)
-        return go(split_kernel<H, S8, 1, 2, 0, 512, 3, W>, 2, 3);
+        return go(Kernel<split_kernel<H, S8, 1, 2, 0, 512, 3, W>>{}, 512, 2, 3);
     if (p.cols <= 8192)
-        return go(split_kernel<H, S8, 2, 1, 0, 512, 3, W>, 2, 3);
+        return go(Kernel<split_kernel<H, S8, 2, 1, 0, 512, 3, W>>{}, 512, 2, 3);
     split_long_kernel<H, S8, W><<<(unsigned)cut.ctas, 1024, 0, stream>>>(p);
     return launch_status();
 }
