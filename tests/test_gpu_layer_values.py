@@ -129,3 +129,27 @@ def test_norms_forms_of_computed_values_are_the_quotients(cols, f8):
     x = (sign * 2.0 ** whole(7, (rows, 1), -3, 3)).to(BF16)
     zs.zero_gated_norms_fp8(torch.zeros_like(x), x, w, 0.0, h, y8=y8)
     assert same_form(y8, quantized(sign * w.double(), f8)[0])
+
+
+def test_what_a_gate_is_does_not_hang_on_the_rows():
+    """Micro-batches of which one has a single row: the gradient of one number is gathered over all of them; a
+    token's is written."""
+    cols, w = 300, torch.ones(300, device="cuda")
+    gate, total, each = torch.full((1,), 0.5, device="cuda"), torch.zeros(1, device="cuda"), []
+    for rows in (3, 1, 2):
+        o, h, dy = (torch.randn(rows, cols, device="cuda", generator=gen(rows + i)).to(BF16) for i in (10, 20, 30))
+        ws = torch.empty(zs.zero_gated_norms_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+        args = (dy, o, h, w, torch.ones(rows, device="cuda"), torch.empty_like(o), torch.empty_like(o), ws)
+        zs.zero_gated_norms_backward(*args, gate=gate, dgate=total, add=True)
+        each.append(torch.zeros(1, device="cuda"))
+        zs.zero_gated_norms_backward(*args, gate=gate, dgate=each[-1])
+        token = torch.full((rows, 1), 7.0, device="cuda")
+        zs.zero_gated_norms_backward(*args, gate=gate.expand(rows, 1).contiguous(), dgate=token, add=True)
+        written = torch.zeros(rows, 1, device="cuda")
+        zs.zero_gated_norms_backward(*args, gate=gate.expand(rows, 1).contiguous(), dgate=written)
+        assert torch.equal(token, written)
+        if rows > 1:
+            with pytest.raises(ValueError):
+                zs.zero_gated_norms_backward(*args, gate=gate.view(1, 1), dgate=total.view(1, 1), add=True)
+    assert torch.equal(total, each[0] + each[1] + each[2])
+    assert zs.layer._gate_kind(gate.view(1, 1), 1, cols) == zs.layer.GATE_ROWS

@@ -64,15 +64,18 @@ def _vector(t: Optional[torch.Tensor], n: int, name: str, dev: int, dtype=None) 
 
 
 def _gate_kind(gate: Optional[torch.Tensor], rows: int, cols: int) -> int:
+    """By the gate's own dimensions, so that a number's meaning (and whether its gradient is added) does not
+    hang on how many rows a call has: two dimensions are a token's, whatever their sizes."""
     if gate is None:
         return GATE_NONE
-    if gate.shape == (rows, 1):
-        return GATE_ROWS
-    if gate.numel() == 1:
+    if gate.dim() == 2:
+        if gate.shape == (rows, 1):
+            return GATE_ROWS
+    elif gate.numel() == 1:
         return GATE_ONE
-    if gate.shape == (cols,):
+    elif gate.shape == (cols,):
         return GATE_COLS
-    raise ValueError(f"gate: shape {tuple(gate.shape)}, expected one element, {(cols,)} or {(rows, 1)}")
+    raise ValueError(f"gate: shape {tuple(gate.shape)}, expected () or (1,), {(cols,)} or {(rows, 1)}")
 
 
 def _norm_weights(w_pre, w_post, cols, dev):
@@ -92,7 +95,7 @@ def zero_gated_norms_fp8(o: torch.Tensor, x: torch.Tensor, w_pre: torch.Tensor, 
                          stream=None) -> None:
     """h = scale * x + gate * norm(o) with w_post (or gate * o without), y = norm(h) with
     w_pre, in o's type and, in 8 bits, into y8; checkpoints of o and h into o8 and
-    h8.  gate: one element, [cols] or [rows, 1]."""
+    h8.  gate: one number as [] or [1], [cols], or [rows, 1], a number a token."""
     if o.dim() != 2:
         raise ValueError("o: matrix expected")
     (rows, cols), dev = o.shape, _current()
@@ -138,7 +141,8 @@ def zero_gated_norms_backward(dy: torch.Tensor, o: torch.Tensor, h: torch.Tensor
                               dgate: Optional[torch.Tensor] = None, add: bool = False, stream=None) -> None:
     """The gradients of zero_gated_norms_fp8 from dy and the gradient dh that reaches h
     along the stream: d_o, dx (the stream's), dw_pre, dw_post, dgate.  o, h: what was
-    kept, both halves, or both E4M3 with the scales so and sh."""
+    kept, both halves, or both E4M3 with the scales so and sh.  add: dw_pre, dw_post and the dgate of
+    one number or of channels are added to what is there; a token's dgate is written."""
     if dy.dim() != 2:
         raise ValueError("dy: matrix expected")
     (rows, cols), dev = dy.shape, _current()
