@@ -153,3 +153,71 @@ def test_what_a_gate_is_does_not_hang_on_the_rows():
                 zs.zero_gated_norms_backward(*args, gate=gate.view(1, 1), dgate=total.view(1, 1), add=True)
     assert torch.equal(total, each[0] + each[1] + each[2])
     assert zs.layer._gate_kind(gate.view(1, 1), 1, cols) == zs.layer.GATE_ROWS
+
+
+@pytest.mark.parametrize("f8", [E4M3, E5M2])
+def test_restored_blocks_that_are_infinite(f8):
+    """A transposed block with an infinite scale has zeros for its numbers, as zero_fp8_quantize's has."""
+    q = whole(1, (200, 130), -15, 15).to(f8)
+    s = torch.ones(2, 200, device="cuda")
+    col = torch.ones(130, device="cuda")
+    col[5], col[129] = float("inf"), float("inf")
+    q[:, [5, 129]] = torch.ones(200, 2, device="cuda").to(f8)
+    got, want, x = pair(130, 200, f8), pair(130, 200, f8), torch.empty(200, 130, device="cuda")
+    zs.zero_fp8_restore(q, s, col=col, x=x, t8=got)
+    zs.zero_fp8_quantize(x.t().contiguous(), *want)
+    assert x[:, 5].isinf().all() and same_form(got, want)
+
+
+# widths that fill the lanes of every kernel, and widths that leave some of them, or a part of a unit, empty
+FILLED = [1, 100, 128, 250, 256, 1000, 1001, 1024, 2300, 2304, 2560, 4000, 4096, 4100, 8192, 9000, 16384, 16390, 16392, 20000]
+
+
+@pytest.mark.parametrize("cols", FILLED)
+@pytest.mark.parametrize("kind", ["one", "rows"])
+def test_an_infinite_gate_at_every_width(cols, kind):
+    """h is infinite, so its squares' sum is and rstd_pre = 0, and so is each block's scale."""
+    rows, inf = 5, float("inf")
+    for pad in (0, 8 - cols % 8):
+        o = strided((torch.randint(0, 2, (rows, cols), device="cuda", generator=gen(1)) * 2 - 1).to(BF16), pad, float("nan"))
+        x = strided(torch.ones(rows, cols, device="cuda", dtype=BF16), pad, float("nan"))
+        gate = torch.full((rows, 1) if kind == "rows" else (1,), inf, device="cuda")
+        hit = torch.ones(rows, dtype=torch.bool, device="cuda")
+        if kind == "rows":
+            gate[2:] = 0.5
+            hit[2:] = False
+        h, h8, y8, rstd = torch.empty_like(o), pair(rows, cols), pair(rows, cols), torch.full((rows,), 7.0, device="cuda")
+        w = torch.ones(cols, device="cuda")
+        for w_post in (None, w):
+            zs.zero_gated_norms_fp8(o, x, w, 1e-5, h, w_post=w_post, gate=gate, y8=y8, h8=h8, rstd_pre=rstd)
+            assert (rstd[hit] == 0).all() and h[hit].isinf().all() and (h8[1][:, hit] == inf).all()
+            assert y8[1][:, hit].isnan().all()  # infinity times 0
+            assert rstd[~hit].isfinite().all() and (rstd[~hit] > 0).all() and h8[1][:, ~hit].isfinite().all()
+
+
+@pytest.mark.parametrize("cols", FILLED)
+def test_rows_whose_squares_vanish_at_every_width(cols):
+    """eps = 0 and squares below fp32's smallest: rstd is infinite, and so is each element of y and each scale."""
+    x = strided(torch.full((3, cols), 2.0 ** -100, device="cuda", dtype=BF16), 8 - cols % 8, float("nan"))
+    y8, rstd = pair(3, cols), torch.empty(3, device="cuda")
+    zs.zero_gated_norms_fp8(torch.zeros_like(x), x, torch.ones(cols, device="cuda"), 0.0, torch.empty_like(x), y8=y8, rstd_pre=rstd)
+    assert rstd.isinf().all() and (y8[1] == float("inf")).all()
+
+
+@pytest.mark.parametrize("cols", [1, 7, 100, 128, 131, 250, 1000, 1003])
+@pytest.mark.parametrize("pad", [0, 16])
+def test_gradients_of_an_infinite_block_at_every_width(cols, pad):
+    """v's last block is infinite: du8's scale of it is too, and dv8 is as without it."""
+    rows, kb = 133, (cols + 127) // 128
+    da, u, v = (torch.full((rows, cols), c, device="cuda") for c in (0.5, 40.0, -2.0))
+    u, v = (strided(t.to(E4M3), pad + 16 - cols % 16 if pad else 0, 5.0) for t in (u, v))
+    su, sv = torch.ones(kb, rows, device="cuda"), torch.ones(kb, rows, device="cuda")
+    sv[-1, ::2] = float("inf")
+    out = dict(du8=pair(rows, cols), dv8=pair(rows, cols), du8t=pair(cols, rows), dv8t=pair(cols, rows), a8t=pair(cols, rows))
+    zs.zero_activation_backward_fp8(da.to(BF16), u, v, "silu", su=su, sv=sv, **out)
+    assert (out["du8"][1][-1, ::2] == float("inf")).all() and out["du8"][1][:, 1::2].isfinite().all()
+    assert out["du8"][1][:-1].isfinite().all() and (out["dv8"][1] == 20.0 / torch.tensor(448.0)).all()
+    last = (cols - 1) // 128 * 128
+    for k in ("du8t", "a8t"):
+        assert (out[k][1][:, last:] == float("inf")).all() and out[k][1][:, :last].isfinite().all()
+    assert same_form(out["dv8t"], quantized(torch.full((cols, rows), 20.0, device="cuda", dtype=torch.float64), E4M3)[0])

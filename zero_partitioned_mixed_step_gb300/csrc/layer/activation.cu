@@ -300,6 +300,7 @@ __device__ __forceinline__ void act_backward_tile(const ActBackParams &p, const 
 #pragma unroll 1
     for (int step = 0; step < 8; step += 2) {
         float2 g[2][4], uf[2][4], vf[2][4], du[2][4], dv[2][4], a[2][4];
+        const int n[2] = {step < left ? nc : 0, step + 1 < left ? nc : 0};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             pairs_of(da[i], g[i]);
@@ -313,8 +314,12 @@ __device__ __forceinline__ void act_backward_tile(const ActBackParams &p, const 
                 if (S8 && GATED)
                     vf[i][k] = mul2(vf[i][k], both(sv[i]));
             }
+            if (S8) {
+                end_unit<W>(uf[i], n[i], su[i]);
+                if (GATED)
+                    end_unit<W>(vf[i], n[i], sv[i]);
+            }
         }
-        const int n[2] = {step < left ? nc : 0, step + 1 < left ? nc : 0};
         if (trans)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -472,44 +477,42 @@ __device__ __forceinline__ void act_backward_tile(const ActBackParams &p, const 
         columns(std::false_type{});
 }
 
-// Whether a short unit of 8 has to be reckoned with is asked of each tile, as only those at the ends
-// have one: 8191x14336 takes what 8192x14336 does, and a third more where the call decides.
-template <class H, bool S8, bool GATED, bool GELU, bool WIDE>
+// Where 8 does not divide the rows or the columns, each tile is asked whether it has a short unit to reckon
+// with, as only those at the ends do: 8191x14336 takes about what 8192x14336 does, and a third more where
+// the call decides.
+template <class H, bool S8, bool GATED, bool GELU, int W>
 __global__ void __launch_bounds__(kBackThreads, 2) act_backward_kernel(const ActBackParams p)
 {
     extern __shared__ __align__(16) unsigned char dynamic[];
     Staged<H, S8> &tile = *reinterpret_cast<Staged<H, S8> *>(dynamic);
     __shared__ TileNumbers numbers;
     const TileAt at = tile_at(p.tiles);
-    const bool whole = (p.cols % 8 == 0 || at.c < p.cols / kBlock) && (p.rows % 8 == 0 || at.r < p.rows / kBlock);
-    if constexpr (!WIDE)
-        act_backward_tile<H, S8, GATED, GELU, kApart>(p, at, tile, numbers);
-    else if (whole)
+    if (W == kWide && whole_units(at, p.rows, p.cols))
         act_backward_tile<H, S8, GATED, GELU, kWhole>(p, at, tile, numbers);
     else
-        act_backward_tile<H, S8, GATED, GELU, kWide>(p, at, tile, numbers);
+        act_backward_tile<H, S8, GATED, GELU, W>(p, at, tile, numbers);
 }
 
-template <class H, bool S8, bool GATED, bool GELU, bool WIDE>
+template <class H, bool S8, bool GATED, bool GELU, int W>
 static int launch_act_backward(const ActBackParams &p, int64_t grid, cudaStream_t stream)
 {
     const bool trans = p.du8t.q || p.dv8t.q || p.a8t.q;
     const int bytes = trans ? Staged<H, S8>::bytes(GATED) : 0;
-    constexpr auto kernel = act_backward_kernel<H, S8, GATED, GELU, WIDE>;
+    constexpr auto kernel = act_backward_kernel<H, S8, GATED, GELU, W>;
     if (const int rc = allow_smem<kernel>(Staged<H, S8>::bytes(GATED)))
         return rc;
     kernel<<<(unsigned)grid, kBackThreads, bytes, stream>>>(p);
     return launch_status();
 }
 
-template <class H, bool S8, bool WIDE>
+template <class H, bool S8, int W>
 static int choose_act_backward(const ActBackParams &p, bool gelu, int64_t grid, cudaStream_t stream)
 {
     if (p.v)
-        return gelu ? launch_act_backward<H, S8, true, true, WIDE>(p, grid, stream)
-                    : launch_act_backward<H, S8, true, false, WIDE>(p, grid, stream);
-    return gelu ? launch_act_backward<H, S8, false, true, WIDE>(p, grid, stream)
-                : launch_act_backward<H, S8, false, false, WIDE>(p, grid, stream);
+        return gelu ? launch_act_backward<H, S8, true, true, W>(p, grid, stream)
+                    : launch_act_backward<H, S8, true, false, W>(p, grid, stream);
+    return gelu ? launch_act_backward<H, S8, false, true, W>(p, grid, stream)
+                : launch_act_backward<H, S8, false, false, W>(p, grid, stream);
 }
 
 }  // namespace zo
@@ -645,8 +648,9 @@ int zero_activation_backward_fp8(const void *da, int64_t ldda, const void *u, in
     auto go = [&](auto half, auto kept) {
         using H = decltype(half);
         constexpr bool S8 = decltype(kept)::value;
-        return wide ? choose_act_backward<H, S8, true>(p, gelu, grid, stream)
-                    : choose_act_backward<H, S8, false>(p, gelu, grid, stream);
+        return !wide ? choose_act_backward<H, S8, kApart>(p, gelu, grid, stream)
+                     : cols % 8 || rows % 8 ? choose_act_backward<H, S8, kWide>(p, gelu, grid, stream)
+                                            : choose_act_backward<H, S8, kWhole>(p, gelu, grid, stream);
     };
     if (type == ZERO_T_F16)
         return su ? go(f16{}, std::true_type{}) : go(f16{}, std::false_type{});

@@ -56,11 +56,10 @@ __device__ __forceinline__ float square_sum(const Raw8<H> &r)
     return s.x + s.y;
 }
 
-// Behind a row's end o, x, w_post and w_pre are zeros, and so are h and y, but for a row whose by or
-// rh is not finite: there they are NaN, and so is the row's own sum or what is made of it.
+// Behind a row's end o, x, w_post and w_pre are zeros, and so are h and y.
 // h of 8 columns (`by`: the row's gate times ro).
 template <int W, class H>
-__device__ __forceinline__ void join8(const JoinParams &p, int c, int n, const Raw8<H> &o, const Raw8<H> &x, float by, float2 h[4])
+__device__ __forceinline__ void join8(const JoinParams &p, int c, int n, const Raw8<H> &o, const Raw8<H> &x, float by, float2 (&h)[4])
 {
     float2 f[4], xo[4], xs[4];
     post_factors<W>(p.w_post, p.w_type, p.gate, c, n, f);
@@ -68,7 +67,8 @@ __device__ __forceinline__ void join8(const JoinParams &p, int c, int n, const R
     pairs_of(x, xs);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        h[i] = fma2(both(p.scale), xs[i], mul2(f[i], mul2(xo[i], both(by))));
+        h[i] = fma2(both(p.scale), xs[i], mul2(f[i], mul2(xo[i], both(in_row_only(by, n)))));
+    end_unit<W>(h, n, by);
 }
 
 // V units of a row, `step` columns apart, into two forms of fp32 values (either may be absent).
@@ -141,7 +141,8 @@ __device__ __forceinline__ void put_units(const JoinParams &p, int64_t row, int 
         get_vector<W>(p.w_pre, p.w_type, at, n, y[v]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            y[v][i] = mul2(mul2(h[v][i], both(rh)), y[v][i]);
+            y[v][i] = mul2(mul2(h[v][i], both(in_row_only(rh, n))), y[v][i]);
+        end_unit<W>(y[v], n, rh);
         if (p.y && n > 0)
             put_pairs<W>(static_cast<H *>(p.y) + row * p.ldy + at, n, y[v]);
     }
@@ -267,7 +268,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 320 ? 2 : 512 / MAXT) join_kerne
             pairs_of(x[r], xs);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                h[r][i] = fma2(both(p.scale), xs[i], mul2(a[i], mul2(xo[i], both(by[r]))));
+                h[r][i] = fma2(both(p.scale), xs[i], mul2(a[i], mul2(xo[i], both(in_row_only(by[r], n)))));
+            end_unit<W>(h[r], n, by[r]);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 s2 = fma2(h[r][i], h[r][i], s2);
@@ -284,7 +286,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 320 ? 2 : 512 / MAXT) join_kerne
                 put_pairs<W>(to_h + r * p.ldh, m[r], h[r]);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                y[r][i] = mul2(mul2(h[r][i], both(rh)), w[i]);
+                y[r][i] = mul2(mul2(h[r][i], both(in_row_only(rh, n))), w[i]);
+            end_unit<W>(y[r], n, rh);
             if (p.y && m[r] > 0)
                 put_pairs<W>(to_y + r * p.ldy, m[r], y[r]);
         }

@@ -81,6 +81,11 @@ __device__ __forceinline__ TileAt tile_at(const Tiles &t)
 {
     return {(int32_t)(blockIdx.x / (uint32_t)t.cols), (int32_t)(blockIdx.x % (uint32_t)t.cols)};
 }
+// Whether a 128x128 tile's units of 8, along either side, are whole or absent.
+__device__ __forceinline__ bool whole_units(const TileAt &at, int rows, int cols)
+{
+    return (cols % 8 == 0 || at.c < cols / kBlock) && (rows % 8 == 0 || at.r < rows / kBlock);
+}
 inline Tiles tiles_of(int64_t rows, int64_t cols, int height)
 {
     return {(int32_t)ceil_div(rows, height), (int32_t)ceil_div(cols, kBlock)};
@@ -214,6 +219,23 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
         : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
+}
+
+// Behind the n elements of a row's last unit are zeros, which a factor that is not finite makes NaN.  They are
+// kept out of the row's sums and its last block's scale: a unit without elements takes 0 as its factor
+// (a select, where a branch in the norms takes 2 us of 66 at 8192x4096), a short one has zeros put back.
+__device__ __forceinline__ float in_row_only(float factor, int n) { return n > 0 ? factor : 0.0f; }
+__device__ __forceinline__ void clear_behind(float2 (&x)[4], int n)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x[i] = make_float2(2 * i < n ? x[i].x : 0.0f, 2 * i + 1 < n ? x[i].y : 0.0f);
+}
+template <int W>
+__device__ __forceinline__ void end_unit(float2 (&x)[4], int n, float factor)
+{
+    if (W != kWhole && n < 8 && !(fabsf(factor) <= 3.402823466e38f))
+        clear_behind(x, n);
 }
 
 // ------------------------------------------------------------------ 8-bit blocks

@@ -29,14 +29,9 @@ struct RestoreParams {
 constexpr int kRestoreThreads = 256;
 
 template <int F8, class X, int W>
-__global__ void __launch_bounds__(kRestoreThreads) restore_kernel(const RestoreParams p)
+__device__ __forceinline__ void restore_tile(const RestoreParams &p, const TileAt tile_of, uint2 (&tile)[kBlock][16], float (&factor)[kBlock])
 {
-    // row r's 8 bytes of columns 8j .. lie at j ^ (r / 8), so that the 16 lanes of a column,
-    // 8 rows each, read different banks
-    __shared__ uint2 tile[kBlock][16];
-    __shared__ __align__(16) float factor[kBlock];
     const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
-    const TileAt tile_of = tile_at(p.tiles);
     const int64_t tr = tile_of.r, tc = tile_of.c, r0 = tr * kBlock, c0 = tc * kBlock;
     const int c = tile_of.c * kBlock + lane * 8, nc = left_of(p.cols, c);
     const int nr = r0 + group * 8 < p.rows ? left_of(p.rows, (int)(r0 + group * 8)) : 0;
@@ -109,10 +104,14 @@ __global__ void __launch_bounds__(kRestoreThreads) restore_kernel(const RestoreP
                 for (int i = 0; i < 4; ++i)
                     x[m][i] = mul2(x[m][i], both(col));
             }
+        if (W != kWhole && n < 8)  // rows behind the last: 0 times a column's factor may be NaN
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                clear_behind(x[m], n);
         uint32_t a[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m)
-            a[m] = amax8(x[m]);
+            a[m] = W != kWhole || n > 0 ? amax8(x[m]) : 0u;
         const float s = scale_of<F8 == ZERO_T_E5M2>(max_shared(a));
         const Inverse inv = inverse_of(s);
         const int mine = shared_index<4>();
@@ -126,6 +125,22 @@ __global__ void __launch_bounds__(kRestoreThreads) restore_kernel(const RestoreP
             to += p.t8.ld;
         }
     }
+}
+
+// As for the activation's gradients, only the last tiles of rows or columns that 8 does not divide have short units
+// to reckon with (8191x4096 23 us, 24 where all do).
+template <int F8, class X, int W>
+__global__ void __launch_bounds__(kRestoreThreads) restore_kernel(const RestoreParams p)
+{
+    // row r's 8 bytes of columns 8j .. lie at j ^ (r / 8), so that the 16 lanes of a column,
+    // 8 rows each, read different banks
+    __shared__ uint2 tile[kBlock][16];
+    __shared__ __align__(16) float factor[kBlock];
+    const TileAt at = tile_at(p.tiles);
+    if (W == kWide && whole_units(at, p.rows, p.cols))
+        restore_tile<F8, X, kWhole>(p, at, tile, factor);
+    else
+        restore_tile<F8, X, W>(p, at, tile, factor);
 }
 
 template <class X, int W>
