@@ -5,7 +5,7 @@ import torch
 
 import zero_partitioned_mixed_step_gb300 as zs
 from layer_reference import check_form, value
-from test_gpu_layer import BF16, E4M3, E5M2, F16, gen, pair, strided
+from test_gpu_layer import BF16, E4M3, E5M2, F16, F32, backward_inputs, gen, pair, run_backward, strided
 
 pytestmark = pytest.mark.gpu
 
@@ -221,3 +221,26 @@ def test_gradients_of_an_infinite_block_at_every_width(cols, pad):
     for k in ("du8t", "a8t"):
         assert (out[k][1][:, last:] == float("inf")).all() and out[k][1][:, :last].isfinite().all()
     assert same_form(out["dv8t"], quantized(torch.full((cols, rows), 20.0, device="cuda", dtype=torch.float64), E4M3)[0])
+
+
+@pytest.mark.parametrize("cols", [100, 200, 1000, 2300, 4000, 8000, 9000])
+@pytest.mark.parametrize("kind", ["none", "one", "cols", "rows"])
+@pytest.mark.parametrize("s8", [True, False])
+def test_gradients_without_a_norm_behind_do_not_read_o(cols, kind, s8):
+    """d_o = gate * dH there: an o that is not finite changes neither d_o nor dx, and dgate alone."""
+    a = backward_inputs(19, cols, BF16, F32, kind, False, s8)
+    want = run_backward(scale=0.5, **a)
+    a["o"][3] = float("nan")
+    if s8:
+        a["so"][0, 5], a["so"][-1, 7] = float("inf"), float("nan")
+    else:
+        a["o"][5, 0], a["o"][7, cols - 1] = float("inf"), float("-inf")
+    got = run_backward(scale=0.5, **a)
+    assert torch.equal(got["d_o"], want["d_o"]) and torch.equal(got["dx"], want["dx"])
+    assert torch.equal(got["dw_pre"], want["dw_pre"])
+    if kind == "rows":
+        bad = torch.tensor([3, 5, 7], device="cuda")
+        good = torch.ones(19, dtype=torch.bool, device="cuda").index_fill_(0, bad, False)
+        assert not got["dgate"][bad].isfinite().any() and torch.equal(got["dgate"][good], want["dgate"][good])
+    elif kind != "none":
+        assert not got["dgate"].isfinite().all()

@@ -10,7 +10,7 @@
 // (|P| and |rh m Q| are sums that dH's own terms bound: nothing is lost that dH keeps).
 //
 // Each input is read once and each output written once.  8192x4096 bf16 from 8-bit
-// checkpoints: 65 us, 5.2 TB/s (0.77 of the copy rate), the pass over the rows 60 (issue slots 64 %
+// checkpoints: 66 us, 5.1 TB/s (0.76 of the copy rate), the pass over the rows 61 (issue slots 64 %
 // busy, FMA 41, DRAM 63), the columns' sums 5; from kept halves 69 (0.85 of a longer floor).  Two
 // units of one row to a thread, and so a barrier for each row, took 111, without the ring of
 // copies 114.  Of the copy rate, from checkpoints: 262144x128 0.73, 65536x512 0.75, 32768x1024 and
@@ -284,6 +284,9 @@ __global__ void __launch_bounds__(MAXT, MAXT == 320 ? 2 : 512 / MAXT) split_kern
             if (t == 0 && live && p.dgate_rows)
                 put_one(p.dgate_rows, p.dgate_type, first + k + r, along);
             const float by = ro[r] * gate[r];
+            // Without a norm behind the block o, which may not be finite, has no part in d_o.  A select takes 1.3 us of
+            // 66 at 8192x4096 and of 83 at 4096x8192, two ways for the row the same and 7.
+            const bool post = p.w_post != nullptr;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float2 qo[4], qh[4], d[4], e[4], x[4], y[4];
@@ -298,7 +301,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 320 ? 2 : 512 / MAXT) split_kern
                     const float2 g = mul2(d[i], w[v][i]);
                     const float2 dH = fma2(both(km), qh[i], fma2(both(rh[r]), g, e[i]));
                     x[i] = mul2(both(p.scale), dH);
-                    y[i] = fma2(a[v][i], mul2(both(by), dH), mul2(both(ko), qo[i]));
+                    const float2 off = mul2(both(ko), qo[i]);
+                    y[i] = fma2(a[v][i], mul2(both(by), dH), make_float2(post ? off.x : 0.0f, post ? off.y : 0.0f));
                     da[v][i] = fma2(mul2(both(part), dH), qo[i], da[v][i]);
                 }
                 const int c = (v * T + t) * 8;
@@ -447,7 +451,9 @@ __global__ void __launch_bounds__(1024) split_long_kernel(const SplitParams p)
                 const float2 g = mul2(d[i], w[i]);
                 d[i] = fma2(both(-rh * m), xh[i], fma2(both(rh), g, e[i]));
                 x[i] = mul2(both(p.scale), d[i]);
-                y[i] = fma2(a[i], mul2(both(ro * gate), d[i]), mul2(both(-ro * mo), xo[i]));
+                y[i] = mul2(a[i], mul2(both(ro * gate), d[i]));
+                if (p.w_post)
+                    y[i] = fma2(a[i], mul2(both(ro * gate), d[i]), mul2(both(-ro * mo), xo[i]));
                 d[i] = mul2(both(share), d[i]);
             }
             if (post)
