@@ -217,25 +217,6 @@ __device__ __forceinline__ void store8(T *p, int n, bool wide, const float x[8])
     }
 }
 
-// Eight elements of a vector of any of the types, as fp32.
-__device__ __forceinline__ void load_w(const void *w, int type, int64_t at, int n, bool wide,
-                                       float x[8])
-{
-    if (type == ZERO_T_F16)
-        load8(static_cast<const f16 *>(w) + at, n, wide, x);
-    else if (type == ZERO_T_BF16)
-        load8(static_cast<const bf16 *>(w) + at, n, wide, x);
-    else
-        load8(static_cast<const float *>(w) + at, n, wide, x);
-}
-
-// How many of the 8 columns from c on a row has.
-__device__ __forceinline__ int in_row(int64_t cols, int64_t c)
-{
-    const int64_t left = cols - c;
-    return left >= 8 ? 8 : left > 0 ? (int)left : 0;
-}
-
 // Eight 8-bit values, packed, to p; `wide`: p is 8-byte aligned.
 __device__ __forceinline__ void store8b(uint8_t *p, int n, bool wide, uint2 v)
 {

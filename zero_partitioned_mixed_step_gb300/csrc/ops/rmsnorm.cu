@@ -43,6 +43,23 @@ struct NormParams {
     int32_t w_type;
 };
 
+__device__ __forceinline__ void load_w(const void *w, int type, int64_t at, int n, bool wide,
+                                       float x[8])
+{
+    if (type == ZERO_T_F16)
+        load8(static_cast<const f16 *>(w) + at, n, wide, x);
+    else if (type == ZERO_T_BF16)
+        load8(static_cast<const bf16 *>(w) + at, n, wide, x);
+    else
+        load8(static_cast<const float *>(w) + at, n, wide, x);
+}
+
+__device__ __forceinline__ int in_row(int64_t cols, int64_t c)
+{
+    const int64_t left = cols - c;
+    return left >= 8 ? 8 : left > 0 ? (int)left : 0;
+}
+
 // Eight neighbouring elements of a row to y and to the 8-bit form; the 16
 // lanes of a 1x128 block come here together.
 template <class H, int F8>
