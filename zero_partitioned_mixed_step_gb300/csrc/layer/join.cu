@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(MAXT) join_wide_kernel(const JoinParams p)
 #pragma unroll
         for (int v = 0; v < V; ++v)
             sq[0] += square_sum(o[v]);
-        row_sums<0, kWarps>(sq, slots[0]);
+        row_sums<kWarps>(sq, slots[0]);
         ro = root(sq[0], p.inv_cols, p.eps);
         if (t == 0 && p.rstd_post)
             p.rstd_post[row] = ro;
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(MAXT) join_wide_kernel(const JoinParams p)
     if (p.o8.q)
         put_halves<W>(p.o8, row, c, step, cols, o);
     float sq[1] = {s2.x + s2.y};
-    row_sums<0, kWarps>(sq, slots[1]);
+    row_sums<kWarps>(sq, slots[1]);
     const float rh = root(sq[0], p.inv_cols, p.eps);
     if (t == 0 && p.rstd_pre)
         p.rstd_pre[row] = rh;
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(1024) join_long_kernel(const JoinParams p)
         float sq[1] = {0.0f};
         for (int64_t c = threadIdx.x * 8; c < p.cols; c += 1024 * 8)
             sq[0] += square_sum(get_raw<W>(po + c, left_of(p.cols, (int)c)));
-        row_sums<0, 32>(sq, slots[0]);
+        row_sums<32>(sq, slots[0]);
         ro = root(sq[0], p.inv_cols, p.eps);
         if (threadIdx.x == 0 && p.rstd_post)
             p.rstd_post[row] = ro;
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(1024) join_long_kernel(const JoinParams p)
             s2 = fma2(h[0][i], h[0][i], s2);
     }
     float sq[1] = {s2.x + s2.y};
-    row_sums<0, 32>(sq, slots[1]);
+    row_sums<32>(sq, slots[1]);
     const float rh = root(sq[0], p.inv_cols, p.eps);
     if (threadIdx.x == 0 && p.rstd_pre)
         p.rstd_pre[row] = rh;

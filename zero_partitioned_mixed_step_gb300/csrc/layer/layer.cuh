@@ -494,18 +494,16 @@ __device__ __forceinline__ float load_one(const void *p, int type, int64_t at)
 
 // ------------------------------------------------------------------ sums over a row
 
-// N sums over the threads of a row: G = 16 or 32 lanes, or (0) the CTA's
-// blockDim.x / 32 warps, at most WARPS (a power of two).  `slot`: WARPS * N floats that
-// the CTA does not use between this call's barrier and the next one's.
-template <int G, int WARPS, int N>
+// N sums over a CTA, whose row it is: its blockDim.x / 32 warps, at most WARPS (a power of two).
+// `slot`: WARPS * N floats that the CTA does not use between this call's barrier and the next
+// one's.
+template <int WARPS, int N>
 __device__ __forceinline__ void row_sums(float (&x)[N], float *slot)
 {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        x[i] = sum_over<G ? G : 32>(x[i]);
-    if (G)
-        return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        x[i] = sum_over<32>(x[i]);
     if (lane == 0)
 #pragma unroll
         for (int i = 0; i < N; ++i)

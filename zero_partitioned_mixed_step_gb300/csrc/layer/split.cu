@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(1024) split_long_kernel(const SplitParams p)
             }
         }
         float sum[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};
-        row_sums<0, 32>(sum, slots[turn]);
+        row_sums<32>(sum, slots[turn]);
         const float m = sum[0] * p.inv_cols;
         const float along = fmaf(-rh * m, sum[2], sum[1]);
         const float mo = p.w_post ? gate * along * p.inv_cols : 0.0f;
