@@ -17,14 +17,16 @@
  * between a row's end and the next row neither read nor written, sizes 0 ..
  * 2^31 - 1025, work enqueued on `stream`, arguments validated before anything is
  * enqueued, the same return codes; calls can be captured in a CUDA graph; no
- * floating-point atomics, sums in an order that the sizes fix).  An input may not
+ * floating-point atomics, sums in an order that the sizes fix, and in
+ * zero_gated_norms_backward whether o and h are kept in 8 bits).  An input may not
  * overlap an output, nor an output another, unless the description allows it.
  * Rows that start on 16-byte boundaries (8-bit ones: 8) run with wide accesses.
  *
  * Checkpoints.  What the backward pass reads of the forward pass is an 8-bit form
  * as zero_fp8_quantize makes it, E4M3 with an fp32 scale for each 1x128 block
  * (8.25 bits an element for 16), or the tensor itself in its half type.  The
- * gradients are those of the formulas below with the values that were kept.
+ * gradients are those of the formulas below with the values that were kept.  Every
+ * 8-bit output is the form that zero_fp8_quantize gives of the fp32 values.
  */
 #ifndef ZEROSTEP_LAYER_H
 #define ZEROSTEP_LAYER_H

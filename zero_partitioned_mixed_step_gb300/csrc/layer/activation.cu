@@ -5,11 +5,11 @@
 //   du = da v (sig + u sig (1 - sig) z'),  dv = da u sig
 //
 // Forward 8192x14336 bf16, gated, three 8-bit forms: 155 us, 5.4 TB/s (0.79 of the copy
-// rate; issue slots 66 % busy, ALU 51, DRAM 65).  Backward from checkpoints, du and dv
-// in 8 bits along the row and along the tokens, a along the tokens: 304 us, 3.6 TB/s (0.52), 16 warps
-// to an SM by registers (128).  The transposed forms' values are computed twice, once for their
-// scales; most of the other instructions are conversions.  CTAs that walk the tiles with the next
-// one's rows on their way were slower.
+// rate; issue slots 73 % busy, ALU 57, DRAM 65).  Backward from checkpoints, du and dv
+// in 8 bits along the row and along the tokens, a along the tokens: 301 us, 3.6 TB/s (0.53; issue
+// 61 %, ALU 48, DRAM 43), 16 warps to an SM by registers (128).  The transposed forms' values are
+// computed twice, once for their scales; conversions and quotients are the larger part of 490
+// instructions for 8 elements.  From kept halves 320 us (0.60).
 #include <initializer_list>
 #include <type_traits>
 

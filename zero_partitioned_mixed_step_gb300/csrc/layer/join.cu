@@ -5,15 +5,13 @@
 //   h = scale * x + gate * w_post * xo
 //   y = h * rh * w_pre, rh = 1 / sqrt(mean(h^2) + eps)
 //
-// Each input is read once and each output written once, but three 8-bit forms make it as
-// much a matter of instructions as of bytes: fp32 values go in pairs, maxima are shared out
-// between lanes and each scale is formed once.  8192x4096 bf16, three forms: 66 us, 4.6 TB/s
-// (0.69 of the copy rate; issue slots 59 % busy, ALU 45, DRAM 49).  One row to a CTA of 256
-// threads, two units to a thread, without the ring of copies and with the factors read for
-// every row took 70; the values one by one and a division for each scale 94.  16384x768 31 us
-// (0.66).  Of the copy rate: 65536x512 0.75, 32768x1024 0.75, 16384x2048 0.73, 14563x2304 0.68,
-// x2309 0.62, 104857x320 0.50, and above 4096 columns 6553x5120 0.61, 4096x8192 0.59,
-// 2048x16384 0.47.
+// Each input is read once and each output written once.  Three 8-bit forms make it a matter of
+// instructions too: fp32 values go in pairs, maxima are shared out between lanes and each scale is
+// formed once.  8192x4096 bf16, three forms: 66 us, 4.6 TB/s (0.69 of the copy rate), bound by
+// waiting: 16 warps to an SM, issue slots 59 % busy, ALU 45, DRAM 49.  The first kernel, with values one
+// by one and a division for each scale, took 94.  16384x768 32 us (0.64).  Of the copy rate: 131072x256
+// 0.77, 65536x512 0.73, 32768x1024 0.71, 16384x2048 0.70, 14563x2304 0.64, x2309 0.59, 104857x320 0.48,
+// and above 4096 columns 6553x5120 0.60, 4096x8192 0.58, 2048x16384 0.46, 1024x32768 0.41.
 #include <initializer_list>
 #include <type_traits>
 
@@ -323,7 +321,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 320 ? 2 : 512 / MAXT) join_kerne
 }
 
 // Rows of more than 4096 columns: one to a CTA, V units of 8 to a thread.  Clusters of 2 to 4
-// CTAs of the kernel above, which exchange their sums, took 117 us for 76 at 4096x8192: the
+// CTAs of the kernel above, which exchange their sums, took 117 us for 77 at 4096x8192: the
 // cluster's barrier waits for the turn's stores.
 template <class H, int V, int MAXT, int W>
 __global__ void __launch_bounds__(MAXT) join_wide_kernel(const JoinParams p)
@@ -443,7 +441,8 @@ static int launch_join(const JoinParams &p, cudaStream_t stream)
         return ring(Kernel<join_kernel<H, 32, 256, kDepth, W>>{}, 256, 256, 8, kDepth);
     if (p.cols <= 2048)
         return ring(Kernel<join_kernel<H, 0, 256, kDepth, W>>{}, 256, threads(1), 1, kDepth);
-    if (p.cols <= 2560)  // two CTAs to an SM where registers are 96 (8192x4096 elements in 14563 rows: 66 us, 87 with one)
+    if (p.cols <= 2560)  // two CTAs to an SM where registers are 96 (8192x4096 elements in 14563 rows: 70 us; with one
+                       // 87 where this took 66)
         return ring(Kernel<join_kernel<H, 0, 320, kDepth, W>>{}, 320, threads(1), 1, kDepth);
     if (p.cols <= 4096)
         return ring(Kernel<join_kernel<H, 0, 512, kDepth, W>>{}, 512, threads(1), 1, kDepth);

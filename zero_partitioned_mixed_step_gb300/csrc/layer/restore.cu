@@ -7,8 +7,8 @@
 // transposed value is a byte times a row's and a column's number.
 //
 // 8192x14336 as bf16: 55 us, 6.4 TB/s (0.95 of the copy rate).  8192x4096 transposed with both
-// factors: 21 us, 3.3 TB/s (0.48; issue slots 65 % busy, ALU 57): taking bytes apart and together
-// again is what it does.  CTAs that walk the tiles with two more on their way took 23, and the
+// factors: 21 us, 3.3 TB/s (0.49; issue slots 66 % busy, ALU 59): taking bytes apart and together
+// again is what it does, and four CTAs to an SM take 2048 tiles in 3.4 waves.  CTAs that walk the tiles with two more on their way took 23, and the
 // first case 63.
 #include "layer.cuh"
 

@@ -10,13 +10,13 @@
 // (|P| and |rh m Q| are sums that dH's own terms bound: nothing is lost that dH keeps).
 //
 // Each input is read once and each output written once.  8192x4096 bf16 from 8-bit
-// checkpoints: 66 us, 5.1 TB/s (0.76 of the copy rate), the pass over the rows 61 (issue slots 64 %
-// busy, FMA 41, DRAM 63), the columns' sums 5; from kept halves 69 (0.85 of a longer floor).  Two
+// checkpoints: 66 us, 5.1 TB/s (0.76 of the copy rate), the pass over the rows 60 (issue slots 65 %
+// busy, FMA 39, DRAM 63), the columns' sums 5; from kept halves 69 (0.85 of a longer floor).  Two
 // units of one row to a thread, and so a barrier for each row, took 111, without the ring of
-// copies 114.  Of the copy rate, from checkpoints: 262144x128 0.73, 65536x512 0.75, 32768x1024 and
+// copies 114.  Of the copy rate, from checkpoints: 262144x128 0.73, 65536x512 0.75, 32768x1024 0.76,
 // 16384x2048 0.77, 14563x2304 0.62 (288 of 512 threads; 640 threads with 96 registers took 126 us for
 // 80), 14563x2309 0.58; above 4096 columns, where a thread has two units, 6553x5120 0.57, 4096x8192
-// 0.61, and above 8192, where a row is read twice, 2730x12288 0.29, 2048x16384 0.31.
+// 0.60, and above 8192, where a row is read twice, 2730x12288 0.29, 2048x16384 0.32.
 #include <type_traits>
 
 #include "norms.cuh"
@@ -539,8 +539,8 @@ __global__ void __launch_bounds__(THREADS) columns_kernel(const ColumnParams p)
     }
 }
 
-// How a backward pass is cut, a rule on the sizes alone, so that the sums' bits do not
-// depend on the GPU: threads, rows side by side in a CTA, CTAs.
+// How a backward pass is cut, a rule on the sizes and on whether o and h are kept in 8 bits, so that the
+// sums' bits do not depend on the GPU: threads, rows side by side in a CTA, CTAs.
 struct Cut {
     int threads, groups;
     int64_t ctas;
