@@ -244,3 +244,101 @@ def test_gradients_without_a_norm_behind_do_not_read_o(cols, kind, s8):
         assert not got["dgate"][bad].isfinite().any() and torch.equal(got["dgate"][good], want["dgate"][good])
     elif kind != "none":
         assert not got["dgate"].isfinite().all()
+
+
+# ----------------------------------------------------------------- calls that the description allows
+
+@pytest.mark.parametrize("rows,cols", [(1, 9), (128, 256), (131, 264), (257, 1001)])
+@pytest.mark.parametrize("s8", [True, False])
+@pytest.mark.parametrize("over", ["du", "dv"])
+def test_gradients_over_da_with_transposed_forms(rows, cols, s8, over):
+    """The columns are formed again behind the rows, which have been written over da by then."""
+    args, _ = exact_act(rows, cols, BF16, s8, True, 30)
+    da, u, v, su, sv = args
+
+    def run(halves):
+        out = dict(du8=pair(rows, cols, E5M2), dv8t=pair(cols, rows, E5M2), du8t=pair(cols, rows, E5M2), a8t=pair(cols, rows))
+        zs.zero_activation_backward_fp8(da, u, v, "gelu", su=su, sv=sv, **out, **halves)
+        return out
+
+    halves = dict(du=torch.empty_like(da), dv=torch.empty_like(da))
+    want = run(halves)
+    other = "dv" if over == "du" else "du"
+    mine = {over: da, other: torch.empty_like(da)}
+    got = run(mine)
+    assert all(same_form(got[k], want[k]) for k in want)
+    assert torch.equal(mine["du"], halves["du"]) and torch.equal(mine["dv"], halves["dv"])
+
+
+@pytest.mark.parametrize("cols", [96, 200, 1000, 2304, 4096, 8192, 8200])
+@pytest.mark.parametrize("crossed", [False, True])
+def test_norms_backward_of_halves_in_place(cols, crossed):
+    a = backward_inputs(50, cols, BF16, F32, "rows", True, False)
+    want = run_backward(scale=1.0, **a)
+    dgate = torch.empty_like(want["dgate"])
+    d_o, dx = (a["dh"], a["dy"]) if crossed else (a["dy"], a["dh"])
+    zs.zero_gated_norms_backward(a["dy"], a["o"], a["h"], a["w_pre"], a["rh"], d_o, dx, None, dh=a["dh"], w_post=a["w_post"],
+                                 rstd_post=a["ro"], gate=a["gate"], dgate=dgate)
+    assert torch.equal(d_o, want["d_o"]) and torch.equal(dx, want["dx"]) and torch.equal(dgate, want["dgate"])
+
+
+def test_sums_of_no_rows_behind_other_work_in_a_graph():
+    """The columns' kernel is launched early; here it is the call's only one, behind a fill and a copy."""
+    a = backward_inputs(0, 200, BF16, F32, "cols", True, True)
+    ws = torch.empty(zs.zero_gated_norms_workspace_bytes(0, 200), dtype=torch.uint8, device="cuda")
+    z, dw, src = torch.empty(0, 200, device="cuda", dtype=BF16), torch.empty(200, device="cuda"), torch.ones(200, device="cuda")
+    other = torch.empty(200, device="cuda")
+
+    def run():
+        dw.fill_(3.0)
+        zs.zero_gated_norms_backward(a["dy"], a["o"], a["h"], a["w_pre"], a["rh"], z, z.clone(), ws, so=a["so"], sh=a["sh"],
+                                     w_post=a["w_post"], rstd_post=a["ro"], gate=a["gate"], dw_pre=dw, add=True)
+        other.copy_(dw)
+        zs.zero_gated_norms_backward(a["dy"], a["o"], a["h"], a["w_pre"], a["rh"], z, z.clone(), ws, so=a["so"], sh=a["sh"],
+                                     w_post=a["w_post"], rstd_post=a["ro"], gate=a["gate"], dw_pre=dw)
+
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    dw.copy_(src)
+    other.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (other == 3.0).all() and (dw == 0).all()
+
+
+def test_activation_gradients_side_by_side_and_in_graphs():
+    """Four streams at once, and the same calls captured and replayed on new inputs: the transposed forms too."""
+    rows, cols = 700, 1096
+    sets = [exact_act(rows, cols, BF16, True, True, 50 + 10 * i)[0] for i in range(4)]
+    outs = [dict(du8=pair(rows, cols), dv8=pair(rows, cols), du8t=pair(cols, rows), dv8t=pair(cols, rows), a8t=pair(cols, rows)) for _ in sets]
+
+    def run(args, out):
+        da, u, v, su, sv = args
+        zs.zero_activation_backward_fp8(da, u, v, "silu", su=su, sv=sv, **out)
+
+    wants = []
+    for args, out in zip(sets, outs):
+        run(args, out)
+        wants.append({k: (q.clone(), s.clone()) for k, (q, s) in out.items()})
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        for st, args, out in zip(streams, sets, outs):
+            st.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(st):
+                run(args, out)
+        for st in streams:
+            torch.cuda.current_stream().wait_stream(st)
+        torch.cuda.synchronize()
+        assert all(same_form(out[k], want[k]) for out, want in zip(outs, wants) for k in want)
+    static = tuple(t.clone() for t in sets[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(static, outs[0])
+    for args, want in zip(sets, wants):
+        for to, t in zip(static, args):
+            to.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(same_form(outs[0][k], want[k]) for k in want)
